@@ -17,6 +17,10 @@ Functions mirror the C ABI (include/qmm.h):
 * ``quantized_matmul(x, qweight, qzeros, scales, bits, group_size, qweight_lo=None, bias=None)``:
   the functional form, M <= 16 to the GEMV, larger M to the GEMM.
 
+The operators of a decoder layer between the products (include/qmm_layer.h) are
+in ``layer`` and exported here: ``qmm_moe_route``, ``qmm_moe``, ``qmm_kv_append``,
+``qmm_attention``, ``qmm_logprobs``.
+
 Bit widths 1, 2, 3, 4 and 8. The floating-point data (x, zeros, scales, bias,
 the result) are all float16 or all bfloat16; bfloat16 calls the ``_bf16``
 entry points of the ABI.
@@ -99,6 +103,7 @@ def _declare(lib):
     lib.qmm_gemv_ex.argtypes = [P, I, I, P, P, P, P, P, I, I, I, U, P, P, SZ, P]
     lib.qmm_gemm_ex.restype = I
     lib.qmm_gemm_ex.argtypes = [P, I, I, P, P, P, P, P, I, I, I, U, P, P]
+    layer.declare(lib)
     if lib.qmm_abi_version() != ABI_VERSION:
         raise RuntimeError(f"libqmm ABI version {lib.qmm_abi_version()} does not match the binding's {ABI_VERSION}")
     return lib
@@ -422,3 +427,7 @@ def quantized_matmul(x, qweight, qzeros, scales, bits: int, group_size: int, qwe
             if e.status != 3:  # QMM_ERR_SHAPE: shape beyond the decode kernel's staging limits
                 raise
     return qmm_gemm(x, qweight, qweight_lo, qzeros, scales, bits, group_size, bias=bias)
+
+
+from . import layer  # noqa: E402  (it uses the helpers above)
+from .layer import qmm_attention, qmm_kv_append, qmm_logprobs, qmm_moe, qmm_moe_route  # noqa: E402,F401

@@ -9,6 +9,11 @@
 
 #include "../../include/qmm.h"
 #include "common.h"
+#include "status.h"
+
+namespace {
+thread_local char g_last_error[512] = "";
+}
 
 namespace qmm {
 
@@ -35,12 +40,6 @@ DeviceTopo device_topology() {
   return cache[dev];
 }
 
-}  // namespace qmm
-
-namespace {
-
-thread_local char g_last_error[512] = "";
-
 qmm_status fail(qmm_status st, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -54,10 +53,21 @@ qmm_status ok() {
   return QMM_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+qmm_status from_hip(hipError_t e, const char* what) {
+  if (e == hipSuccess) return ok();
+  return fail(QMM_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+}
 
-bool bits_ok(int bits) { return bits == 1 || bits == 2 || bits == 3 || bits == 4 || bits == 8; }
+}  // namespace qmm
+
+namespace {
+
+using qmm::aligned;
+using qmm::aligned16;
+using qmm::bits_ok;
+using qmm::fail;
+using qmm::from_hip;
+using qmm::ok;
 
 // Codes per word of the plane that sets the K granularity.
 int k_multiple(int bits) { return bits == 3 ? 32 : 32 / bits; }
@@ -132,11 +142,6 @@ qmm_status check_strips_call(const void* in, int rows, int N, const void* out) {
   if (!in || !out) return fail(QMM_ERR_NULL, "the input and output planes must not be NULL");
   if (!aligned(in, 4) || !aligned(out, 4)) return fail(QMM_ERR_ALIGN, "the planes must be 4-byte aligned");
   return QMM_OK;
-}
-
-qmm_status from_hip(hipError_t e, const char* what) {
-  if (e == hipSuccess) return ok();
-  return fail(QMM_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
 qmm_status dequant_impl(const int32_t* qweight, const int32_t* qweight_lo, const uint16_t* zeros,

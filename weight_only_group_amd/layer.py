@@ -1,0 +1,280 @@
+"""Python binding of the layer operators (include/qmm_layer.h): argument
+marshalling over libqmm, in the manner of the products' binding.
+
+* ``qmm_moe_route(x, router, top_k, renormalize=True)`` -> ``(ids, weights, logits)``
+* ``qmm_moe(x, ids, weights, gate_up, down, bits, group_size, strips=False)`` -> y
+* ``qmm_kv_append(q, k, v, cos, sin, positions, slots, k_cache, v_cache, adjacent=False)`` -> rotated q
+* ``qmm_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q, max_kv, ...)`` -> out
+* ``qmm_logprobs(logits, targets=None, top=0)`` -> ``(logprob, entropy, top_logprobs, top_ids)``
+
+Work runs on the current stream of the tensors' device; results are new
+tensors unless ``out`` arguments are given. The workspace is the decode
+product's, one per device and stream, unless one is passed.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+import weight_only_group_amd as _qmm
+
+QMM_BF16, QMM_STRIPS = 1, 2
+QMM_RENORMALIZE, QMM_ADJACENT, QMM_FP32 = 4, 8, 16
+MOE_MAX_TOKENS = 64
+
+# Every symbol qmm_layer.h declares.
+EXPORTS = (
+    "qmm_moe_route_workspace_bytes", "qmm_moe_route", "qmm_moe_workspace_bytes", "qmm_moe", "qmm_kv_append",
+    "qmm_attention_workspace_bytes", "qmm_attention", "qmm_logprobs_workspace_bytes", "qmm_logprobs",
+)
+
+
+class Experts(ctypes.Structure):
+    """qmm_experts of the C ABI."""
+
+    _fields_ = [("qweight", ctypes.c_void_p), ("qweight_lo", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
+
+
+def declare(lib):
+    P, I, L, SZ, U, F = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_uint, ctypes.c_float)
+    E = ctypes.POINTER(Experts)
+    for name, res, args in (
+            ("qmm_moe_route_workspace_bytes", SZ, [I, I, I]),
+            ("qmm_moe_route", I, [P, I, I, P, I, I, U, P, P, P, P, SZ, P]),
+            ("qmm_moe_workspace_bytes", SZ, [I, I, I, I, I]),
+            ("qmm_moe", I, [P, I, I, I, I, I, P, P, E, E, I, I, U, P, P, SZ, P]),
+            ("qmm_kv_append", I, [P, L, P, L, P, L, I, I, I, I, P, P, I, I, P, P, P, P, P, I, I, U, P]),
+            ("qmm_attention_workspace_bytes", SZ, [I, I, I, I, I, I, I]),
+            ("qmm_attention", I, [P, L, I, I, I, I, P, P, I, I, P, I, P, P, I, I, I, P, P, F, F, P, U, P, P, SZ, P]),
+            ("qmm_logprobs_workspace_bytes", SZ, [I, I, I]),
+            ("qmm_logprobs", I, [P, L, I, I, P, I, U, P, P, P, P, P, SZ, P])):
+        f = getattr(lib, name)
+        f.restype, f.argtypes = res, args
+    return lib
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev} (got {t.device})")
+
+
+def _array(t, name, dtype, shape):
+    """A contiguous GPU tensor of exactly this type and shape."""
+    _qmm._gpu(t, name, dtype, ndim=len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)} (got {tuple(t.shape)})")
+    return t
+
+
+def _result(out, name, dtype, shape, dev):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    return _array(out, name, dtype, shape)
+
+
+def _space(workspace, dev, nbytes):
+    ws = workspace if workspace is not None else _qmm.gemv_workspace(dev, nbytes)
+    return _qmm._ptr(ws), 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def qmm_moe_route(x, router, top_k: int, renormalize: bool = True, workspace=None):
+    """The experts of each token: ``ids`` (T, top_k) int32, largest logit first, their ``weights``
+    (T, top_k) float32, and the ``logits`` (T, E) float32 = x @ router.T. ``router`` is (E, H)."""
+    dt = _qmm._data_dtype(x, "x")
+    _qmm._gpu(x, "x", dt)
+    _qmm._gpu(router, "router", dt)
+    T, H = x.shape
+    E = router.shape[0]
+    if router.shape[1] != H:
+        raise ValueError(f"router must be (E, {H}) (got {tuple(router.shape)})")
+    dev = x.device
+    _same_device(dev, router=router)
+    k = max(0, top_k)
+    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+    flags = (QMM_BF16 if dt == torch.bfloat16 else 0) | (QMM_RENORMALIZE if renormalize else 0)
+    lib = _qmm.library()
+    with torch.cuda.device(dev):
+        ws = _space(workspace, dev, lib.qmm_moe_route_workspace_bytes(T, H, E))
+        _qmm._check(lib.qmm_moe_route(_qmm._ptr(x), T, H, _qmm._ptr(router), E, top_k, flags, _qmm._ptr(ids),
+                                      _qmm._ptr(weights), _qmm._ptr(logits), *ws, _qmm._stream(dev)), "qmm_moe_route")
+    return ids, weights, logits
+
+
+def _experts(w, name, E, K, N, bits, group_size, dt, strips, dev):
+    """(qweight, qweight_lo, zeros, scales) of E experts, checked, as the C structure."""
+    qw, qlo, zeros, scales = w
+    if bits in _qmm.BITS and (group_size == -1 or (group_size > 0 and K % group_size == 0)):
+        shapes = _qmm.packed_shapes(K, N, bits)
+        if strips:
+            shapes = tuple(s and _qmm.strips_shape(s[0], N) for s in shapes)
+        _array(qw, f"{name} qweight", torch.int32, (E, *shapes[0]))
+        if bits == 3:
+            if qlo is None:
+                raise ValueError(f"{name}: 3-bit weights need qweight_lo (the 1-bit plane)")
+            _array(qlo, f"{name} qweight_lo", torch.int32, (E, *shapes[1]))
+        groups = 1 if group_size == -1 else K // group_size
+        _array(zeros, f"{name} zeros", dt, (E, groups, N))
+        _array(scales, f"{name} scales", dt, (E, groups, N))
+        _same_device(dev, qweight=qw, qweight_lo=qlo if bits == 3 else None, zeros=zeros, scales=scales)
+    return Experts(*(None if t is None else t.data_ptr() for t in (qw, qlo if bits == 3 else None, zeros, scales)))
+
+
+def qmm_moe(x, ids, weights, gate_up, down, bits: int, group_size: int, strips: bool = False, out=None, workspace=None):
+    """y[t] = sum_j weights[t, j] * (silu(g) * u) @ dequantize(down[ids[t, j]]), (g, u) the halves of
+    x[t] @ dequantize(gate_up[ids[t, j]]), for up to 64 tokens. ``gate_up`` and ``down`` are each
+    ``(qweight, qweight_lo, zeros, scales)`` with a leading expert axis, the planes K-major or, with
+    ``strips=True``, in the 16-column strips of qmm_to_strips."""
+    dt = _qmm._data_dtype(x, "x")
+    _qmm._gpu(x, "x", dt)
+    T, H = x.shape
+    dev = x.device
+    _qmm._gpu(ids, "ids", torch.int32)
+    k = ids.shape[1]
+    _array(ids, "ids", torch.int32, (T, k))
+    _array(weights, "weights", torch.float32, (T, k))
+    _same_device(dev, ids=ids, weights=weights)
+    if down[2].dim() != 3 or gate_up[2].dim() != 3 or gate_up[2].shape[2] % 2:
+        raise ValueError("zeros must be (E, G, 2 I) for gate_up and (E, G, H) for down")
+    E, _, N = gate_up[2].shape
+    I = N // 2
+    gu = _experts(gate_up, "gate_up", E, H, N, bits, group_size, dt, strips, dev)
+    dn = _experts(down, "down", E, I, H, bits, group_size, dt, strips, dev)
+    y = _result(out, "out", dt, (T, H), dev)
+    lib = _qmm.library()
+    with torch.cuda.device(dev):
+        ws = _space(workspace, dev, lib.qmm_moe_workspace_bytes(T, H, I, E, k))
+        _qmm._check(lib.qmm_moe(_qmm._ptr(x), T, H, I, E, k, _qmm._ptr(ids), _qmm._ptr(weights), ctypes.byref(gu),
+                                ctypes.byref(dn), bits, group_size, _qmm._flags(dt, strips), _qmm._ptr(y), *ws,
+                                _qmm._stream(dev)), "qmm_moe")
+    return y
+
+
+def _heads(t, name, dt):
+    """(T, heads, D) with dense heads; the token stride is free (a view of a product's rows)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU (got {t.device})")
+    if t.dtype != dt:
+        raise TypeError(f"{name} must be {dt} (got {t.dtype})")
+    if t.dim() != 3 or (t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]))):
+        raise ValueError(f"{name} must be (tokens, heads, D) with dense heads (got shape {tuple(t.shape)}, strides {t.stride()})")
+    # One token's stride is never used; a view may report any.
+    return t, t.shape[1] * t.shape[2] if t.shape[0] < 2 else t.stride(0)
+
+
+def _cache(k_cache, v_cache, Hkv, D, dt):
+    _qmm._gpu(k_cache, "k_cache", dt, ndim=4)
+    _array(v_cache, "v_cache", dt, k_cache.shape)
+    pages, hkv, page_size, d = k_cache.shape
+    if d != D or (Hkv is not None and hkv != Hkv):
+        raise ValueError(f"k_cache must be (pages, Hkv, page_size, {D}) (got {tuple(k_cache.shape)})")
+    return pages, hkv, page_size
+
+
+def qmm_kv_append(q, k, v, cos, sin, positions, slots, k_cache, v_cache, adjacent: bool = False, out=None):
+    """Rotates q (T, Hq, D) and k (T, Hkv, D) by the rows ``positions`` of cos and sin (P, R / 2), stores
+    k and v at ``slots`` (int64; a token with a slot outside the cache is not stored) of the caches
+    (pages, Hkv, page_size, D), and returns the rotated q. q, k and v may be views of one product's
+    rows. ``adjacent``: pairs are (2i, 2i + 1), else (i, i + R / 2). cos None: no rotation."""
+    dt = _qmm._data_dtype(q, "q")
+    q, qs = _heads(q, "q", dt)
+    k, ks = _heads(k, "k", dt)
+    v, vs = _heads(v, "v", dt)
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if tuple(k.shape) != (T, Hkv, D) or tuple(v.shape) != (T, Hkv, D):
+        raise ValueError(f"k and v must be ({T}, Hkv, {D}) (got {tuple(k.shape)}, {tuple(v.shape)})")
+    pages, _, page_size = _cache(k_cache, v_cache, Hkv, D, dt)
+    P = R = 0
+    if cos is not None:
+        _qmm._gpu(cos, "cos", torch.float32)
+        _array(sin, "sin", torch.float32, cos.shape)
+        _array(positions, "positions", torch.int32, (T,))
+        P, R = cos.shape[0], 2 * cos.shape[1]
+    _array(slots, "slots", torch.int64, (T,))
+    dev = q.device
+    _same_device(dev, k=k, v=v, cos=cos, sin=sin if R else None, positions=positions if R else None, slots=slots,
+                 k_cache=k_cache, v_cache=v_cache)
+    out = _result(out, "out", dt, (T, Hq, D), dev)
+    flags = (QMM_BF16 if dt == torch.bfloat16 else 0) | (QMM_ADJACENT if adjacent else 0)
+    p = _qmm._ptr
+    with torch.cuda.device(dev):
+        _qmm._check(_qmm.library().qmm_kv_append(p(q), qs, p(k), ks, p(v), vs, T, Hq, Hkv, D, p(cos) if R else None,
+                                                 p(sin) if R else None, R, P, p(positions) if R else None, p(slots),
+                                                 p(out), p(k_cache), p(v_cache), pages, page_size, flags,
+                                                 _qmm._stream(dev)), "qmm_kv_append")
+    return out
+
+
+def qmm_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q: int, max_kv: int, scale=None,
+                  softcap: float = 0.0, slopes=None, first=None, end=None, out=None, workspace=None):
+    """Attention of the queries q (T, Hq, D) to the cached keys of their sequences. Sequence b has the
+    rows q_starts[b] to q_starts[b + 1] and kv_lens[b] cached tokens, its new ones the last. A query at
+    position p sees the keys from ``first`` (default 0) up to, without, ``end`` (default p + 1); one that
+    sees none gets 0. ``scale`` defaults to 1 / sqrt(D); ``softcap`` c > 0 takes c tanh(s / c) of the
+    scores; ``slopes`` (Hq,) subtract slope * |p - key position|. max_q and max_kv bound the lengths."""
+    dt = _qmm._data_dtype(q, "q")
+    q, qs = _heads(q, "q", dt)
+    T, Hq, D = q.shape
+    pages, Hkv, page_size = _cache(k_cache, v_cache, None, D, dt)
+    _qmm._gpu(page_table, "page_table", torch.int32)
+    B = page_table.shape[0]
+    _array(kv_lens, "kv_lens", torch.int32, (B,))
+    _array(q_starts, "q_starts", torch.int32, (B + 1,))
+    if first is not None:
+        _array(first, "first", torch.int32, (T,))
+    if end is not None:
+        _array(end, "end", torch.int32, (T,))
+    if slopes is not None:
+        _array(slopes, "slopes", torch.float32, (Hq,))
+    dev = q.device
+    _same_device(dev, k_cache=k_cache, v_cache=v_cache, page_table=page_table, kv_lens=kv_lens, q_starts=q_starts,
+                 first=first, end=end, slopes=slopes)
+    out = _result(out, "out", dt, (T, Hq, D), dev)
+    lib, p = _qmm.library(), _qmm._ptr
+    with torch.cuda.device(dev):
+        ws = _space(workspace, dev, lib.qmm_attention_workspace_bytes(B, T, Hq, Hkv, D, max_q, max_kv))
+        _qmm._check(lib.qmm_attention(p(q), qs, T, Hq, Hkv, D, p(k_cache), p(v_cache), pages, page_size, p(page_table),
+                                      page_table.shape[1], p(kv_lens), p(q_starts), B, max_q, max_kv, p(first), p(end),
+                                      1.0 / math.sqrt(D) if scale is None else scale, softcap, p(slopes),
+                                      QMM_BF16 if dt == torch.bfloat16 else 0, p(out), *ws, _qmm._stream(dev)),
+                    "qmm_attention")
+    return out
+
+
+def qmm_logprobs(logits, targets=None, top: int = 0, workspace=None):
+    """Per row of logits (M, V) (float16, bfloat16 or float32; rows may be strided): the log probability
+    of ``targets`` (int64; None: not asked for), the entropy, and the ``top`` likeliest tokens' log
+    probabilities and ids. All float32, ids int32. A negative target gives 0."""
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if logits.dtype not in (*_qmm.DTYPES, torch.float32):
+        raise TypeError(f"logits must be float16, bfloat16 or float32 (got {logits.dtype})")
+    if not logits.is_cuda:
+        raise ValueError(f"logits must be on a GPU (got {logits.device})")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError(f"logits must be (M, V) with dense rows (got shape {tuple(logits.shape)}, strides {logits.stride()})")
+    M, V = logits.shape
+    stride = V if M < 2 else logits.stride(0)
+    dev = logits.device
+    if targets is not None:
+        _array(targets, "targets", torch.int64, (M,))
+        _same_device(dev, targets=targets)
+    new = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+    n = max(0, top)
+    logprob, entropy = new(M) if targets is not None else None, new(M)
+    top_logprobs, top_ids = new(M, n), new(M, n, dtype=torch.int32)
+    flags = {torch.float16: 0, torch.bfloat16: QMM_BF16, torch.float32: QMM_FP32}[logits.dtype]
+    lib, p = _qmm.library(), _qmm._ptr
+    with torch.cuda.device(dev):
+        ws = _space(workspace, dev, lib.qmm_logprobs_workspace_bytes(M, V, top))
+        _qmm._check(lib.qmm_logprobs(p(logits), stride, M, V, p(targets), top, flags, p(logprob), p(entropy),
+                                     p(top_logprobs), p(top_ids), *ws, _qmm._stream(dev)), "qmm_logprobs")
+    return logprob, entropy, top_logprobs, top_ids
