@@ -96,6 +96,7 @@ qmm_status qmm_moe(const uint16_t* x, int T, int H, int I, int E, int top_k, con
  * Paged cache: keys and values of Hkv heads in pages of page_size tokens,
  * k_cache and v_cache (pages, Hkv, page_size, D): a head's tokens of one page
  * lie one behind another. Slot s is token s % page_size of page s / page_size.
+ * pages * Hkv * page_size < 2^31.
  *
  * qmm_kv_append -- rotates the queries and the keys of T new tokens and puts
  * keys and values into the cache:
@@ -145,7 +146,8 @@ qmm_status qmm_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* k,
  * Requirements: D 64, 128 or 256; Hq % Hkv == 0; page_size >= 1; q_stride % 8
  * == 0 and >= Hq * D; scale and softcap finite, softcap >= 0; q, out, caches
  * and workspace 16-byte aligned, the int32 and fp32 arrays 4-byte;
- * max_kv <= table_stride * page_size < 2^31, T * Hq < 2^31. Flags: QMM_BF16.
+ * max_kv <= table_stride * page_size < 2^31, T * Hq and max_q * Hq < 2^31, B <=
+ * 65535, pages * Hkv * page_size < 2^31. Flags: QMM_BF16.
  * Page ids are cut to [0, pages). Equal inputs give equal bits.
  */
 size_t qmm_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int max_q, int max_kv);

@@ -65,9 +65,10 @@ qmm_status check_heads(int Hq, int Hkv, int D) {
   return QMM_OK;
 }
 
-qmm_status check_cache(const void* k_cache, const void* v_cache, int pages, int page_size) {
-  if (pages < 1 || page_size < 1 || (long long)pages * page_size >= (1ll << 40))
-    return fail(QMM_ERR_SHAPE, "pages=%d and page_size=%d must be >= 1", pages, page_size);
+// The kernels number a cache's rows (a token of a head) with 32 bits.
+qmm_status check_cache(const void* k_cache, const void* v_cache, int pages, int Hkv, int page_size) {
+  if (pages < 1 || page_size < 1 || (long long)pages * page_size >= (1ll << 31) || (long long)pages * page_size * Hkv >= (1ll << 31))
+    return fail(QMM_ERR_SHAPE, "pages=%d and page_size=%d must be >= 1, pages * Hkv * page_size below 2^31", pages, page_size);
   if (!k_cache || !v_cache) return fail(QMM_ERR_NULL, "k_cache or v_cache is NULL");
   if (!aligned16(k_cache) || !aligned16(v_cache)) return fail(QMM_ERR_ALIGN, "k_cache and v_cache must be 16-byte aligned");
   return QMM_OK;
@@ -76,7 +77,8 @@ qmm_status check_cache(const void* k_cache, const void* v_cache, int pages, int 
 bool stride_ok(long long stride, long long least) { return stride >= least && stride % 8 == 0 && stride < (1ll << 40); }
 
 bool attention_counts_ok(int B, int T, int Hq, int max_q, int max_kv) {
-  return B >= 0 && T >= 0 && (long long)T * Hq < (1ll << 31) && max_q >= 0 && max_kv >= 0 && B <= 65535;
+  return B >= 0 && T >= 0 && (long long)T * Hq < (1ll << 31) && max_q >= 0 && max_kv >= 0 && B <= 65535 &&
+         (long long)max_q * Hq < (1ll << 31);
 }
 
 }  // namespace
@@ -155,7 +157,7 @@ qmm_status qmm_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* k,
       !stride_ok(v_stride, (long long)Hkv * D))
     return fail(QMM_ERR_SHAPE, "token strides must be multiples of 8 and at least a token's size");
   if (T == 0) return ok();
-  st = check_cache(k_cache, v_cache, pages, page_size);
+  st = check_cache(k_cache, v_cache, pages, Hkv, page_size);
   if (st != QMM_OK) return st;
   if (!q || !k || !v || !slots || !q_out || (R > 0 && (!cos || !sin || !positions)))
     return fail(QMM_ERR_NULL, "a required pointer is NULL");
@@ -186,14 +188,14 @@ qmm_status qmm_attention(const uint16_t* q, int64_t q_stride, int T, int Hq, int
   if (st == QMM_OK) st = check_heads(Hq, Hkv, D);
   if (st != QMM_OK) return st;
   if (!attention_counts_ok(B, T, Hq, max_q, max_kv))
-    return fail(QMM_ERR_SHAPE, "B=%d (at most 65535), T=%d, max_q=%d and max_kv=%d must be >= 0, T * Hq below 2^31", B, T,
+    return fail(QMM_ERR_SHAPE, "B=%d (at most 65535), T=%d, max_q=%d and max_kv=%d must be >= 0, T * Hq and max_q * Hq below 2^31", B, T,
                 max_q, max_kv);
   if (!stride_ok(q_stride, (long long)Hq * D))
     return fail(QMM_ERR_SHAPE, "q_stride=%lld must be a multiple of 8, at least Hq * D", (long long)q_stride);
   if (!isfinite(scale) || !isfinite(softcap) || softcap < 0)
     return fail(QMM_ERR_SHAPE, "scale=%g and softcap=%g must be finite, softcap not negative", scale, softcap);
   if (T == 0 || B == 0 || max_q == 0) return ok();
-  st = check_cache(k_cache, v_cache, pages, page_size);
+  st = check_cache(k_cache, v_cache, pages, Hkv, page_size);
   if (st != QMM_OK) return st;
   if (table_stride < 1 || (long long)table_stride * page_size >= (1ll << 31) || max_kv > (long long)table_stride * page_size)
     return fail(QMM_ERR_SHAPE, "max_kv=%d must not exceed table_stride=%d * page_size=%d (below 2^31)", max_kv,
