@@ -11,6 +11,7 @@ namespace qmm {
 constexpr size_t kWorkspaceHeader = size_t(kGemvMaxStrips) * 4;
 
 // ---- mixture of experts ---------------------------------------------------------
+constexpr int kMoeTokens = 64, kMoeExperts = 1024;  // most of a call
 struct RouteArgs {
   const uint16_t* x;
   const uint16_t* router;

@@ -29,6 +29,8 @@ qmm_status check_workspace(const void* workspace, size_t bytes, size_t need) {
 
 // ---- mixture of experts ---------------------------------------------------------
 
+static_assert(QMM_MOE_MAX_TOKENS == qmm::kMoeTokens && QMM_MOE_MAX_EXPERTS == qmm::kMoeExperts, "limits of the kernels");
+
 qmm_status check_route_shape(int T, int H, int E) {
   if (T < 0 || T > QMM_MOE_MAX_TOKENS) return fail(QMM_ERR_SHAPE, "T=%d must be in [0, %d]", T, QMM_MOE_MAX_TOKENS);
   if (H < 32 || H % 32 || H > (1 << 20)) return fail(QMM_ERR_SHAPE, "H=%d must be a multiple of 32 in [32, 2^20]", H);
