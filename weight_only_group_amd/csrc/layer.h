@@ -74,6 +74,7 @@ size_t attention_workspace(int B, int T, int Hq, int Hkv, int D, int max_q, int 
 hipError_t launch_attention(const AttentionArgs& a, bool bf16, hipStream_t stream);
 
 // ---- log probabilities ----------------------------------------------------------------
+constexpr int kMaxTop = 32;
 enum class LogitType { kFp16, kBf16, kFp32 };
 struct LogprobArgs {
   const void* logits;

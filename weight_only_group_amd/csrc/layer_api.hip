@@ -29,7 +29,8 @@ qmm_status check_workspace(const void* workspace, size_t bytes, size_t need) {
 
 // ---- mixture of experts ---------------------------------------------------------
 
-static_assert(QMM_MOE_MAX_TOKENS == qmm::kMoeTokens && QMM_MOE_MAX_EXPERTS == qmm::kMoeExperts, "limits of the kernels");
+static_assert(QMM_MOE_MAX_TOKENS == qmm::kMoeTokens && QMM_MOE_MAX_EXPERTS == qmm::kMoeExperts &&
+              QMM_LOGPROBS_MAX_TOP == qmm::kMaxTop, "limits of the kernels");
 
 qmm_status check_route_shape(int T, int H, int E) {
   if (T < 0 || T > QMM_MOE_MAX_TOKENS) return fail(QMM_ERR_SHAPE, "T=%d must be in [0, %d]", T, QMM_MOE_MAX_TOKENS);

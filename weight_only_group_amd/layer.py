@@ -14,6 +14,7 @@ product's, one per device and stream, unless one is passed.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -76,9 +77,35 @@ def _result(out, name, dtype, shape, dev):
     return _array(out, name, dtype, shape)
 
 
-def _space(workspace, dev, nbytes):
-    ws = workspace if workspace is not None else _qmm.gemv_workspace(dev, nbytes)
-    return _qmm._ptr(ws), 0 if ws is None else ws.numel() * ws.element_size()
+@functools.lru_cache(maxsize=4096)
+def _need(name, *shape):
+    """A call's ..._workspace_bytes (a plan of the shape alone: asked once per shape and device)."""
+    return getattr(_qmm.library(), name + "_workspace_bytes")(*shape[1:])
+
+
+def _launch(name, dev, args, out=(), workspace=None, shape=None):
+    """Calls the entry point on the device's current stream; with `shape`, a workspace goes before the stream."""
+    here = torch.cuda.current_device()
+    if here != dev.index:
+        with torch.cuda.device(dev):
+            return _launch(name, dev, args, out, workspace, shape)
+    stream = torch._C._cuda_getCurrentRawStream(here)
+    if shape is not None:
+        if workspace is None:
+            need = _need(name, here, *shape)
+            workspace = _qmm._workspaces.get((here, stream))
+            if need and (workspace is None or workspace.numel() < need):
+                workspace = _qmm.gemv_workspace(dev, need)
+        ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        args = (*args, *ws)
+    status = getattr(_qmm._lib or _qmm.library(), name)(*args, stream)
+    if status:
+        _qmm._check(status, name)
+    return out
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
 
 
 def qmm_moe_route(x, router, top_k: int, renormalize: bool = True, workspace=None):
@@ -98,12 +125,8 @@ def qmm_moe_route(x, router, top_k: int, renormalize: bool = True, workspace=Non
     weights = torch.empty((T, k), dtype=torch.float32, device=dev)
     logits = torch.empty((T, E), dtype=torch.float32, device=dev)
     flags = (QMM_BF16 if dt == torch.bfloat16 else 0) | (QMM_RENORMALIZE if renormalize else 0)
-    lib = _qmm.library()
-    with torch.cuda.device(dev):
-        ws = _space(workspace, dev, lib.qmm_moe_route_workspace_bytes(T, H, E))
-        _qmm._check(lib.qmm_moe_route(_qmm._ptr(x), T, H, _qmm._ptr(router), E, top_k, flags, _qmm._ptr(ids),
-                                      _qmm._ptr(weights), _qmm._ptr(logits), *ws, _qmm._stream(dev)), "qmm_moe_route")
-    return ids, weights, logits
+    return _launch("qmm_moe_route", dev, (_p(x), T, H, _p(router), E, top_k, flags, _p(ids), _p(weights), _p(logits)),
+                   (ids, weights, logits), workspace, (T, H, E))
 
 
 def _experts(w, name, E, K, N, bits, group_size, dt, strips, dev):
@@ -146,13 +169,8 @@ def qmm_moe(x, ids, weights, gate_up, down, bits: int, group_size: int, strips: 
     gu = _experts(gate_up, "gate_up", E, H, N, bits, group_size, dt, strips, dev)
     dn = _experts(down, "down", E, I, H, bits, group_size, dt, strips, dev)
     y = _result(out, "out", dt, (T, H), dev)
-    lib = _qmm.library()
-    with torch.cuda.device(dev):
-        ws = _space(workspace, dev, lib.qmm_moe_workspace_bytes(T, H, I, E, k))
-        _qmm._check(lib.qmm_moe(_qmm._ptr(x), T, H, I, E, k, _qmm._ptr(ids), _qmm._ptr(weights), ctypes.byref(gu),
-                                ctypes.byref(dn), bits, group_size, _qmm._flags(dt, strips), _qmm._ptr(y), *ws,
-                                _qmm._stream(dev)), "qmm_moe")
-    return y
+    return _launch("qmm_moe", dev, (_p(x), T, H, I, E, k, _p(ids), _p(weights), ctypes.byref(gu), ctypes.byref(dn), bits,
+                                    group_size, _qmm._flags(dt, strips), _p(y)), y, workspace, (T, H, I, E, k))
 
 
 def _heads(t, name, dt):
@@ -204,13 +222,9 @@ def qmm_kv_append(q, k, v, cos, sin, positions, slots, k_cache, v_cache, adjacen
                  k_cache=k_cache, v_cache=v_cache)
     out = _result(out, "out", dt, (T, Hq, D), dev)
     flags = (QMM_BF16 if dt == torch.bfloat16 else 0) | (QMM_ADJACENT if adjacent else 0)
-    p = _qmm._ptr
-    with torch.cuda.device(dev):
-        _qmm._check(_qmm.library().qmm_kv_append(p(q), qs, p(k), ks, p(v), vs, T, Hq, Hkv, D, p(cos) if R else None,
-                                                 p(sin) if R else None, R, P, p(positions) if R else None, p(slots),
-                                                 p(out), p(k_cache), p(v_cache), pages, page_size, flags,
-                                                 _qmm._stream(dev)), "qmm_kv_append")
-    return out
+    turn = (_p(cos), _p(sin), R, P, _p(positions)) if R else (None, None, 0, 0, None)
+    return _launch("qmm_kv_append", dev, (_p(q), qs, _p(k), ks, _p(v), vs, T, Hq, Hkv, D, *turn, _p(slots), _p(out),
+                                          _p(k_cache), _p(v_cache), pages, page_size, flags), out)
 
 
 def qmm_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q: int, max_kv: int, scale=None,
@@ -238,15 +252,10 @@ def qmm_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q: int
     _same_device(dev, k_cache=k_cache, v_cache=v_cache, page_table=page_table, kv_lens=kv_lens, q_starts=q_starts,
                  first=first, end=end, slopes=slopes)
     out = _result(out, "out", dt, (T, Hq, D), dev)
-    lib, p = _qmm.library(), _qmm._ptr
-    with torch.cuda.device(dev):
-        ws = _space(workspace, dev, lib.qmm_attention_workspace_bytes(B, T, Hq, Hkv, D, max_q, max_kv))
-        _qmm._check(lib.qmm_attention(p(q), qs, T, Hq, Hkv, D, p(k_cache), p(v_cache), pages, page_size, p(page_table),
-                                      page_table.shape[1], p(kv_lens), p(q_starts), B, max_q, max_kv, p(first), p(end),
-                                      1.0 / math.sqrt(D) if scale is None else scale, softcap, p(slopes),
-                                      QMM_BF16 if dt == torch.bfloat16 else 0, p(out), *ws, _qmm._stream(dev)),
-                    "qmm_attention")
-    return out
+    args = (_p(q), qs, T, Hq, Hkv, D, _p(k_cache), _p(v_cache), pages, page_size, _p(page_table), page_table.shape[1],
+            _p(kv_lens), _p(q_starts), B, max_q, max_kv, _p(first), _p(end), 1.0 / math.sqrt(D) if scale is None else scale,
+            softcap, _p(slopes), QMM_BF16 if dt == torch.bfloat16 else 0, _p(out))
+    return _launch("qmm_attention", dev, args, out, workspace, (B, T, Hq, Hkv, D, max_q, max_kv))
 
 
 def qmm_logprobs(logits, targets=None, top: int = 0, workspace=None):
@@ -272,9 +281,6 @@ def qmm_logprobs(logits, targets=None, top: int = 0, workspace=None):
     logprob, entropy = new(M) if targets is not None else None, new(M)
     top_logprobs, top_ids = new(M, n), new(M, n, dtype=torch.int32)
     flags = {torch.float16: 0, torch.bfloat16: QMM_BF16, torch.float32: QMM_FP32}[logits.dtype]
-    lib, p = _qmm.library(), _qmm._ptr
-    with torch.cuda.device(dev):
-        ws = _space(workspace, dev, lib.qmm_logprobs_workspace_bytes(M, V, top))
-        _qmm._check(lib.qmm_logprobs(p(logits), stride, M, V, p(targets), top, flags, p(logprob), p(entropy),
-                                     p(top_logprobs), p(top_ids), *ws, _qmm._stream(dev)), "qmm_logprobs")
-    return logprob, entropy, top_logprobs, top_ids
+    return _launch("qmm_logprobs", dev, (_p(logits), stride, M, V, _p(targets), top, flags, _p(logprob), _p(entropy),
+                                         _p(top_logprobs), _p(top_ids)),
+                   (logprob, entropy, top_logprobs, top_ids), workspace, (M, V, top))
