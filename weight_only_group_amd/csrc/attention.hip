@@ -7,6 +7,9 @@
 // The rows of one key head are the (token, head of the group) pairs of a
 // sequence, i * G + g; sixteen rows make a tile, and a wave takes 32 keys of a
 // tile at a time (a chunk).
+#include <type_traits>
+
+#include "handoff.h"
 #include "layer.h"
 #include "mfma.h"
 
@@ -39,8 +42,22 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int max_q, int max_kv, DeviceTopo top
   return p;
 }
 
+// Division of 0 <= n < 2^31 by a fixed divisor: n mul >> shift, with mul = ceil(2^shift / d)
+// and shift = 31 + ceil(log2 d) (the excess of mul stays below one part in n).
+struct FixedDiv {
+  uint32_t mul;
+  int shift;
+  __device__ __forceinline__ int operator()(int n) const { return (int)((uint64_t)(uint32_t)n * mul >> shift); }
+};
+FixedDiv fixed_div(int d) {
+  int l = 0;
+  while ((1ll << l) < d) ++l;
+  return {(uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d), 31 + l};
+}
+
 struct AttnKernelArgs {
   AttentionArgs a;
+  FixedDiv by_page, by_group;
   int group, rtiles, split;
   uint32_t* counters;
   float* part;  // (tiles, split, 16, D) sums, then (tiles, split, 16, 2) maximum and denominator
@@ -73,12 +90,13 @@ __device__ __forceinline__ ScoreRule score_rule(const AttentionArgs& a, int head
 struct Row {
   int token, head, pos, lo, hi;
 };
-__device__ __forceinline__ Row row_of(const AttentionArgs& a, int r, int q0, int q1, int kv, int hk, int group) {
+__device__ __forceinline__ Row row_of(const AttnKernelArgs& p, int r, int q0, int q1, int kv, int hk) {
+  const AttentionArgs& a = p.a;
   Row w = {-1, 0, 0, 0, 0};
-  const int i = r / group;
+  const int i = p.by_group(r);
   if (i >= q1 - q0) return w;
   w.token = q0 + i;
-  w.head = hk * group + r - i * group;
+  w.head = hk * p.group + r - i * p.group;
   w.pos = kv - (q1 - q0) + i;
   w.lo = a.first ? max(a.first[w.token], 0) : 0;
   w.hi = min(a.end ? a.end[w.token] : w.pos + 1, kv);
@@ -104,7 +122,7 @@ __device__ __forceinline__ bool not_finite(uint32_t v) {
 // dimensions of its eight keys, whole cache lines per 16 lanes, and pairs them up
 // with byte permutes; dimension d = 8 m + i is row m of product i.
 template <bool BF, int D>
-__global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_split_kernel(AttnKernelArgs p) {
+__global__ void __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) attention_split_kernel(AttnKernelArgs p) {
   constexpr int STEPS = D / 32;
   constexpr int CH = D >= 128 ? 8 : 4;  // dimensions per lane and half
   constexpr int NH = D / (16 * CH);
@@ -122,12 +140,12 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_split_kernel(
   const int kv = min(max(a.kv_lens[b], 0), a.max_kv);
   if (rt * kRows >= (q1 - q0) * p.group) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 15, kg = lane >> 4;
-  const Row row = row_of(a, rt * kRows + n, q0, q1, kv, hk, p.group);
+  const Row row = row_of(p, rt * kRows + n, q0, q1, kv, hk);
   const ScoreRule rule = score_rule(a, row.head);
 
   // The keys that any row sees, and those that all see.
   int lo = row.lo < row.hi ? row.lo : INT32_MAX, hi = row.lo < row.hi ? row.hi : 0;
-  int all_lo = row.lo, all_hi = row.hi;
+  int all_lo = row.token < 0 ? 0 : row.lo, all_hi = row.token < 0 ? INT32_MAX : row.hi;  // rows past the last count as seeing all
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) {
     lo = min(lo, __shfl_xor(lo, o));
@@ -152,7 +170,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_split_kernel(
   const int32_t* table = a.page_table + (long long)b * a.table_stride;
   auto key_row = [&](int c) -> uint32_t {
     const int j = min(max(c * kChunk + (lane & 31), lo), hi - 1);
-    const int at = j / a.page_size;
+    const int at = p.by_page(j);
     const int page = min(max(table[at], 0), a.pages - 1);
     return ((uint32_t)page * a.Hkv + hk) * a.page_size + (j - at * a.page_size);
   };
@@ -179,25 +197,23 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_split_kernel(
   f32x4 acc[NH][CH] = {};
   float mx = -INFINITY, sum = 0;
   bool any_bad = false;
-  int c = c0 + wave;
   uint32_t rows = 0, rows_next = 0;
-  if (c < c1) {
-    rows = key_row(c);
-    load_k(rows);
-    load_v(rows);
-    rows_next = key_row(c + kWaves);
-  }
-  for (; c < c1; c += kWaves) {
+  // One chunk; with MORE the next one's loads go out as the registers fall free.
+  auto step = [&](int c, auto more) {
+    constexpr bool MORE = decltype(more)::value;
     f32x4 st[2] = {};
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
 #pragma unroll
       for (int t = 0; t < 2; ++t) st[t] = mfma16<BF>(k[t][s], q[s], st[t]);
-    const bool more = c + kWaves < c1;
-    rows = rows_next;
-    if (more) {
-      load_k(rows);
+    if constexpr (MORE) {
+      // The page lookup before the keys: loads come back in order, and its row is computed with first.
+      const uint32_t next = rows_next;
       rows_next = key_row(c + 2 * kWaves);
+      rows = next;
+      __builtin_amdgcn_sched_barrier(0);  // the loads take the registers that the products above have read
+      load_k(rows);
+      __builtin_amdgcn_sched_barrier(0);
     }
     // Scores: keys 32c + 16t + 4kg + r of row n.
     const int j0 = c * kChunk + 4 * kg;
@@ -268,7 +284,20 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_split_kernel(
         for (int x = 0; x < 4; ++x) vt[x] = __builtin_amdgcn_perm(v[h][2 * x + 1][i / 2], v[h][2 * x][i / 2], sel);
         acc[h][i] = mfma16<BF>(vt, w, acc[h][i]);
       }
-    if (more) load_v(rows);
+    if constexpr (MORE) {
+      __builtin_amdgcn_sched_barrier(0);
+      load_v(rows);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  int c = c0 + wave;
+  if (c < c1) {
+    rows = key_row(c);
+    load_k(rows);
+    load_v(rows);
+    rows_next = key_row(c + kWaves);
+    for (; c + kWaves < c1; c += kWaves) step(c, std::true_type{});
+    step(c, std::false_type{});
   }
 
   // The waves' sums meet in LDS, in wave order.
@@ -311,41 +340,50 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_split_kernel(
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] += so[w][r][d0 + e] * f;
   }
-  const Row mine = row_of(a, rt * kRows + r, q0, q1, kv, hk, p.group);
+  const Row mine = row_of(p, rt * kRows + r, q0, q1, kv, hk);
   if (p.split > 1) {
     // Partial sums of the parts, joined in order by the block that arrives last.
     const size_t tile = ((size_t)b * a.Hkv + hk) * p.rtiles + rt;
     float* po = p.part + ((tile * p.split + part) * kRows + r) * D + d0;
 #pragma unroll
-    for (int e = 0; e < E; e += 4) *reinterpret_cast<f32x4*>(po + e) = f32x4{o[e], o[e + 1], o[e + 2], o[e + 3]};
-    if ((tid & 15) == 0) {
-      float* pm = p.part_ml + ((tile * p.split + part) * kRows + r) * 2;
-      pm[0] = m;
-      pm[1] = l;
-    }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-    __syncthreads();
-    if (tid == 0) {
-      const uint32_t ticket = __hip_atomic_fetch_add(&p.counters[tile], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-      s_last = ticket == (uint32_t)p.split - 1;
-      if (s_last) __hip_atomic_store(&p.counters[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
-    if (!s_last) return;
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    for (int e = 0; e < E; e += 2) handoff_store(po + e, o[e], o[e + 1]);
+    if ((tid & 15) == 0) handoff_store(p.part_ml + ((tile * p.split + part) * kRows + r) * 2, m, l);
+    if (!handoff_last(&p.counters[tile], (uint32_t)p.split, &s_last)) return;
     const float* qo = p.part + (tile * p.split * kRows + r) * D + d0;
     const float* qm = p.part_ml + (tile * p.split * kRows + r) * 2;
+    // Four parts' loads at a time; places past the last part repeat it with a factor of 0.
+    constexpr int kBatch = 4;
     m = -INFINITY;
-    for (int s = 0; s < p.split; ++s) m = fmaxf(m, qm[s * kRows * 2]);
+    for (int s0 = 0; s0 < p.split; s0 += kBatch) {
+      float ms[kBatch];
+#pragma unroll
+      for (int s = 0; s < kBatch; ++s) ms[s] = handoff_load(qm + min(s0 + s, p.split - 1) * kRows * 2);
+#pragma unroll
+      for (int s = 0; s < kBatch; ++s) m = fmaxf(m, ms[s]);
+    }
     l = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0;
-    for (int s = 0; s < p.split; ++s) {
-      const float ms = qm[s * kRows * 2];
-      const float f = ms == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms - m);
-      l += qm[s * kRows * 2 + 1] * f;
+    for (int s0 = 0; s0 < p.split; s0 += kBatch) {
+      float ms[kBatch], ls[kBatch];
+      FloatPair os[kBatch][E / 2];
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] += qo[(size_t)s * kRows * D + e] * f;
+      for (int s = 0; s < kBatch; ++s) {
+        const int at = min(s0 + s, p.split - 1);
+        const FloatPair ml = handoff_load_pair(qm + at * kRows * 2);
+        ms[s] = ml.a;
+        ls[s] = ml.b;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) os[s][e] = handoff_load_pair(qo + (size_t)at * kRows * D + 2 * e);
+      }
+#pragma unroll
+      for (int s = 0; s < kBatch; ++s) {
+        const float f = s0 + s >= p.split || ms[s] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms[s] - m);
+        l += ls[s] * f;
+        // (a sum that is not finite goes with a finite maximum or a weight that is not: f is not 0 then)
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += f == 0.f ? 0.f : (e & 1 ? os[s][e / 2].b : os[s][e / 2].a) * f;
+      }
     }
   }
   if (mine.token < 0) return;
@@ -359,7 +397,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_split_kernel(
 template <bool BF, int D>
 hipError_t launch_split(const AttentionArgs& a, hipStream_t stream) {
   const AttnPlan plan = attn_plan(a.B, a.Hq, a.Hkv, a.max_q, a.max_kv, device_topology());
-  AttnKernelArgs p = {a, plan.group, plan.rtiles, plan.split, reinterpret_cast<uint32_t*>(a.workspace), nullptr, nullptr};
+  AttnKernelArgs p = {a, fixed_div(a.page_size), fixed_div(plan.group), plan.group, plan.rtiles, plan.split, reinterpret_cast<uint32_t*>(a.workspace), nullptr, nullptr};
   if (plan.split > 1) {
     p.part = reinterpret_cast<float*>(a.workspace + kWorkspaceHeader);
     p.part_ml = p.part + plan.tiles * plan.split * kRows * D;

@@ -9,6 +9,7 @@
 // index in the lower half, so that keys differ, and larger keys come first. A wave
 // keeps the largest key that each lane has seen: the top-th largest of those is no
 // larger than the wave's top-th key, and few keys reach it. They go to a list.
+#include "handoff.h"
 #include "layer.h"
 
 namespace qmm {
@@ -262,36 +263,31 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobKernelArgs p)
   }
   if (p.split > 1) {
     const size_t at = (size_t)m * p.split + part;
-    if (tid < top) p.keys[at * top + tid] = best[tid];
+    if (tid < top) handoff_store(&p.keys[at * top + tid], best[tid]);
     if (tid == 0) {
-      float* w = p.sums + at * 4;
-      w[0] = sum.m;
-      w[1] = sum.s;
-      w[2] = sum.a;
+      handoff_store(p.sums + at * 4, sum.m, sum.s);
+      handoff_store(p.sums + at * 4 + 2, sum.a);
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-    __syncthreads();
-    if (tid == 0) {
-      const uint32_t ticket = __hip_atomic_fetch_add(&p.counters[m], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-      s_last = ticket == (uint32_t)p.split - 1;
-      if (s_last) __hip_atomic_store(&p.counters[m], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
-    if (!s_last) return;
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    if (!handoff_last(&p.counters[m], (uint32_t)p.split, &s_last)) return;
     const float* w = p.sums + (size_t)m * p.split * 4;
-    sum = lane < p.split ? Sums{w[lane * 4], w[lane * 4 + 1], w[lane * 4 + 2]} : Sums{-INFINITY, 0, 0};
+    sum = Sums{-INFINITY, 0, 0};
+    if (lane < p.split) {
+      const FloatPair ms = handoff_load_pair(w + lane * 4);
+      sum = Sums{ms.a, ms.b, handoff_load(w + lane * 4 + 2)};
+    }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) sum.join(Sums{__shfl_xor(sum.m, o), __shfl_xor(sum.s, o), __shfl_xor(sum.a, o)});
     if (top > 0) {
       // No key below the largest of the parts' last ones is among the row's.
       const uint64_t* keys = p.keys + (size_t)m * p.split * top;
-      const uint64_t from = wave_max_key(lane < p.split ? keys[(size_t)lane * top + top - 1] : 0);
+      const uint64_t from = wave_max_key(lane < p.split ? handoff_load(&keys[(size_t)lane * top + top - 1]) : 0);
       if (tid < kWaves) count[tid] = 0;
       if (tid < top) best[tid] = 0;
       __syncthreads();
-      for (int i = tid; i < p.split * top; i += kThreads)
-        if (keys[i] >= from && keys[i] != 0) list[0][atomicAdd(&count[0], 1)] = keys[i];  // any order: places go by keys
+      for (int i = tid; i < p.split * top; i += kThreads) {
+        const uint64_t key = handoff_load(&keys[i]);
+        if (key >= from && key != 0) list[0][atomicAdd(&count[0], 1)] = key;  // any order: places go by keys
+      }
       __syncthreads();
       rank_lists();
       __syncthreads();

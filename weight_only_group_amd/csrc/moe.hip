@@ -6,6 +6,7 @@
 // product is s (sum_k x q - z sum_k x): codes go to the matrix cores as they are,
 // the scale and zero point are applied to the sums.
 #include "gemv_common.h"
+#include "handoff.h"
 #include "layer.h"
 #include "mfma.h"
 
@@ -43,7 +44,7 @@ __device__ void route_top(const RouteArgs& a, int t, int lane) {
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = lane * PER + i;
-    key[i] = e < a.E ? float_order(__hip_atomic_load(&l[e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) : 0;
+    key[i] = e < a.E ? float_order(handoff_load(&l[e])) : 0;
   }
   auto value = [](uint32_t k) {
     return __builtin_bit_cast(float, k == 0xFFFFFFFFu ? 0x7FC00000u : (k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
@@ -118,18 +119,9 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs a) {
 #pragma unroll
     for (int w = 0; w < kRouteWaves; ++w) s += part[w][row][col];
     if (t0 + row < a.T && (int)blockIdx.x * 16 + col < a.E)
-      __hip_atomic_store(&a.logits[(size_t)(t0 + row) * a.E + blockIdx.x * 16 + col], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      handoff_store(&a.logits[(size_t)(t0 + row) * a.E + blockIdx.x * 16 + col], s);
   }
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-  __syncthreads();
-  if (tid == 0) {
-    const uint32_t ticket = __hip_atomic_fetch_add(&a.counters[blockIdx.y], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-    s_last = ticket == gridDim.x - 1;
-    if (s_last) __hip_atomic_store(&a.counters[blockIdx.y], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  __syncthreads();
-  if (!s_last) return;
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+  if (!handoff_last(&a.counters[blockIdx.y], gridDim.x, &s_last)) return;
   for (int i = t0 + wave; i < min(t0 + 16, a.T); i += kRouteWaves) {
     if (a.E <= 64) route_top<1>(a, i, lane);
     else if (a.E <= 128) route_top<2>(a, i, lane);
