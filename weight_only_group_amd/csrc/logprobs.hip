@@ -9,6 +9,8 @@
 // index in the lower half, so that keys differ, and larger keys come first. A wave
 // keeps the largest key that each lane has seen: the top-th largest of those is no
 // larger than the wave's top-th key, and few keys reach it. They go to a list.
+#include <algorithm>
+
 #include "handoff.h"
 #include "layer.h"
 
@@ -17,12 +19,15 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 256, kWaves = kThreads / 64;
-constexpr int kPer = 16;                // logits per thread and step
-constexpr int kStep = kThreads * kPer;  // logits per block and step
-constexpr int kList = 1024;             // keys a wave's list holds
+constexpr int kPerBytes = 64;  // of logits per thread and step
+constexpr int kList = 1024;    // keys a wave's list holds
 constexpr int kMaxSplit = 64;
+constexpr int kMaxKeys = 512;  // keys of a block's waves before their last selection
 
-template <LogitType TYPE> constexpr int kSize = TYPE == LogitType::kFp32 ? 4 : 2;
+constexpr int logit_size(LogitType t) { return t == LogitType::kFp32 ? 4 : 2; }
+// Leading bits of a logit's order that differ between values of the type; the
+// others are 1 below zero (the order is the complement there) and 0 above.
+constexpr int order_bits(LogitType t) { return t == LogitType::kFp32 ? 32 : t == LogitType::kBf16 ? 16 : 19; }
 
 template <LogitType TYPE>
 __device__ __forceinline__ float load_logit(const char* row, long long i) {
@@ -34,6 +39,10 @@ __device__ __forceinline__ float load_logit(const char* row, long long i) {
 __device__ __forceinline__ uint32_t float_order(float l) {
   const uint32_t b = __builtin_bit_cast(uint32_t, l + 0.0f);
   return l != l ? 0xFFFFFFFFu : (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float order_float(uint32_t order) {  // of an order that is no NaN's; -inf for 0
+  const uint32_t b = order & 0x80000000u ? order & 0x7FFFFFFFu : ~order;
+  return order == 0 ? -INFINITY : __builtin_bit_cast(float, b);
 }
 __device__ __forceinline__ uint64_t make_key(float l, uint32_t index) { return (uint64_t)float_order(l) << 32 | (uint32_t)~index; }
 __device__ __forceinline__ int key_index(uint64_t k) { return (int)~(uint32_t)k; }
@@ -47,54 +56,51 @@ __device__ __forceinline__ uint64_t wave_max_key(uint64_t v) {
   return v;
 }
 
-// The k-th largest of N keys per lane of a wave (0: none; 0 where there are fewer
-// than k), bit by bit: the order first, then, only among keys of that order, the index.
-template <int N>
-__device__ uint64_t kth_key(const uint64_t (&key)[N], int k) {
+// The k-th largest of a wave's keys (0: none; 0 where there are fewer than k), bit by
+// bit: the order first, then, only among keys of that order, the index. `count(f)`
+// says for how many keys f holds.
+template <int BITS, typename COUNT>
+__device__ __forceinline__ uint64_t kth_key(COUNT count, int k) {
   uint32_t hi = 0;
-  int above = 0;  // keys of a larger order
-  for (int b = 31; b >= 0; --b) {
+#pragma unroll 1
+  for (int b = 31; b >= 32 - BITS; --b) {
     const uint32_t t = hi | 1u << b;
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) n += __builtin_popcountll(__ballot((uint32_t)(key[i] >> 32) >= t));
-    if (n >= k) hi = t;
+    if (count([=](uint64_t x) { return (uint32_t)(x >> 32) >= t; }) >= k) hi = t;
   }
   if (hi == 0) return 0;
-  int same = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    above += __builtin_popcountll(__ballot((uint32_t)(key[i] >> 32) > hi));
-    same += __builtin_popcountll(__ballot((uint32_t)(key[i] >> 32) == hi));
-  }
+  if (BITS < 32 && !(hi & 0x80000000u)) hi |= (1u << (32 - BITS) % 32) - 1;
+  const int above = count([=](uint64_t x) { return (uint32_t)(x >> 32) > hi; });
   uint32_t lo = 0;
-  if (above + same > k) {
+  if (count([=](uint64_t x) { return (uint32_t)(x >> 32) >= hi; }) > k) {
+#pragma unroll 1
     for (int b = 31; b >= 0; --b) {
       const uint32_t t = lo | 1u << b;
-      int n = above;
-#pragma unroll
-      for (int i = 0; i < N; ++i) n += __builtin_popcountll(__ballot((uint32_t)(key[i] >> 32) == hi && (uint32_t)key[i] >= t));
-      if (n >= k) lo = t;
+      if (above + count([=](uint64_t x) { return (uint32_t)(x >> 32) == hi && (uint32_t)x >= t; }) >= k) lo = t;
     }
   }
   return (uint64_t)hi << 32 | lo;
 }
 
-// Reduces a wave's list of n <= kList keys to its k largest; returns the smallest of them.
-__device__ uint64_t shrink_list(uint64_t* list, int& n, int k, int lane) {
-  uint64_t key[kList / 64];
-#pragma unroll
-  for (int i = 0; i < kList / 64; ++i) key[i] = i * 64 + lane < n ? list[i * 64 + lane] : 0;
-  const uint64_t least = kth_key(key, k);
+// Reduces a wave's list of n keys, k <= n <= kList, to its k largest; returns the
+// smallest of them. Rare (rows that rise along the vocabulary): the list is read
+// from LDS again and again rather than kept in registers.
+template <int BITS>
+__device__ __forceinline__ uint64_t shrink_list(uint64_t* list, int n, int k, int lane) {
+  const uint64_t least = kth_key<BITS>(
+      [=](auto f) {
+        int c = 0;
+        for (int i = 0; i < n; i += 64) c += __builtin_popcountll(__ballot(i + lane < n && f(list[i + lane])));
+        return c;
+      },
+      k);
   int at = 0;
-#pragma unroll
-  for (int i = 0; i < kList / 64; ++i) {
-    const bool keep = key[i] != 0 && key[i] >= least;
-    const uint64_t hits = __ballot(keep);
-    if (keep) list[at + __builtin_popcountll(hits & ((1ull << lane) - 1))] = key[i];
+#pragma unroll 1
+  for (int i = 0; i < n; i += 64) {
+    const uint64_t key = i + lane < n ? list[i + lane] : 0;
+    const uint64_t hits = __ballot(key >= least);
+    if (key >= least) list[at + __builtin_popcountll(hits & ((1ull << lane) - 1))] = key;
     at += __builtin_popcountll(hits);
   }
-  n = at;
   return least;
 }
 
@@ -123,13 +129,13 @@ struct LogprobKernelArgs {
 // joins them. Bound: HBM, each logit is read once (a row that is not finite again,
 // per alternative).
 template <LogitType TYPE>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobKernelArgs p) {
-  constexpr int SIZE = kSize<TYPE>, VEC = 16 / SIZE, LOADS = kPer / VEC;
-  __shared__ uint64_t list[kWaves][kList];
-  __shared__ uint64_t best[kMaxTop];
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(LogprobKernelArgs p) {
+  constexpr int SIZE = logit_size(TYPE), VEC = 16 / SIZE, PER = kPerBytes / SIZE, STEP = kThreads * PER, BITS = order_bits(TYPE);
+  constexpr int LOADS = PER / VEC;
+  __shared__ __attribute__((aligned(16))) uint64_t list[kWaves][kList];
+  __shared__ uint64_t best[kMaxTop], first_least, wave_least[kWaves];
   __shared__ float wsum[kWaves][3];
-  __shared__ int count[kWaves];
-  __shared__ int s_last;
+  __shared__ int s_count, s_last;
   const LogprobArgs& a = p.l;
   const int m = blockIdx.x / p.split, part = blockIdx.x - m * p.split;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), top = a.top;
@@ -168,22 +174,24 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobKernelArgs p)
   };
 
   Sums sum = {-INFINITY, 0, 0};
-  uint64_t lane_best = 0, least = 0;  // the largest key of this lane; keys below `least` are out
+  uint64_t lane_best = 0;      // the largest key of this lane
+  uint64_t least = 0;          // keys below it are out
+  float least_logit = -INFINITY;
   int listed = 0;
-  const long long begin = (long long)part * p.steps * kStep, end = min(begin + (long long)p.steps * kStep, places);
+  const long long begin = (long long)part * p.steps * STEP, end = min(begin + (long long)p.steps * STEP, places);
   if (begin < end) load(begin);
-  for (long long first = begin; first < end; first += kStep) {
-    float l[kPer];
+  for (long long first = begin; first < end; first += STEP) {
+    float l[PER];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
       const uint32_t v = raw[i / VEC][i % VEC / (4 / SIZE)];
       if constexpr (SIZE == 4) l[i] = __builtin_bit_cast(float, v);
       else l[i] = bits_to_float<TYPE == LogitType::kBf16>((uint16_t)(v >> (16 * (i & 1))));
     }
-    if (first + kStep < end) load(first + kStep);
+    if (first + STEP < end) load(first + STEP);
     float lm = l[0];
 #pragma unroll
-    for (int i = 1; i < kPer; ++i) lm = fmaxf(lm, l[i]);
+    for (int i = 1; i < PER; ++i) lm = fmaxf(lm, l[i]);
     const float n = fmaxf(sum.m, lm), off = n == -INFINITY ? 0.f : n;
     if (n > sum.m) {
       const float d = fmaxf((sum.m - off) * kLog2e, -1e30f), f = __builtin_amdgcn_exp2f(d);
@@ -192,40 +200,66 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobKernelArgs p)
       sum.m = n;
     }
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
       const float d = (l[i] - off) * kLog2e, e = __builtin_amdgcn_exp2f(d);
       sum.s += e;
       sum.a += e * fmaxf(d, -1e30f);  // 0 for a logit of -inf
     }
-    if (top > 0) {
-      // Index of place `first + ((i / VEC) * kThreads + tid) * VEC + i % VEC`.
-      auto index = [&](int i) { return (int)(first - pad + ((long long)(i / VEC) * kThreads + tid) * VEC + i % VEC); };
-      const uint32_t least_order = (uint32_t)(least >> 32), lm_order = float_order(lm);
-      const uint64_t hot = __ballot(lm_order >= least_order);
-      if (hot) {
-        if (lm_order > (uint32_t)(lane_best >> 32)) {
+    if (top == 0) continue;
+    const uint64_t hot = __ballot(lm >= least_logit);
+    if (hot != 0 || first == begin) {
+      // Index of a thread's i-th logit of the step.
+      const int base = (int)(first - pad) + tid * VEC;
+      auto index = [&](int i) { return base + (i / VEC) * (kThreads * VEC) + i % VEC; };
+      if (float_order(lm) > (uint32_t)(lane_best >> 32)) {
+        int at = PER;
 #pragma unroll
-          for (int i = kPer - 1; i >= 0; --i)
-            if (l[i] == lm && (unsigned)index(i) < (unsigned)a.V) lane_best = make_key(lm, index(i));
+        for (int i = PER - 1; i >= 0; --i) at = l[i] == lm ? i : at;
+        // (places outside the row hold -inf: with a maximum of -inf the first one inside counts)
+        while (at < PER && (unsigned)index(at) >= (unsigned)a.V) ++at;
+        if (at < PER) lane_best = make_key(lm, index(at));
+      }
+      if (first == begin) {
+        // The bound that holds at first: the top-th of the threads' largest keys, found by one wave.
+        list[0][tid] = lane_best;
+        __syncthreads();
+        if (wave == 0) {
+          uint64_t key[kWaves];
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) key[w] = list[0][w * 64 + lane];
+          least = kth_key<BITS>(
+              [&](auto f) {
+                int c = 0;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) c += __builtin_popcountll(__ballot(f(key[w])));
+                return c;
+              },
+              top);
+          if (lane == 0) first_least = least;
         }
-        if (least == 0 || __builtin_popcountll(hot) > 8) {
-          const uint64_t one[1] = {lane_best};
-          const uint64_t t = kth_key(one, top);
+        __syncthreads();
+        least = first_least;
+      } else if (least == 0 || __builtin_popcountll(hot) > 8) {
+        const uint64_t t = kth_key<BITS>([&](auto f) { return (int)__builtin_popcountll(__ballot(f(lane_best))); }, top);
+        least = t > least ? t : least;
+      }
+      least_logit = order_float((uint32_t)(least >> 32));
+#pragma unroll
+      for (int g = 0; g < PER; g += 8) {
+        if (listed > kList - 8 * 64) {
+          const uint64_t t = shrink_list<BITS>(list[wave], listed, top, lane);
+          listed = top;
           least = t > least ? t : least;
-        }
-        if (listed > kList / 2) {
-          const uint64_t t = shrink_list(list[wave], listed, top, lane);
-          least = t > least ? t : least;
+          least_logit = order_float((uint32_t)(least >> 32));
         }
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
+        for (int i = g; i < g + 8; ++i) {
+          if (!__any(l[i] >= least_logit)) continue;
           const uint64_t key = make_key(l[i], index(i));
           const bool in = key >= least && (unsigned)index(i) < (unsigned)a.V;
           const uint64_t hits = __ballot(in);
-          if (hits) {
-            if (in) list[wave][listed + __builtin_popcountll(hits & ((1ull << lane) - 1))] = key;
-            listed += __builtin_popcountll(hits);
-          }
+          if (in) list[wave][listed + __builtin_popcountll(hits & ((1ull << lane) - 1))] = key;
+          listed += __builtin_popcountll(hits);
         }
       }
     }
@@ -234,31 +268,48 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobKernelArgs p)
   // The block's sums and alternatives.
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) sum.join(Sums{__shfl_xor(sum.m, o), __shfl_xor(sum.s, o), __shfl_xor(sum.a, o)});
-  if (listed > kList / kWaves / 2) shrink_list(list[wave], listed, top, lane);
+  if (listed > kMaxKeys / kWaves) {
+    const uint64_t t = shrink_list<BITS>(list[wave], listed, top, lane);
+    listed = top;
+    least = t > least ? t : least;
+  }
   if (lane == 0) {
     wsum[wave][0] = sum.m;
     wsum[wave][1] = sum.s;
     wsum[wave][2] = sum.a;
-    count[wave] = listed;
+    wave_least[wave] = least;
   }
   if (tid < top) best[tid] = 0;
+  if (tid == 0) s_count = 0;
+  // Of the waves' keys those that reach the largest bound; a key's place is the number of larger ones.
+  uint64_t mine[kMaxKeys / kWaves / 64];
+#pragma unroll
+  for (int i = 0; i < kMaxKeys / kWaves / 64; ++i) mine[i] = i * 64 + lane < listed ? list[wave][i * 64 + lane] : 0;
   __syncthreads();
+  uint64_t* keys = &list[0][0];
+  auto gather = [&](uint64_t key, uint64_t from) {
+    if (key >= from && key != 0) keys[atomicAdd(&s_count, 1)] = key;  // in any order: places go by keys
+  };
+  auto rank_keys = [&]() {
+    const int n = s_count;
+    for (int i = tid; i < n; i += kThreads) {
+      const uint64_t key = keys[i];
+      int rank = 0;
+#pragma unroll 8
+      for (int y = 0; y < n; ++y) rank += keys[y] > key;
+      if (rank < top) best[rank] = key;
+    }
+  };
   sum = Sums{wsum[0][0], wsum[0][1], wsum[0][2]};
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) sum.join(Sums{wsum[w][0], wsum[w][1], wsum[w][2]});
-  // A key's place is the number of larger ones.
-  auto rank_lists = [&]() {
-    for (int w = 0; w < kWaves; ++w)
-      for (int i = tid; i < count[w]; i += kThreads) {
-        const uint64_t key = list[w][i];
-        int rank = 0;
-        for (int x = 0; x < kWaves; ++x)
-          for (int y = 0; y < count[x]; ++y) rank += list[x][y] > key;
-        if (rank < top) best[rank] = key;
-      }
-  };
   if (top > 0) {
-    rank_lists();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) least = wave_least[w] > least ? wave_least[w] : least;
+#pragma unroll
+    for (int i = 0; i < kMaxKeys / kWaves / 64; ++i) gather(mine[i], least);
+    __syncthreads();
+    rank_keys();
     __syncthreads();
   }
   if (p.split > 1) {
@@ -279,17 +330,14 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobKernelArgs p)
     for (int o = 32; o > 0; o >>= 1) sum.join(Sums{__shfl_xor(sum.m, o), __shfl_xor(sum.s, o), __shfl_xor(sum.a, o)});
     if (top > 0) {
       // No key below the largest of the parts' last ones is among the row's.
-      const uint64_t* keys = p.keys + (size_t)m * p.split * top;
-      const uint64_t from = wave_max_key(lane < p.split ? handoff_load(&keys[(size_t)lane * top + top - 1]) : 0);
-      if (tid < kWaves) count[tid] = 0;
+      const uint64_t* parts = p.keys + (size_t)m * p.split * top;
+      const uint64_t from = wave_max_key(lane < p.split ? handoff_load(&parts[(size_t)lane * top + top - 1]) : 0);
+      if (tid == 0) s_count = 0;
       if (tid < top) best[tid] = 0;
       __syncthreads();
-      for (int i = tid; i < p.split * top; i += kThreads) {
-        const uint64_t key = handoff_load(&keys[i]);
-        if (key >= from && key != 0) list[0][atomicAdd(&count[0], 1)] = key;  // any order: places go by keys
-      }
+      for (int i = tid; i < p.split * top; i += kThreads) gather(handoff_load(&parts[i]), from);
       __syncthreads();
-      rank_lists();
+      rank_keys();
       __syncthreads();
     }
   }
@@ -331,12 +379,13 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobKernelArgs p)
 struct LogprobPlan {
   int split, steps;
 };
-LogprobPlan logprob_plan(int M, int V, int top, DeviceTopo topo) {
-  // Blocks enough for four per CU, a step each at least; the joining block's list holds all parts' keys.
-  const long long places = (long long)V + 7, most = (places + kStep - 1) / kStep;
+LogprobPlan logprob_plan(int M, int V, int top, LogitType type, DeviceTopo topo) {
+  // Blocks enough for four per CU, a step each at least; the joining block's lists hold all parts' keys.
+  const int step = kThreads * kPerBytes / logit_size(type);
+  const long long places = (long long)V + 16 / logit_size(type) - 1, most = (places + step - 1) / step;
   long long split = 4ll * topo.cus / M;
   if (split > kMaxSplit) split = kMaxSplit;
-  if (top > 0 && split > kList / top) split = kList / top;
+  if (top > 0 && split > kWaves * kList / top) split = kWaves * kList / top;
   if (split > most) split = most;
   if (split < 1 || M > kGemvMaxStrips) split = 1;
   const long long steps = (most + split - 1) / split;
@@ -346,12 +395,16 @@ LogprobPlan logprob_plan(int M, int V, int top, DeviceTopo topo) {
 }  // namespace
 
 size_t logprobs_workspace(int M, int V, int top) {
-  const LogprobPlan p = logprob_plan(M, V, top, device_topology());
-  return p.split > 1 ? kWorkspaceHeader + (size_t)M * p.split * (16 + 8 * (size_t)top) : 0;
+  size_t need = 0;
+  for (LogitType type : {LogitType::kFp16, LogitType::kBf16, LogitType::kFp32}) {
+    const LogprobPlan p = logprob_plan(M, V, top, type, device_topology());
+    if (p.split > 1) need = std::max(need, kWorkspaceHeader + (size_t)M * p.split * (16 + 8 * (size_t)top));
+  }
+  return need;
 }
 
 hipError_t launch_logprobs(const LogprobArgs& a, LogitType type, hipStream_t stream) {
-  const LogprobPlan plan = logprob_plan(a.M, a.V, a.top, device_topology());
+  const LogprobPlan plan = logprob_plan(a.M, a.V, a.top, type, device_topology());
   LogprobKernelArgs p = {a, plan.split, plan.steps, reinterpret_cast<uint32_t*>(a.workspace), nullptr, nullptr};
   if (plan.split > 1) {
     p.sums = reinterpret_cast<float*>(a.workspace + kWorkspaceHeader);
