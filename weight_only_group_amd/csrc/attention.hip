@@ -9,6 +9,7 @@
 // tile at a time (a chunk).
 #include <type_traits>
 
+#include "fixed_div.h"
 #include "handoff.h"
 #include "layer.h"
 #include "mfma.h"
@@ -40,19 +41,6 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int max_q, int max_kv, DeviceTopo top
   if (p.split > kMaxSplit) p.split = kMaxSplit;
   if (p.split < 1 || p.tiles > (size_t)kGemvMaxStrips) p.split = 1;
   return p;
-}
-
-// Division of 0 <= n < 2^31 by a fixed divisor: n mul >> shift, with mul = ceil(2^shift / d)
-// and shift = 31 + ceil(log2 d) (the excess of mul stays below one part in n).
-struct FixedDiv {
-  uint32_t mul;
-  int shift;
-  __device__ __forceinline__ int operator()(int n) const { return (int)((uint64_t)(uint32_t)n * mul >> shift); }
-};
-FixedDiv fixed_div(int d) {
-  int l = 0;
-  while ((1ll << l) < d) ++l;
-  return {(uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d), 31 + l};
 }
 
 struct AttnKernelArgs {

@@ -132,6 +132,8 @@ qmm_status qmm_moe(const uint16_t* x, int T, int H, int I, int E, int top_k, con
   // The kernels address one expert's plane and scales with 32-bit byte offsets.
   if ((unsigned long long)H * 2 * I * (bits == 3 ? 2 : bits) / 8 >= (1ull << 32))
     return fail(QMM_ERR_SHAPE, "one expert's plane of H=%d by 2I=%d must be smaller than 4 GiB", H, 2 * I);
+  if ((unsigned long long)T * top_k * I * 4 >= (1ull << 32))
+    return fail(QMM_ERR_SHAPE, "T=%d, top_k=%d and I=%d: the intermediate must be smaller than 4 GiB", T, top_k, I);
   if (T == 0) return ok();
   if (!x || !ids || !weights || !y) return fail(QMM_ERR_NULL, "a required pointer is NULL");
   st = check_experts(gate_up, "gate_up", bits);

@@ -5,6 +5,7 @@
 // An assignment is a (token, choice) pair, t * top_k + j. A group's part of a
 // product is s (sum_k x q - z sum_k x): codes go to the matrix cores as they are,
 // the scale and zero point are applied to the sums.
+#include "fixed_div.h"
 #include "gemv_common.h"
 #include "handoff.h"
 #include "layer.h"
@@ -184,43 +185,89 @@ __device__ __forceinline__ int operand_place(int k) {
   else return (k & 16) | ((k & 4) << 1) | ((k & 3) << 1) | ((k >> 3) & 1);
 }
 
-// Words of one plane for strip columns c0..c0 + 15: word (r, c0 + n) at base[r * stride].
-struct PlaneColumn {
-  const uint32_t *hi, *lo;
-  int stride;
+// One expert's weight (K x N) as its kernels address it: byte offsets are 32-bit,
+// a lane's part of them fixed, a unit's part uniform.
+template <int BITS> struct ExpertView {
+  __amdgpu_buffer_rsrc_t hi, lo, scales, zeros;
+  int N, rows, rows_lo, stride;  // word rows per plane, words per row step
+  int strips;
 };
 template <int BITS>
-__device__ __forceinline__ PlaneColumn plane_column(const ExpertPlanes& w, int e, int K, int N, int strips, int col) {
-  constexpr int HB = BITS == 3 ? 2 : BITS;
-  const int rows = K * HB / 32;
-  PlaneColumn p;
-  p.stride = plane_row_stride(N, strips);
-  p.hi = w.qw + (size_t)e * rows * N + plane_col(col, rows, strips);
-  p.lo = BITS == 3 ? w.qlo + (size_t)e * (K / 32) * N + plane_col(col, K / 32, strips) : nullptr;
-  return p;
+__device__ __forceinline__ ExpertView<BITS> expert_view(const ExpertPlanes& w, int e, int K, int N, int groups, int strips) {
+  ExpertView<BITS> v;
+  v.N = N;
+  v.rows = K * (BITS == 3 ? 2 : BITS) / 32;
+  v.rows_lo = K / 32;
+  v.stride = plane_row_stride(N, strips);
+  v.strips = strips;
+  const size_t plane = (size_t)v.rows * N, plane_lo = (size_t)v.rows_lo * N, params = (size_t)groups * N;
+  v.hi = make_rsrc(w.qw + e * plane, plane * 4);
+  v.lo = BITS == 3 ? make_rsrc(w.qlo + e * plane_lo, plane_lo * 4) : v.hi;
+  v.scales = make_rsrc(w.scales + e * params, params * 2);
+  v.zeros = make_rsrc(w.zeros + e * params, params * 2);
+  return v;
 }
 
-// A chunk: four units (32 k each) of one column strip.
+// A chunk: four units (32 k each) of one column strip, and the scale and zero point
+// of lane group j's unit for this lane's column. A wave keeps a run of chunks in
+// registers (16 words a lane) and asks for a chunk's successor as it has used it.
 constexpr int kUnits = 4;
-template <int BITS> struct ChunkWords { uint32_t w[kUnits][Bits<BITS>::NW]; };
+template <int BITS> constexpr int kRun = 4 / Bits<BITS>::NW;
+template <int BITS> struct Chunk {
+  uint32_t w[kUnits][Bits<BITS>::NW];
+  uint16_t scale, zero;
+};
 
+// Chunk c of column col; units past the last repeat it.
 template <int BITS>
-__device__ __forceinline__ void load_chunk(ChunkWords<BITS>& c, const PlaneColumn& p, int u0, int units, int j) {
+__device__ __forceinline__ void load_chunk(Chunk<BITS>& r, const ExpertView<BITS>& v, int col, int c, int units, FixedDiv by_upg, int j) {
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
-    const int u = min(u0 + i, units - 1);
+    const uint32_t u = (uint32_t)min(c * kUnits + i, units - 1);
 #pragma unroll
     for (int x = 0; x < Bits<BITS>::NW; ++x) {
-      const uint32_t* base = BITS == 3 && x == 1 ? p.lo : p.hi;
-      c.w[i][x] = __builtin_nontemporal_load(base + (uint32_t)(u * unit_rows<BITS>(x) + lane_row<BITS>(j, x)) * (uint32_t)p.stride);
+      const bool low = BITS == 3 && x == 1;
+      const uint32_t lane = 4u * (plane_col(col, low ? v.rows_lo : v.rows, v.strips) + (uint32_t)lane_row<BITS>(j, x) * (uint32_t)v.stride);
+      r.w[i][x] = __builtin_amdgcn_raw_buffer_load_b32(low ? v.lo : v.hi, lane, u * (uint32_t)(4 * unit_rows<BITS>(x)) * (uint32_t)v.stride,
+                                                       kNonTemporal);
     }
   }
+  const uint32_t at = 2u * ((uint32_t)by_upg(min(c * kUnits + j, units - 1)) * (uint32_t)v.N + (uint32_t)col);
+  r.scale = __builtin_amdgcn_raw_buffer_load_b16(v.scales, at, 0, 0);
+  r.zero = __builtin_amdgcn_raw_buffer_load_b16(v.zeros, at, 0, 0);
 }
 
-// Scale (low half) and zero point of lane group j's unit of the chunk, for this lane's column.
-__device__ __forceinline__ uint32_t load_group(const ExpertPlanes& w, size_t expert_groups, int N, int col, int u, int upg) {
-  const size_t at = (expert_groups + (uint32_t)u / (uint32_t)upg) * N + col;
-  return (uint32_t)w.scales[at] | (uint32_t)w.zeros[at] << 16;
+// total += a (16 rows) @ dequantize(chunk) for COLS strips' chunks. BF: of the
+// operands; SBF: of the scales and zero points.
+template <int BITS, bool BF, bool SBF, int COLS>
+__device__ __forceinline__ void chunk_product(f32x4 (&total)[COLS], const u32x4 (&a)[kUnits], const Chunk<BITS>* const (&w)[COLS], int c,
+                                              int units, int upg, FixedDiv by_upg, int j, int n) {
+  constexpr uint32_t kOne = BF ? 0x3F803F80u : 0x3C003C00u;
+  constexpr float kUp = BF ? 1.f : 16777216.f;
+  f32x4 acc[COLS] = {}, as = {};
+  int in_group = c * kUnits - by_upg(c * kUnits) * upg;
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    if (c * kUnits + i < units) {
+      as = mfma16<BF>(a[i], u32x4{kOne, kOne, kOne, kOne}, as);
+#pragma unroll
+      for (int v = 0; v < COLS; ++v)
+        acc[v] = mfma16<BF>(a[i], codes8<BITS, BF>(w[v]->w[i][0], w[v]->w[i][Bits<BITS>::NW - 1], j), acc[v]);
+    }
+    // The end of a group or of the chunk: scale and zero point, from the lane group that holds the unit's.
+    if (++in_group == upg || i == kUnits - 1) {
+      in_group = 0;
+#pragma unroll
+      for (int v = 0; v < COLS; ++v) {
+        const uint32_t sz = __shfl((uint32_t)w[v]->scale | (uint32_t)w[v]->zero << 16, 16 * i + n);
+        const float sc = bits_to_float<SBF>((uint16_t)sz), z = bits_to_float<SBF>((uint16_t)(sz >> 16)) + kCodeOffset<BITS, BF>;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) total[v][r] += sc * (acc[v][r] * kUp - z * as[r]);
+        acc[v] = f32x4{};
+      }
+      as = f32x4{};
+    }
+  }
 }
 
 // ---- gate and up products --------------------------------------------------------------
@@ -238,116 +285,72 @@ struct Slots {
 
 struct MoeKernelArgs {
   MoeArgs a;
+  FixedDiv by_upg_h, by_upg_i, by_top_k;  // 32-row units per group of both products; choices per token
   Slots slots;
   uint16_t* h;  // (assignments, 2, I) bf16: high and low parts, each unit in operand order
   int strips;
 };
 
-// Row tiles of NT * 16 assignments from `base` on: partial sums of a wave.
-template <int BITS, bool BF, int NT>
+// The 16 assignments from `base` on.
+template <int BITS, bool BF>
 __device__ __forceinline__ void gate_up_rows(const MoeKernelArgs& p, int e, int strip, const uint16_t* list, int base, int rows,
-                                             float (*sums)[2][16 * NT][17]) {
+                                             float (*sums)[2][16][17]) {
   const MoeArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 15, j = lane >> 4;
-  const int units = a.H / 32, upg = a.gs_h / 32, chunks = (units + kUnits - 1) / kUnits, N = 2 * a.I;
-  const PlaneColumn col[2] = {plane_column<BITS>(a.gate_up, e, a.H, N, p.strips, strip * 16 + n),
-                              plane_column<BITS>(a.gate_up, e, a.H, N, p.strips, a.I + strip * 16 + n)};
-  const size_t groups = (size_t)e * (units / upg);
-  const uint16_t* x[NT];
+  const int units = a.H / 32, upg = a.gs_h / 32, chunks = (units + kUnits - 1) / kUnits;
+  const ExpertView<BITS> view = expert_view<BITS>(a.gate_up, e, a.H, 2 * a.I, p.by_upg_h(units), p.strips);
+  Chunk<BITS> run[kRun<BITS>][2];
+  auto load_words = [&](int k, int c) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int at = list[min(base + 16 * t + n, rows - 1)];
-    x[t] = a.x + (size_t)(at / a.top_k) * a.H + x_first<BITS>(j);
-  }
-  struct Stage {
-    ChunkWords<BITS> w[2];
-    uint32_t sz[2];
-    u32x4 x[NT][kUnits];
-  } st[2];
-  auto load = [&](Stage& s, int c) {
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      load_chunk<BITS>(s.w[v], col[v], c * kUnits, units, j);
-      s.sz[v] = load_group(a.gate_up, groups, N, v * a.I + strip * 16 + n, min(c * kUnits + j, units - 1), upg);
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const uint16_t* src = x[t] + min(c * kUnits + i, units - 1) * 32;
-        if constexpr (BITS == 2 || BITS == 3) {
-          const u32x2 lo = *reinterpret_cast<const u32x2*>(src), hi = *reinterpret_cast<const u32x2*>(src + 8);
-          s.x[t][i] = u32x4{lo.x, lo.y, hi.x, hi.y};
-        } else {
-          s.x[t][i] = *reinterpret_cast<const u32x4*>(src);
-        }
-      }
+    for (int v = 0; v < 2; ++v) load_chunk<BITS>(run[k][v], view, v * a.I + strip * 16 + n, min(c, chunks - 1), units, p.by_upg_h, j);
   };
-  f32x4 total[2][NT] = {};
-  constexpr uint32_t kOne = BF ? 0x3F803F80u : 0x3C003C00u;
-  auto compute = [&](const Stage& s, int c) {
-    f32x4 acc[2][NT] = {}, xs[NT] = {};
-    int in_group = (c * kUnits) % upg;
+#pragma unroll
+  for (int k = 0; k < kRun<BITS>; ++k)
+    if (wave + k * kGateWaves < chunks) load_words(k, wave + k * kGateWaves);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, (size_t)a.T * a.H * 2);
+  const uint32_t x = 2u * ((uint32_t)p.by_top_k(list[min(base + n, rows - 1)]) * (uint32_t)a.H + (uint32_t)x_first<BITS>(j));
+  u32x4 xv[2][kUnits];
+  auto load_x = [&](int c, u32x4 (&to)[kUnits]) {
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      if (c * kUnits + i < units) {
-        u32x4 xa[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          xa[t] = x_operand<BITS>(s.x[t][i]);
-          xs[t] = mfma16<BF>(xa[t], u32x4{kOne, kOne, kOne, kOne}, xs[t]);
-        }
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const u32x4 b = codes8<BITS, BF>(s.w[v].w[i][0], s.w[v].w[i][Bits<BITS>::NW - 1], j);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) acc[v][t] = mfma16<BF>(xa[t], b, acc[v][t]);
-        }
-      }
-      // The end of a group or of the chunk: scale and zero point, from the lane group that holds the unit's.
-      if (++in_group == upg || i == kUnits - 1) {
-        if (in_group == upg) in_group = 0;
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const uint32_t sz = __shfl(s.sz[v], 16 * i + n);
-          const float sc = bits_to_float<BF>((uint16_t)sz), z = bits_to_float<BF>((uint16_t)(sz >> 16)) + kCodeOffset<BITS, BF>;
-          constexpr float kUp = BF ? 1.f : 16777216.f;
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) total[v][t][r] += sc * (acc[v][t][r] * kUp - z * xs[t][r]);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) acc[v][t] = f32x4{};
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) xs[t] = f32x4{};
+      const uint32_t u = (uint32_t)min(c * kUnits + i, units - 1) * 64u;
+      if constexpr (BITS == 2 || BITS == 3) {
+        const u32x2 lo = __builtin_amdgcn_raw_buffer_load_b64(xr, x, u, 0), hi = __builtin_amdgcn_raw_buffer_load_b64(xr, x + 16, u, 0);
+        to[i] = u32x4{lo.x, lo.y, hi.x, hi.y};
+      } else {
+        to[i] = __builtin_amdgcn_raw_buffer_load_b128(xr, x, u, 0);
       }
     }
   };
+  f32x4 total[2] = {};
   int c = wave;
-  if (c < chunks) load(st[0], c);
+  if (c < chunks) load_x(c, xv[0]);
   while (c < chunks) {
-    if (c + kGateWaves < chunks) load(st[1], c + kGateWaves);
-    compute(st[0], c);
-    c += kGateWaves;
-    if (c >= chunks) break;
-    if (c + kGateWaves < chunks) load(st[0], c + kGateWaves);
-    compute(st[1], c);
-    c += kGateWaves;
+#pragma unroll
+    for (int k = 0; k < kRun<BITS>; ++k) {
+      if (c >= chunks) break;
+      load_x(c + kGateWaves, xv[(k + 1) & 1]);
+      u32x4 xa[kUnits];
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) xa[i] = x_operand<BITS>(xv[k & 1][i]);
+      const Chunk<BITS>* const w[2] = {&run[k][0], &run[k][1]};
+      chunk_product<BITS, BF, BF, 2>(total, xa, w, c, units, upg, p.by_upg_h, j, n);
+      __builtin_amdgcn_sched_barrier(0);
+      if (c + kRun<BITS> * kGateWaves < chunks) load_words(k, c + kRun<BITS> * kGateWaves);
+      __builtin_amdgcn_sched_barrier(0);
+      c += kGateWaves;
+    }
   }
 #pragma unroll
   for (int v = 0; v < 2; ++v)
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) sums[wave][v][16 * t + 4 * j + r][n] = total[v][t][r];
+    for (int r = 0; r < 4; ++r) sums[wave][v][4 * j + r][n] = total[v][r];
   __syncthreads();
-  for (int o = tid; o < 16 * NT * 16; o += 64 * kGateWaves) {
-    const int row = o >> 4, cc = o & 15;
+  if (tid < 256 && base + (tid >> 4) < rows) {
+    const int row = tid >> 4, cc = tid & 15;
     float g = 0, u = 0;
 #pragma unroll
     for (int w = 0; w < kGateWaves; ++w) g += sums[w][0][row][cc], u += sums[w][1][row][cc];
-    if (base + row >= rows) continue;
     const float h = g / (1 + __expf(-g)) * u;
     const bf16 hi = (bf16)h;
     const float rest = h - (float)hi;
@@ -362,10 +365,10 @@ __device__ __forceinline__ void gate_up_rows(const MoeKernelArgs& p, int e, int 
 }
 
 // Block: 16 gate and the 16 up columns of one expert, its waves over H. Bound: HBM,
-// an expert's words are read once for all its tokens (twice from 33 on).
+// an expert's words are read once per 16 of its tokens (from the L2 after the first).
 template <int BITS, bool BF>
-__global__ void __launch_bounds__(64 * kGateWaves, 2) gate_up_kernel(MoeKernelArgs p) {
-  __shared__ float sums[kGateWaves][2][32][17];
+__global__ void __launch_bounds__(64 * kGateWaves, 4) gate_up_kernel(MoeKernelArgs p) {
+  __shared__ float sums[kGateWaves][2][16][17];
   __shared__ uint16_t list[kMoeTokens];
   __shared__ int counts[2][kGateWaves];
   const MoeArgs& a = p.a;
@@ -373,50 +376,48 @@ __global__ void __launch_bounds__(64 * kGateWaves, 2) gate_up_kernel(MoeKernelAr
   const int assignments = a.T * a.top_k;
   const bool by_assignment = p.slots.count == assignments;
   const int e = by_assignment ? a.ids[slot] : slot;
-  // The expert's assignments, in order; a slot whose expert came before is not in use.
-  bool dup = false;
   int rows = 0;
-  for (int base = 0; base < assignments; base += 64 * kGateWaves) {
-    const int i = base + tid;
-    const bool mine = i < assignments && a.ids[i] == e;
-    dup |= mine && by_assignment && i < slot;
-    const uint64_t hits = __ballot(mine);
-    int* count = counts[(base / (64 * kGateWaves)) & 1];
-    if (lane == 0) count[wave] = __builtin_popcountll(hits);
+  if (a.T == 1 && by_assignment) {  // one token: every choice an expert of its own
+    rows = e >= 0 && e < a.E;
+    if (tid == 0) list[0] = (uint16_t)slot;
     __syncthreads();
-    int before = rows;
-    for (int w = 0; w < kGateWaves; ++w) {
-      if (w < wave) before += count[w];
-      rows += count[w];
+  } else {
+    // The expert's assignments, in order; a slot whose expert came before is not in use.
+    bool dup = false;
+    for (int base = 0; base < assignments; base += 64 * kGateWaves) {
+      const int i = base + tid;
+      const bool mine = i < assignments && a.ids[i] == e;
+      dup |= mine && by_assignment && i < slot;
+      const uint64_t hits = __ballot(mine);
+      int* count = counts[(base / (64 * kGateWaves)) & 1];
+      if (lane == 0) count[wave] = __builtin_popcountll(hits);
+      __syncthreads();
+      int before = rows;
+      for (int w = 0; w < kGateWaves; ++w) {
+        if (w < wave) before += count[w];
+        rows += count[w];
+      }
+      before += __builtin_popcountll(hits & ((1ull << lane) - 1));
+      if (mine && before < a.T) list[before] = (uint16_t)i;
     }
-    before += __builtin_popcountll(hits & ((1ull << lane) - 1));
-    if (mine && before < a.T) list[before] = (uint16_t)i;
-  }
-  const bool unused = __syncthreads_or(dup) || e < 0 || e >= a.E || rows == 0;
-  rows = unused ? 0 : min(rows, a.T);
-  if (strip == 0) {
-    if (tid == 0) p.slots.rows[slot] = rows;
-    if (tid < rows) p.slots.list[(size_t)slot * a.T + tid] = list[tid];
-  }
-  for (int base = 0; base < rows;) {
-    if (rows - base <= 16) {
-      gate_up_rows<BITS, BF, 1>(p, e, strip, list, base, rows, reinterpret_cast<float (*)[2][16][17]>(sums));
-      base += 16;
-    } else {
-      gate_up_rows<BITS, BF, 2>(p, e, strip, list, base, rows, sums);
-      base += 32;
+    const bool unused = __syncthreads_or(dup) || e < 0 || e >= a.E;
+    rows = unused ? 0 : min(rows, a.T);
+    if (strip == 0) {
+      if (tid == 0) p.slots.rows[slot] = rows;
+      if (tid < rows) p.slots.list[(size_t)slot * a.T + tid] = list[tid];
     }
   }
+  for (int base = 0; base < rows; base += 16) gate_up_rows<BITS, BF>(p, e, strip, list, base, rows, sums);
 }
 
 // ---- down products and the weighted sum ---------------------------------------------------
 
 constexpr int kDownWaves = 16;
 
-// Block: 16 columns of y for all tokens; its waves take (expert, chunk) pairs in
-// turn and add to sums of their own, which meet in wave order. A row tile is 8
-// assignments: the high parts of h in rows 0-7, the low parts in rows 8-15.
-// Bound: HBM, as above.
+// Block: 16 columns of y for all tokens; its waves take (expert, run of chunks)
+// pairs in turn, the next one's words on the way as the current ones are used, and
+// add to sums of their own, which meet in wave order. A row tile is 8 assignments: the high
+// parts of h in rows 0-7, the low parts in rows 8-15. Bound: HBM, as above.
 template <int BITS, bool BF>
 __global__ void __launch_bounds__(64 * kDownWaves) down_kernel(MoeKernelArgs p) {
   extern __shared__ float sums[];  // (waves, T, 16)
@@ -425,8 +426,9 @@ __global__ void __launch_bounds__(64 * kDownWaves) down_kernel(MoeKernelArgs p) 
   const MoeArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 15, j = lane >> 4;
   const int strip = blockIdx.x, units = a.I / 32, upg = a.gs_i / 32, chunks = (units + kUnits - 1) / kUnits;
-  const bool by_assignment = p.slots.count == a.T * a.top_k;
-  if (wave == 0) {
+  const int runs = (chunks + kRun<BITS> - 1) / kRun<BITS>;
+  const bool by_assignment = p.slots.count == a.T * a.top_k, one = a.T == 1 && by_assignment;
+  if (wave == 0 && !one) {
     int total = 0;
     for (int base = 0; base < p.slots.count; base += 64) {
       const bool in_use = base + lane < p.slots.count && p.slots.rows[base + lane] > 0;
@@ -439,48 +441,68 @@ __global__ void __launch_bounds__(64 * kDownWaves) down_kernel(MoeKernelArgs p) 
   float* mine = sums + (size_t)wave * a.T * 16;
   for (int i = lane; i < a.T * 16; i += 64) mine[i] = 0;
   __syncthreads();
-  const int items = s_used * chunks;
-  for (int it = wave; it < items; it += kDownWaves) {
-    const int slot = used[it / chunks], c = it % chunks;
-    const int e = by_assignment ? a.ids[slot] : slot, rows = p.slots.rows[slot];
-    const uint16_t* list = p.slots.list + (size_t)slot * a.T;
-    ChunkWords<BITS> w;
-    load_chunk<BITS>(w, plane_column<BITS>(a.down, e, a.I, a.H, p.strips, strip * 16 + n), c * kUnits, units, j);
-    const uint32_t sz = load_group(a.down, (size_t)e * (units / upg), a.H, strip * 16 + n, min(c * kUnits + j, units - 1), upg);
-    for (int base = 0; base < rows; base += 8) {
-      const int at = list[min(base + (n & 7), rows - 1)];
-      const uint16_t* h = p.h + ((size_t)at * 2 + (n >> 3)) * a.I + j * 8;
-      u32x4 ha[kUnits];
+  // Items: runs of one expert's chunks. The row of a slot's first tile and its
+  // expert's view change with the item only.
+  const int items = (one ? a.top_k : s_used) * runs;
+  struct Item {
+    int slot, e, c0;
+  };
+  auto item = [&](int it) {
+    const int nth = it / runs;
+    Item x;
+    x.slot = one ? nth : __builtin_amdgcn_readfirstlane(used[nth]);
+    x.e = by_assignment ? a.ids[x.slot] : x.slot;
+    x.c0 = (it - nth * runs) * kRun<BITS>;
+    if (x.e < 0 || x.e >= a.E) x.e = -1;  // one token's choice of no expert
+    return x;
+  };
+  Chunk<BITS> run[kRun<BITS>];
+  auto load = [&](int k, const Item& x) {
+    load_chunk<BITS>(run[k], expert_view<BITS>(a.down, max(x.e, 0), a.I, a.H, p.by_upg_i(units), p.strips), strip * 16 + n,
+                     min(x.c0 + k, chunks - 1), units, p.by_upg_i, j);
+  };
+  const __amdgpu_buffer_rsrc_t hr = make_rsrc(p.h, (size_t)a.T * a.top_k * a.I * 4);
+  int it = wave;
+  if (it < items) {
+    Item x = item(it);
 #pragma unroll
-      for (int i = 0; i < kUnits; ++i) ha[i] = *reinterpret_cast<const u32x4*>(h + min(c * kUnits + i, units - 1) * 32);
-      f32x4 total = {}, acc = {}, hs = {};
-      int in_group = (c * kUnits) % upg;
+    for (int k = 0; k < kRun<BITS>; ++k) load(k, x);
+    for (;;) {
+      const Item next = item(min(it + kDownWaves, items - 1));
+      const int rows = x.e < 0 ? 0 : one ? 1 : p.slots.rows[x.slot];
+      const uint16_t* list = p.slots.list + (size_t)x.slot * a.T;
 #pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        if (c * kUnits + i < units) {
-          hs = mfma16<true>(ha[i], u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}, hs);
-          acc = mfma16<true>(ha[i], codes8<BITS, true>(w.w[i][0], w.w[i][Bits<BITS>::NW - 1], j), acc);
-        }
-        if (++in_group == upg || i == kUnits - 1) {
-          if (in_group == upg) in_group = 0;
-          const uint32_t g = __shfl(sz, 16 * i + n);
-          const float sc = bits_to_float<BF>((uint16_t)g), z = bits_to_float<BF>((uint16_t)(g >> 16)) + kCodeOffset<BITS, true>;
+      for (int k = 0; k < kRun<BITS>; ++k) {
+        const int c = x.c0 + k;
+        if (c < chunks) {
+          for (int base = 0; base < rows; base += 8) {
+            const int at = one ? x.slot : list[min(base + (n & 7), rows - 1)];
+            const uint32_t h = 2u * (((uint32_t)at * 2u + (uint32_t)(n >> 3)) * (uint32_t)a.I + (uint32_t)j * 8u);
+            u32x4 ha[kUnits];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) total[r] += sc * (acc[r] - z * hs[r]);
-          acc = hs = f32x4{};
-        }
-      }
-      // Rows 4 j + r of lanes j < 2 are the high parts, of lanes j + 2 the low ones.
+            for (int i = 0; i < kUnits; ++i) ha[i] = __builtin_amdgcn_raw_buffer_load_b128(hr, h, (uint32_t)min(c * kUnits + i, units - 1) * 64u, 0);
+            f32x4 total[1] = {};
+            const Chunk<BITS>* const w[1] = {&run[k]};
+            chunk_product<BITS, true, BF, 1>(total, ha, w, c, units, upg, p.by_upg_i, j, n);
+            // Rows 4 j + r of lanes j < 2 are the high parts, of lanes j + 2 the low ones.
 #pragma unroll
-      for (int r = 0; r < 4; ++r) total[r] += __shfl_xor(total[r], 32);
-      if (j < 2) {
+            for (int r = 0; r < 4; ++r) total[0][r] += __shfl_xor(total[0][r], 32);
+            if (j < 2) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (base + 4 * j + r < rows) {
-            const int as = list[base + 4 * j + r];
-            mine[(as / a.top_k) * 16 + n] += a.weights[as] * total[r];
+              for (int r = 0; r < 4; ++r)
+                if (base + 4 * j + r < rows) {
+                  const int as = one ? x.slot : list[base + 4 * j + r];
+                  mine[p.by_top_k(as) * 16 + n] += a.weights[as] * total[0][r];
+                }
+            }
           }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        load(k, next);
+        __builtin_amdgcn_sched_barrier(0);
       }
+      if ((it += kDownWaves) >= items) break;
+      x = next;
     }
   }
   __syncthreads();
@@ -516,7 +538,7 @@ size_t moe_workspace(int T, int H, int I, int E, int top_k) {
 }
 
 hipError_t launch_moe(const MoeArgs& a, int bits, bool bf16, bool strips, hipStream_t stream) {
-  MoeKernelArgs p = {a, {}, nullptr, strips};
+  MoeKernelArgs p = {a, fixed_div(a.gs_h / 32), fixed_div(a.gs_i / 32), fixed_div(a.top_k), {}, nullptr, strips};
   p.slots.count = cmin(a.E, a.T * a.top_k);
   char* at = a.workspace + kWorkspaceHeader;
   p.h = reinterpret_cast<uint16_t*>(at);
