@@ -11,7 +11,8 @@ namespace qmm {
 constexpr size_t kWorkspaceHeader = size_t(kGemvMaxStrips) * 4;
 
 // ---- mixture of experts ---------------------------------------------------------
-constexpr int kMoeTokens = 64, kMoeExperts = 1024;  // most of a call
+constexpr int kMoeTokens = 64, kMoeExperts = 1024, kMoeTopK = 16;  // most of a call
+constexpr int kMoeAssignments = kMoeTokens * kMoeTopK;
 struct RouteArgs {
   const uint16_t* x;
   const uint16_t* router;

@@ -29,7 +29,7 @@ qmm_status check_workspace(const void* workspace, size_t bytes, size_t need) {
 
 // ---- mixture of experts ---------------------------------------------------------
 
-static_assert(QMM_MOE_MAX_TOKENS == qmm::kMoeTokens && QMM_MOE_MAX_EXPERTS == qmm::kMoeExperts &&
+static_assert(QMM_MOE_MAX_TOKENS == qmm::kMoeTokens && QMM_MOE_MAX_EXPERTS == qmm::kMoeExperts && QMM_MOE_MAX_TOP_K == qmm::kMoeTopK &&
               QMM_LOGPROBS_MAX_TOP == qmm::kMaxTop, "limits of the kernels");
 
 qmm_status check_route_shape(int T, int H, int E) {

@@ -136,13 +136,25 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs a) {
 // Eight codes of lane group j, in decode8's element order, as 16-bit numbers:
 // fp16: q 2^-24 (a subnormal half, exact); bf16: 128 + q for up to 4 bits (the
 // code in the mantissa's low bits), q for 8 bits (exact in 8 significant bits).
+//
+// The masks are made once and kept in vector registers, the bits put around the code
+// (nothing for fp16) in a scalar one, so that inserting is one operation.
+template <int BITS, bool BF> struct CodeMasks {
+  uint32_t code, low, around;
+  __device__ __forceinline__ CodeMasks()
+      : code(BITS == 4 ? 0x000F000Fu : BITS == 3 ? 0x00060006u : BITS == 2 ? 0x00030003u : 0x00010001u), low(0x00010001u),
+        around(BF ? 0x43004300u : 0u) {
+    if (BITS != 8) asm("" : "+v"(code));
+    if (BITS == 3) asm("" : "+v"(low));
+    if (BF && BITS != 8) asm("" : "+s"(around));
+  }
+};
 template <int BITS, bool BF>
-__device__ __forceinline__ u32x4 codes8(uint32_t w0, uint32_t w1, int j) {
+__device__ __forceinline__ u32x4 codes8(uint32_t w0, uint32_t w1, int j, const CodeMasks<BITS, BF>& m) {
   u32x4 b;
-  constexpr uint32_t kOr = BF ? 0x43004300u : 0u;
   if constexpr (BITS == 4) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) b[p] = ((w0 >> (4 * p)) & 0x000F000Fu) | kOr;
+    for (int p = 0; p < 4; ++p) b[p] = ((w0 >> (4 * p)) & m.code) | m.around;
   } else if constexpr (BITS == 8) {
     if constexpr (BF) {
 #pragma unroll
@@ -160,17 +172,17 @@ __device__ __forceinline__ u32x4 codes8(uint32_t w0, uint32_t w1, int j) {
   } else if constexpr (BITS == 2) {
     const uint32_t t = w0 >> (8 * (j & 1));
 #pragma unroll
-    for (int p = 0; p < 4; ++p) b[p] = ((t >> (2 * p)) & 0x00030003u) | kOr;
+    for (int p = 0; p < 4; ++p) b[p] = ((t >> (2 * p)) & m.code) | m.around;
   } else if constexpr (BITS == 3) {
     const uint32_t h = w0 >> (8 * (j & 1));
     const uint32_t t = w1 >> (16 * (j >> 1) + 4 * (j & 1));
     const uint32_t l = __builtin_amdgcn_perm(0u, t, 0x0C010C00u);  // bytes (0, -, 1, -) of t
 #pragma unroll
-    for (int p = 0; p < 4; ++p) b[p] = (((h >> (2 * p)) & 0x00030003u) << 1) | ((l >> p) & 0x00010001u) | kOr;
+    for (int p = 0; p < 4; ++p) b[p] = ((l >> p) & m.low) | (((p == 0 ? h << 1 : h >> (2 * p - 1)) & m.code) | m.around);
   } else {
     const uint32_t t = (w0 >> (8 * j)) & 0xFFu, both = t | (t << 12);  // slots p and p + 4 sixteen bits apart
 #pragma unroll
-    for (int p = 0; p < 4; ++p) b[p] = ((both >> p) & 0x00010001u) | kOr;
+    for (int p = 0; p < 4; ++p) b[p] = ((both >> p) & m.code) | m.around;
   }
   return b;
 }
@@ -237,36 +249,54 @@ __device__ __forceinline__ void load_chunk(Chunk<BITS>& r, const ExpertView<BITS
   r.zero = __builtin_amdgcn_raw_buffer_load_b16(v.zeros, at, 0, 0);
 }
 
-// total += a (16 rows) @ dequantize(chunk) for COLS strips' chunks. BF: of the
-// operands; SBF: of the scales and zero points.
-template <int BITS, bool BF, bool SBF, int COLS>
+// Where groups end within a chunk: every kUnits or kUnits / 2 units, known at
+// compile time, or anywhere.
+enum Groups { kWholeChunk, kHalfChunk, kAnywhere };
+inline Groups groups_of(int upg) { return upg % kUnits == 0 ? kWholeChunk : upg == kUnits / 2 ? kHalfChunk : kAnywhere; }
+
+// total += a (16 rows) @ dequantize(chunk) for COLS strips' chunks; units past the
+// last must be 0 in a. BF: of the operands; SBF: of the scales and zero points.
+template <int BITS, bool BF, bool SBF, int COLS, Groups G>
 __device__ __forceinline__ void chunk_product(f32x4 (&total)[COLS], const u32x4 (&a)[kUnits], const Chunk<BITS>* const (&w)[COLS], int c,
-                                              int units, int upg, FixedDiv by_upg, int j, int n) {
+                                              int upg, FixedDiv by_upg, int j, int n, const CodeMasks<BITS, BF>& masks) {
   constexpr uint32_t kOne = BF ? 0x3F803F80u : 0x3C003C00u;
   constexpr float kUp = BF ? 1.f : 16777216.f;
   f32x4 acc[COLS] = {}, as = {};
-  int in_group = c * kUnits - by_upg(c * kUnits) * upg;
+  int in_group = G == kAnywhere ? c * kUnits - by_upg(c * kUnits) * upg : 0;
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
-    if (c * kUnits + i < units) {
-      as = mfma16<BF>(a[i], u32x4{kOne, kOne, kOne, kOne}, as);
+    as = mfma16<BF>(a[i], u32x4{kOne, kOne, kOne, kOne}, as);
 #pragma unroll
-      for (int v = 0; v < COLS; ++v)
-        acc[v] = mfma16<BF>(a[i], codes8<BITS, BF>(w[v]->w[i][0], w[v]->w[i][Bits<BITS>::NW - 1], j), acc[v]);
-    }
-    // The end of a group or of the chunk: scale and zero point, from the lane group that holds the unit's.
-    if (++in_group == upg || i == kUnits - 1) {
+    for (int v = 0; v < COLS; ++v)
+      acc[v] = mfma16<BF>(a[i], codes8<BITS, BF>(w[v]->w[i][0], w[v]->w[i][Bits<BITS>::NW - 1], j, masks), acc[v]);
+    // The end of a group or of the chunk: scale and zero point, from the lane group that
+    // holds the unit's (its own where the chunk is of one group).
+    if (G == kWholeChunk ? i == kUnits - 1 : G == kHalfChunk ? i % 2 == 1 : ++in_group == upg || i == kUnits - 1) {
       in_group = 0;
 #pragma unroll
       for (int v = 0; v < COLS; ++v) {
-        const uint32_t sz = __shfl((uint32_t)w[v]->scale | (uint32_t)w[v]->zero << 16, 16 * i + n);
-        const float sc = bits_to_float<SBF>((uint16_t)sz), z = bits_to_float<SBF>((uint16_t)(sz >> 16)) + kCodeOffset<BITS, BF>;
+        float sc = bits_to_float<SBF>(w[v]->scale), z = bits_to_float<SBF>(w[v]->zero);
+        if constexpr (G != kWholeChunk) {
+          const uint32_t sz = __shfl((uint32_t)w[v]->scale | (uint32_t)w[v]->zero << 16, 16 * i + n);
+          sc = bits_to_float<SBF>((uint16_t)sz);
+          z = bits_to_float<SBF>((uint16_t)(sz >> 16));
+        }
+        z += kCodeOffset<BITS, BF>;
 #pragma unroll
         for (int r = 0; r < 4; ++r) total[v][r] += sc * (acc[v][r] * kUp - z * as[r]);
         acc[v] = f32x4{};
       }
       as = f32x4{};
     }
+  }
+}
+
+// Zeroes a chunk's operands of units past the last.
+__device__ __forceinline__ void cut_units(u32x4 (&a)[kUnits], int c, int units) {
+  if ((c + 1) * kUnits > units) {
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+      if (c * kUnits + i >= units) a[i] = u32x4{0, 0, 0, 0};
   }
 }
 
@@ -292,7 +322,7 @@ struct MoeKernelArgs {
 };
 
 // The 16 assignments from `base` on.
-template <int BITS, bool BF>
+template <int BITS, bool BF, Groups G>
 __device__ __forceinline__ void gate_up_rows(const MoeKernelArgs& p, int e, int strip, const uint16_t* list, int base, int rows,
                                              float (*sums)[2][16][17]) {
   const MoeArgs& a = p.a;
@@ -309,7 +339,7 @@ __device__ __forceinline__ void gate_up_rows(const MoeKernelArgs& p, int e, int 
     if (wave + k * kGateWaves < chunks) load_words(k, wave + k * kGateWaves);
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, (size_t)a.T * a.H * 2);
   const uint32_t x = 2u * ((uint32_t)p.by_top_k(list[min(base + n, rows - 1)]) * (uint32_t)a.H + (uint32_t)x_first<BITS>(j));
-  u32x4 xv[2][kUnits];
+  u32x4 xv[kUnits];
   auto load_x = [&](int c, u32x4 (&to)[kUnits]) {
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
@@ -322,20 +352,22 @@ __device__ __forceinline__ void gate_up_rows(const MoeKernelArgs& p, int e, int 
       }
     }
   };
+  const CodeMasks<BITS, BF> masks;
   f32x4 total[2] = {};
   int c = wave;
-  if (c < chunks) load_x(c, xv[0]);
+  if (c < chunks) load_x(c, xv);
   while (c < chunks) {
 #pragma unroll
     for (int k = 0; k < kRun<BITS>; ++k) {
       if (c >= chunks) break;
-      load_x(c + kGateWaves, xv[(k + 1) & 1]);
       u32x4 xa[kUnits];
 #pragma unroll
-      for (int i = 0; i < kUnits; ++i) xa[i] = x_operand<BITS>(xv[k & 1][i]);
+      for (int i = 0; i < kUnits; ++i) xa[i] = x_operand<BITS>(xv[i]);
+      cut_units(xa, c, units);
       const Chunk<BITS>* const w[2] = {&run[k][0], &run[k][1]};
-      chunk_product<BITS, BF, BF, 2>(total, xa, w, c, units, upg, p.by_upg_h, j, n);
+      chunk_product<BITS, BF, BF, 2, G>(total, xa, w, c, upg, p.by_upg_h, j, n, masks);
       __builtin_amdgcn_sched_barrier(0);
+      load_x(c + kGateWaves, xv);
       if (c + kRun<BITS> * kGateWaves < chunks) load_words(k, c + kRun<BITS> * kGateWaves);
       __builtin_amdgcn_sched_barrier(0);
       c += kGateWaves;
@@ -366,7 +398,7 @@ __device__ __forceinline__ void gate_up_rows(const MoeKernelArgs& p, int e, int 
 
 // Block: 16 gate and the 16 up columns of one expert, its waves over H. Bound: HBM,
 // an expert's words are read once per 16 of its tokens (from the L2 after the first).
-template <int BITS, bool BF>
+template <int BITS, bool BF, Groups G>
 __global__ void __launch_bounds__(64 * kGateWaves, 4) gate_up_kernel(MoeKernelArgs p) {
   __shared__ float sums[kGateWaves][2][16][17];
   __shared__ uint16_t list[kMoeTokens];
@@ -379,7 +411,13 @@ __global__ void __launch_bounds__(64 * kGateWaves, 4) gate_up_kernel(MoeKernelAr
   int rows = 0;
   if (a.T == 1 && by_assignment) {  // one token: every choice an expert of its own
     rows = e >= 0 && e < a.E;
-    if (tid == 0) list[0] = (uint16_t)slot;
+    if (tid == 0) {
+      list[0] = (uint16_t)slot;
+      if (strip == 0) {
+        p.slots.rows[slot] = rows;
+        p.slots.list[slot] = (uint16_t)slot;
+      }
+    }
     __syncthreads();
   } else {
     // The expert's assignments, in order; a slot whose expert came before is not in use.
@@ -407,7 +445,7 @@ __global__ void __launch_bounds__(64 * kGateWaves, 4) gate_up_kernel(MoeKernelAr
       if (tid < rows) p.slots.list[(size_t)slot * a.T + tid] = list[tid];
     }
   }
-  for (int base = 0; base < rows; base += 16) gate_up_rows<BITS, BF>(p, e, strip, list, base, rows, sums);
+  for (int base = 0; base < rows; base += 16) gate_up_rows<BITS, BF, G>(p, e, strip, list, base, rows, sums);
 }
 
 // ---- down products and the weighted sum ---------------------------------------------------
@@ -418,92 +456,120 @@ constexpr int kDownWaves = 16;
 // pairs in turn, the next one's words on the way as the current ones are used, and
 // add to sums of their own, which meet in wave order. A row tile is 8 assignments: the high
 // parts of h in rows 0-7, the low parts in rows 8-15. Bound: HBM, as above.
-template <int BITS, bool BF>
+template <int BITS, bool BF, Groups G>
 __global__ void __launch_bounds__(64 * kDownWaves) down_kernel(MoeKernelArgs p) {
   extern __shared__ float sums[];  // (waves, T, 16)
-  __shared__ uint16_t used[kMoeExperts];
+  __shared__ uint16_t used_slot[kMoeExperts], used_expert[kMoeExperts], used_first[kMoeExperts + 1], list[kMoeAssignments];
+  __shared__ float weight[kMoeAssignments];
   __shared__ int s_used;
   const MoeArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 15, j = lane >> 4;
   const int strip = blockIdx.x, units = a.I / 32, upg = a.gs_i / 32, chunks = (units + kUnits - 1) / kUnits;
   const int runs = (chunks + kRun<BITS> - 1) / kRun<BITS>;
-  const bool by_assignment = p.slots.count == a.T * a.top_k, one = a.T == 1 && by_assignment;
-  if (wave == 0 && !one) {
-    int total = 0;
+  const bool by_assignment = p.slots.count == a.T * a.top_k;
+  // The slots in use, their experts and assignments (used_first[u] on in the list), all in LDS.
+  for (int i = tid; i < a.T * a.top_k; i += 64 * kDownWaves) weight[i] = a.weights[i];
+  if (wave == 0) {
+    int total = 0, first = 0;
     for (int base = 0; base < p.slots.count; base += 64) {
-      const bool in_use = base + lane < p.slots.count && p.slots.rows[base + lane] > 0;
-      const uint64_t hits = __ballot(in_use);
-      if (in_use) used[total + __builtin_popcountll(hits & ((1ull << lane) - 1))] = (uint16_t)(base + lane);
+      const int slot = base + lane;
+      const bool in = slot < p.slots.count;
+      const int e = !in ? -1 : by_assignment ? a.ids[slot] : slot;
+      int rows = !in ? 0 : p.slots.rows[slot], upto = rows;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int before = __shfl_up(upto, o);
+        if (lane >= o) upto += before;
+      }
+      const uint64_t hits = __ballot(rows > 0);
+      if (rows > 0) {
+        const int u = total + __builtin_popcountll(hits & ((1ull << lane) - 1));
+        used_slot[u] = (uint16_t)slot;
+        used_expert[u] = (uint16_t)e;
+        used_first[u] = (uint16_t)(first + upto - rows);
+      }
       total += __builtin_popcountll(hits);
+      first += __shfl(upto, 63);
     }
-    if (lane == 0) s_used = total;
+    if (lane == 0) {
+      s_used = total;
+      used_first[total] = (uint16_t)first;
+    }
   }
   float* mine = sums + (size_t)wave * a.T * 16;
   for (int i = lane; i < a.T * 16; i += 64) mine[i] = 0;
   __syncthreads();
-  // Items: runs of one expert's chunks. The row of a slot's first tile and its
-  // expert's view change with the item only.
-  const int items = (one ? a.top_k : s_used) * runs;
+  for (int u = wave; u < s_used; u += kDownWaves) {
+    const int first = used_first[u];
+    if (lane < used_first[u + 1] - first) list[first + lane] = p.slots.list[(size_t)used_slot[u] * a.T + lane];
+  }
+  // Items: runs of one expert's chunks.
+  const int items = s_used * runs;
   struct Item {
-    int slot, e, c0;
+    int u, c0;
   };
   auto item = [&](int it) {
-    const int nth = it / runs;
-    Item x;
-    x.slot = one ? nth : __builtin_amdgcn_readfirstlane(used[nth]);
-    x.e = by_assignment ? a.ids[x.slot] : x.slot;
-    x.c0 = (it - nth * runs) * kRun<BITS>;
-    if (x.e < 0 || x.e >= a.E) x.e = -1;  // one token's choice of no expert
-    return x;
+    const int u = it / runs;
+    return Item{u, (it - u * runs) * kRun<BITS>};
   };
   Chunk<BITS> run[kRun<BITS>];
   auto load = [&](int k, const Item& x) {
-    load_chunk<BITS>(run[k], expert_view<BITS>(a.down, max(x.e, 0), a.I, a.H, p.by_upg_i(units), p.strips), strip * 16 + n,
+    const int e = __builtin_amdgcn_readfirstlane(used_expert[x.u]);
+    load_chunk<BITS>(run[k], expert_view<BITS>(a.down, e, a.I, a.H, p.by_upg_i(units), p.strips), strip * 16 + n,
                      min(x.c0 + k, chunks - 1), units, p.by_upg_i, j);
   };
-  const __amdgpu_buffer_rsrc_t hr = make_rsrc(p.h, (size_t)a.T * a.top_k * a.I * 4);
   int it = wave;
+  Item x = item(min(it, max(items - 1, 0)));
   if (it < items) {
-    Item x = item(it);
 #pragma unroll
     for (int k = 0; k < kRun<BITS>; ++k) load(k, x);
-    for (;;) {
-      const Item next = item(min(it + kDownWaves, items - 1));
-      const int rows = x.e < 0 ? 0 : one ? 1 : p.slots.rows[x.slot];
-      const uint16_t* list = p.slots.list + (size_t)x.slot * a.T;
+  }
+  __syncthreads();
+  const __amdgpu_buffer_rsrc_t hr = make_rsrc(p.h, (size_t)a.T * a.top_k * a.I * 4);
+  const CodeMasks<BITS, true> masks;
+  // h of chunk c for the 8 assignments from `at` on of an item.
+  auto load_h = [&](const Item& x, int base, int c, u32x4 (&h)[kUnits]) {
+    const int first = used_first[x.u], rows = used_first[x.u + 1] - first;
+    const uint32_t as = list[first + min(base + (n & 7), rows - 1)];
+    const uint32_t off = 2u * ((as * 2u + (uint32_t)(n >> 3)) * (uint32_t)a.I + (uint32_t)j * 8u);
 #pragma unroll
-      for (int k = 0; k < kRun<BITS>; ++k) {
-        const int c = x.c0 + k;
-        if (c < chunks) {
-          for (int base = 0; base < rows; base += 8) {
-            const int at = one ? x.slot : list[min(base + (n & 7), rows - 1)];
-            const uint32_t h = 2u * (((uint32_t)at * 2u + (uint32_t)(n >> 3)) * (uint32_t)a.I + (uint32_t)j * 8u);
-            u32x4 ha[kUnits];
+    for (int i = 0; i < kUnits; ++i) h[i] = __builtin_amdgcn_raw_buffer_load_b128(hr, off, (uint32_t)min(c * kUnits + i, units - 1) * 64u, 0);
+  };
+  u32x4 ha[kUnits];
+  if (it < items) load_h(x, 0, x.c0, ha);
+  for (; it < items; it += kDownWaves) {
+    const Item next = item(min(it + kDownWaves, items - 1));
+    const int first = used_first[x.u], rows = used_first[x.u + 1] - first;
 #pragma unroll
-            for (int i = 0; i < kUnits; ++i) ha[i] = __builtin_amdgcn_raw_buffer_load_b128(hr, h, (uint32_t)min(c * kUnits + i, units - 1) * 64u, 0);
-            f32x4 total[1] = {};
-            const Chunk<BITS>* const w[1] = {&run[k]};
-            chunk_product<BITS, true, BF, 1>(total, ha, w, c, units, upg, p.by_upg_i, j, n);
-            // Rows 4 j + r of lanes j < 2 are the high parts, of lanes j + 2 the low ones.
+    for (int k = 0; k < kRun<BITS>; ++k) {
+      const int c = x.c0 + k;
+      if (c < chunks) {
+        for (int base = 0; base < rows; base += 8) {
+          if (base > 0) load_h(x, base, c, ha);
+          cut_units(ha, c, units);
+          f32x4 total[1] = {};
+          const Chunk<BITS>* const w[1] = {&run[k]};
+          chunk_product<BITS, true, BF, 1, G>(total, ha, w, c, upg, p.by_upg_i, j, n, masks);
+          // Rows 4 j + r of lanes j < 2 are the high parts, of lanes j + 2 the low ones.
 #pragma unroll
-            for (int r = 0; r < 4; ++r) total[0][r] += __shfl_xor(total[0][r], 32);
-            if (j < 2) {
+          for (int r = 0; r < 4; ++r) total[0][r] += __shfl_xor(total[0][r], 32);
+          if (j < 2) {
 #pragma unroll
-              for (int r = 0; r < 4; ++r)
-                if (base + 4 * j + r < rows) {
-                  const int as = one ? x.slot : list[base + 4 * j + r];
-                  mine[p.by_top_k(as) * 16 + n] += a.weights[as] * total[0][r];
-                }
-            }
+            for (int r = 0; r < 4; ++r)
+              if (base + 4 * j + r < rows) {
+                const int as = list[first + base + 4 * j + r];
+                mine[p.by_top_k(as) * 16 + n] += weight[as] * total[0][r];
+              }
           }
         }
-        __builtin_amdgcn_sched_barrier(0);
-        load(k, next);
-        __builtin_amdgcn_sched_barrier(0);
       }
-      if ((it += kDownWaves) >= items) break;
-      x = next;
+      __builtin_amdgcn_sched_barrier(0);
+      if (k + 1 < kRun<BITS>) load_h(x, 0, min(c + 1, chunks - 1), ha);
+      else load_h(next, 0, next.c0, ha);
+      load(k, next);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    x = next;
   }
   __syncthreads();
   for (int i = tid; i < a.T * 16; i += 64 * kDownWaves) {
@@ -516,8 +582,24 @@ __global__ void __launch_bounds__(64 * kDownWaves) down_kernel(MoeKernelArgs p) 
 
 template <int BITS, bool BF>
 hipError_t launch_bits(const MoeKernelArgs& p, hipStream_t stream) {
-  gate_up_kernel<BITS, BF><<<dim3(p.a.I / 16, p.slots.count), 64 * kGateWaves, 0, stream>>>(p);
-  down_kernel<BITS, BF><<<p.a.H / 16, 64 * kDownWaves, (size_t)kDownWaves * p.a.T * 16 * 4, stream>>>(p);
+  const dim3 gate_grid(p.a.I / 16, p.slots.count), down_grid(p.a.H / 16);
+  const size_t lds = (size_t)kDownWaves * p.a.T * 16 * 4;
+  const auto run = [&](auto gate, auto down) {
+    gate<<<gate_grid, 64 * kGateWaves, 0, stream>>>(p);
+    down<<<down_grid, 64 * kDownWaves, lds, stream>>>(p);
+  };
+  const auto down_for = [&](auto gate) {
+    switch (groups_of(p.a.gs_i / 32)) {
+      case kWholeChunk: return run(gate, down_kernel<BITS, BF, kWholeChunk>);
+      case kHalfChunk: return run(gate, down_kernel<BITS, BF, kHalfChunk>);
+      default: return run(gate, down_kernel<BITS, BF, kAnywhere>);
+    }
+  };
+  switch (groups_of(p.a.gs_h / 32)) {
+    case kWholeChunk: down_for(gate_up_kernel<BITS, BF, kWholeChunk>); break;
+    case kHalfChunk: down_for(gate_up_kernel<BITS, BF, kHalfChunk>); break;
+    default: down_for(gate_up_kernel<BITS, BF, kAnywhere>); break;
+  }
   return hipGetLastError();
 }
 
