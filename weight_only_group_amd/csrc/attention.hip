@@ -57,12 +57,14 @@ struct ScoreRule {
   float scale;       // without a cap: factor; with one: 2 log2(e) scale / cap, of the exponential in tanh
   float cap;         // cap log2(e), or 0
   float slope;       // slope log2(e) of this lane's head
+  template <bool CAP, bool SLOPES>
+  __device__ __forceinline__ float score(float dot, int pos, int key) const {
+    // cap tanh(x) = cap - 2 cap / (1 + e^2x): cap at x = inf, -cap at -inf
+    const float s = CAP ? cap - 2 * cap * __builtin_amdgcn_rcpf(1 + __builtin_amdgcn_exp2f(dot * scale)) : dot * scale;
+    return SLOPES ? s - slope * fabsf((float)(pos - key)) : s;
+  }
   __device__ __forceinline__ float operator()(float dot, int pos, int key) const {
-    float s;
-    // cap tanh(x) = cap - 2 cap / (1 + e^2x): 1 at x = inf, -1 at -inf
-    if (cap > 0) s = cap - 2 * cap * __builtin_amdgcn_rcpf(1 + __builtin_amdgcn_exp2f(dot * scale));
-    else s = dot * scale;
-    return s - slope * fabsf((float)(pos - key));
+    return cap > 0 ? score<true, true>(dot, pos, key) : score<false, true>(dot, pos, key);
   }
 };
 
@@ -382,6 +384,315 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) attentio
     *reinterpret_cast<u32x2*>(dst + e) = u32x2{pack_pair<BF>(o[e] * inv, o[e + 1] * inv), pack_pair<BF>(o[e + 2] * inv, o[e + 3] * inv)};
 }
 
+// Sixteen bytes per lane from its own address to LDS, lane l's to lds_addr + 16 l
+// (lds_addr uniform). One asm block, as the compiler would make every later LDS read
+// wait for the builtin's; the wait before the barrier that publishes the tile is
+// explicit. No vector register is written; m0 is restored.
+__device__ __forceinline__ void load_to_lds(uint32_t lds_addr, const void* src) {
+  uint32_t saved;
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, off\n\ts_mov_b32 m0, %0"
+               : "=&s"(saved)
+               : "s"(lds_addr), "v"(src)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+// Transposed read: each 16 lanes' 8-byte pieces are four rows of sixteen 16-bit
+// values (four lanes a row); lane c of them gets column c of the four rows.
+__device__ __forceinline__ u32x2 read_transposed(const void* p) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
+}
+
+constexpr int kTileRows = 128;                                   // rows per block, 32 per wave
+template <int D> constexpr int kTileKeys = D == 256 ? 32 : 64;  // keys per step
+
+// Block: 128 rows of one key head, all their keys in steps that go through two LDS
+// buffers, loaded straight from the cache a step ahead. Bound: the matrix cores and,
+// above all with a cap, the exponentials (a quarter of the vector rate).
+//
+// As above K q^T is taken, whose result has a query per lane column: the softmax
+// needs one exchange between lanes, and its weights are the operand of V^T p^T as
+// they are, for the four neighbouring keys that a transposed LDS read of V gives.
+// The 16-byte pieces of an LDS row are reordered by the row (an exclusive or), so
+// that both the rows' reads and the transposed reads fall on distinct banks.
+template <bool BF, int D, bool CAP, bool SLOPES>
+__global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(AttnKernelArgs p) {
+  constexpr int BN = kTileKeys<D>, SUB = BN / 32, PIECES = D / 8, STEPS = D / 16, MT = D / 32;
+  constexpr int OWN = BN / kWaves, LOADS = OWN * D * 2 / 1024, PER_LOAD = 512 / D;  // keys a wave loads, in how many loads
+  constexpr int LDO = 36;
+  __shared__ __attribute__((aligned(16))) uint16_t kvs[2][2][BN * D];
+  __shared__ int range[2][kWaves];
+  static_assert(sizeof(kvs) >= kTileRows * LDO * 4, "the result passes through the same LDS");
+  const AttentionArgs& a = p.a;
+  const int per = 8 * p.rtiles, w8 = blockIdx.x % per;
+  const int rt = p.rtiles - 1 - w8 / 8, unit = blockIdx.x / per * 8 + w8 % 8;  // the longest rows of a causal mask first
+  if (unit >= a.B * a.Hkv) return;
+  const int hk = unit % a.Hkv, b = unit / a.Hkv;
+  const int q0 = min(max(a.q_starts[b], 0), a.T), q1 = min(max(a.q_starts[b + 1], q0), min(a.T, q0 + a.max_q));
+  const int kv = min(max(a.kv_lens[b], 0), a.max_kv);
+  if ((long long)rt * kTileRows >= (long long)(q1 - q0) * p.group) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 31, kg = lane >> 5;
+  const int r0 = rt * kTileRows + wave * 32;
+  const Row row = row_of(p, r0 + n, q0, q1, kv, hk);
+  // A negative scale turns the queries' signs instead: products are then in the scores' order.
+  ScoreRule rule = score_rule(a, row.head);
+  const uint32_t q_sign = rule.scale < 0 ? 0x80008000u : 0u;
+  rule.scale = fabsf(rule.scale);
+
+  // Keys that any row of the wave sees, and those that all see; the block's from the waves'.
+  int lo = row.lo < row.hi ? row.lo : INT32_MAX, hi = row.lo < row.hi ? row.hi : 0;
+  int all_lo = row.token < 0 ? 0 : row.lo, all_hi = row.token < 0 ? INT32_MAX : row.hi;  // rows past the last count as seeing all
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    lo = min(lo, __shfl_xor(lo, o));
+    hi = max(hi, __shfl_xor(hi, o));
+    all_lo = max(all_lo, __shfl_xor(all_lo, o));
+    all_hi = min(all_hi, __shfl_xor(all_hi, o));
+  }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
+  all_lo = __builtin_amdgcn_readfirstlane(all_lo);
+  all_hi = __builtin_amdgcn_readfirstlane(all_hi);
+  if (lane == 0) range[0][wave] = lo, range[1][wave] = hi;
+  __syncthreads();
+  int block_lo = INT32_MAX, block_hi = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) block_lo = min(block_lo, range[0][w]), block_hi = max(block_hi, range[1][w]);
+  block_lo = __builtin_amdgcn_readfirstlane(block_lo);
+  block_hi = __builtin_amdgcn_readfirstlane(block_hi);
+  const int t0 = block_lo < block_hi ? block_lo / BN : 0, t1 = block_lo < block_hi ? (block_hi + BN - 1) / BN : 0;
+
+  u32x4 q[STEPS];
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s)
+    q[s] = row.token < 0 ? u32x4{0, 0, 0, 0}
+                         : *reinterpret_cast<const u32x4*>(a.q + row.token * a.q_stride + (long long)row.head * D + s * 16 + kg * 8) ^ q_sign;
+
+  // Reordering of row r's pieces.
+  auto turn = [](int r) { return D == 64 ? ((r >> 1) & 1) << 2 | ((r >> 2) & 3) : (r & 3) << 2 | ((r >> 2) & 3); };
+  const int32_t* table = a.page_table + (long long)b * a.table_stride;
+  auto key_row = [&](int j) -> uint32_t {  // keys past those seen repeat the nearest
+    j = min(max(j, block_lo), block_hi - 1);
+    const int at = p.by_page(j);
+    const int page = min(max(table[at], 0), a.pages - 1);
+    return ((uint32_t)page * a.Hkv + hk) * a.page_size + (j - at * a.page_size);
+  };
+  auto own_rows = [&](int t) { return key_row(t * BN + wave * OWN + (lane & (OWN - 1))); };
+  auto load_tile = [&](int buf, uint32_t rows) {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int local = i * PER_LOAD + lane / PIECES;
+      const size_t at = (size_t)__shfl(rows, local) * D + ((lane % PIECES) ^ turn(wave * OWN + local)) * 8;
+      const uint32_t to = (uint32_t)(wave * OWN + i * PER_LOAD) * D * 2;
+      load_to_lds(lds_offset(kvs[buf][0]) + to, a.k_cache + at);
+      load_to_lds(lds_offset(kvs[buf][1]) + to, a.v_cache + at);
+    }
+  };
+  // Byte offsets of this lane's reads: keys' pieces per step, values' per 32 dimensions and four keys.
+  uint32_t k_at[STEPS], v_at[MT][2];
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) k_at[s] = n * D * 2 + ((2 * s + kg) ^ turn(n)) * 16;
+  {
+    const int i = (lane & 15) >> 2;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int key = 4 * kg + 8 * h + i, piece = 4 * m + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
+        v_at[m][h] = key * D * 2 + (piece ^ turn(key)) * 16 + (lane & 1) * 8;
+      }
+  }
+
+  f32x16 o[MT] = {};
+  float mx = -INFINITY, sum = 0;
+  bool any_bad = false;
+  uint32_t rows = 0;
+  if (t0 < t1) {
+    load_tile(t0 & 1, own_rows(t0));
+    rows = own_rows(t0 + 1);
+  }
+  for (int t = t0; t < t1; ++t) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (t + 1 < t1) {
+      load_tile((t + 1) & 1, rows);
+      rows = own_rows(t + 2);
+    }
+    const int key0 = t * BN;
+    if (key0 + BN <= lo || key0 >= hi) continue;  // nothing for this wave's rows
+    const char* ks = reinterpret_cast<const char*>(kvs[t & 1][0]);
+    const char* vs = reinterpret_cast<const char*>(kvs[t & 1][1]);
+    f32x16 st[SUB] = {};
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+        st[u] = mfma32<BF>(*reinterpret_cast<const u32x4*>(ks + k_at[s] + u * 32 * D * 2), q[s], st[u]);
+    const bool whole = key0 >= all_lo && key0 + BN <= all_hi;
+    auto key_of = [&](int u, int i) { return key0 + 32 * u + 8 * (i >> 2) + 4 * kg + (i & 3); };
+    auto sees = [&](int u, int i) { return key_of(u, i) >= row.lo && key_of(u, i) < row.hi; };
+    // The largest score of the row; without a distance bias that of the largest product.
+    float best = -INFINITY;
+    bool some = whole;
+    if (SLOPES) {
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st[u][i] = rule.template score<CAP, true>(st[u][i], row.pos, key_of(u, i));
+    }
+    if (whole) {
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) best = fmaxf(best, st[u][i]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          best = fmaxf(best, sees(u, i) ? st[u][i] : -INFINITY);
+          some |= sees(u, i);
+        }
+    }
+    if (!SLOPES) best = some ? rule.template score<CAP, false>(best, 0, 0) : -INFINITY;
+    best = fmaxf(best, __shfl_xor(best, 32));
+    // A row's maximum is left where it is while no weight passes 2^8: rescaling is rare.
+    if (__any(best > mx + 8)) {
+      const float m = best > mx + 8 ? best : mx;
+      const float f = mx == m ? 1.f : __builtin_amdgcn_exp2f(mx - m);
+      sum *= f;
+#pragma unroll
+      for (int m2 = 0; m2 < MT; ++m2) o[m2] *= f;
+      mx = m;
+    }
+    const float off = mx == -INFINITY ? 0.f : mx;
+    // Exponents: the scores less the maximum, in one multiply-add of the product (or, with a cap, of
+    // the reciprocal in the tanh).
+    if (SLOPES) {
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) st[u] -= off;
+    } else if (CAP) {
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          st[u][i] = fmaf(-2 * rule.cap, __builtin_amdgcn_rcpf(1 + __builtin_amdgcn_exp2f(st[u][i] * rule.scale)), rule.cap - off);
+    } else {
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st[u][i] = fmaf(st[u][i], rule.scale, -off);
+    }
+    if (!whole) {
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st[u][i] = sees(u, i) ? st[u][i] : -INFINITY;
+    }
+    u32x4 w[BN / 16];
+#pragma unroll
+    for (int g = 0; g < BN / 16; ++g)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int i = 8 * (g & 1) + 2 * x;
+        w[g][x] = pack_pair<BF>(__builtin_amdgcn_exp2f(st[g >> 1][i]), __builtin_amdgcn_exp2f(st[g >> 1][i + 1]));
+        sum = add_pair<BF>(w[g][x], sum);  // the rounded weights make the denominator too
+      }
+    auto add_values = [&](auto cut) {
+#pragma unroll
+      for (int g = 0; g < BN / 16; ++g)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const u32x2 x = read_transposed(vs + v_at[m][0] + g * 16 * D * 2), y = read_transposed(vs + v_at[m][1] + g * 16 * D * 2);
+          u32x4 v = {x[0], x[1], y[0], y[1]};
+          if constexpr (decltype(cut)::value) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] &= (not_finite<BF>(v[i]) ? 0u : 0xFFFFu) | (not_finite<BF>(v[i] >> 16) ? 0u : 0xFFFF0000u);
+          }
+          o[m] = mfma32<BF>(v, w[g], o[m]);
+        }
+    };
+    bool bad = false;
+    if (!whole) {
+      // A value that is not finite must not reach rows that do not see it: see the split kernel.
+#pragma unroll 4
+      for (int i = lane; i < BN * D / 8; i += 64) {
+        const u32x4 x = reinterpret_cast<const u32x4*>(vs)[i];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) bad |= (int)not_finite<BF>(x[y]) | (int)not_finite<BF>(x[y] >> 16);
+      }
+      bad = __any(bad);
+      any_bad |= bad;
+    }
+    if (__builtin_expect(bad, 0)) add_values(std::true_type{});
+    else add_values(std::false_type{});
+  }
+
+  // Results leave by LDS, 32 dimensions at a time, each wave for its own rows.
+  sum += __shfl_xor(sum, 32);
+  const float inv = row.lo < row.hi ? 1 / sum : 0.f;
+  __syncthreads();
+  float* so = reinterpret_cast<float*>(&kvs[0][0][0]) + wave * 32 * LDO;
+  const Row mine = row_of(p, r0 + (lane >> 1), q0, q1, kv, hk);
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      *reinterpret_cast<f32x4*>(so + n * LDO + 8 * g + 4 * kg) =
+          f32x4{o[m][4 * g] * inv, o[m][4 * g + 1] * inv, o[m][4 * g + 2] * inv, o[m][4 * g + 3] * inv};
+    if (any_bad) {
+      // Rare: the values left out above, to the rows that see them.
+      for (int t = t0; t < t1; ++t) {
+        const int key0 = t * BN;
+        if (key0 + BN <= lo || key0 >= hi || (key0 >= all_lo && key0 + BN <= all_hi)) continue;
+        const uint32_t here = key_row(key0 + (lane & (BN - 1)));
+        for (int key = 0; key < BN; ++key) {
+          const uint16_t* src = a.v_cache + (size_t)__shfl(here, key) * D + 32 * m;
+          if (key0 + key < row.lo || key0 + key >= row.hi) continue;
+          for (int d = kg; d < 32; d += 2)
+            if (not_finite<BF>(src[d])) so[n * LDO + d] += bits_to_float<BF>(src[d]);
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (mine.token >= 0) {
+      const float* src = so + (lane >> 1) * LDO + 16 * (lane & 1);
+      uint16_t* dst = a.out + ((long long)mine.token * a.Hq + mine.head) * D + 32 * m + 16 * (lane & 1);
+#pragma unroll
+      for (int e = 0; e < 16; e += 8)
+        *reinterpret_cast<u32x4*>(dst + e) = u32x4{pack_pair<BF>(src[e], src[e + 1]), pack_pair<BF>(src[e + 2], src[e + 3]),
+                                                   pack_pair<BF>(src[e + 4], src[e + 5]), pack_pair<BF>(src[e + 6], src[e + 7])};
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// Blocks of 128 rows where they are enough to fill most of the CUs, else tiles of 16
+// split over the keys.
+bool use_tiles(int B, int Hq, int Hkv, int max_q, DeviceTopo topo) {
+  const long long rows = (long long)max_q * (Hq / Hkv);
+  return rows > 64 && (long long)B * Hkv * ((rows + kTileRows - 1) / kTileRows) * 3 >= topo.cus;
+}
+
+template <bool BF, int D>
+hipError_t launch_tiles(const AttentionArgs& a, hipStream_t stream) {
+  const int group = a.Hq / a.Hkv, rtiles = (int)(((long long)a.max_q * group + kTileRows - 1) / kTileRows);
+  const AttnKernelArgs p = {a, fixed_div(a.page_size), fixed_div(group), group, rtiles, 1, nullptr, nullptr, nullptr};
+  const long long blocks = ((long long)a.B * a.Hkv + 7) / 8 * 8 * rtiles;
+  if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)blocks);
+  if (a.softcap > 0 && a.slopes) attention_tile_kernel<BF, D, true, true><<<grid, 64 * kWaves, 0, stream>>>(p);
+  else if (a.softcap > 0) attention_tile_kernel<BF, D, true, false><<<grid, 64 * kWaves, 0, stream>>>(p);
+  else if (a.slopes) attention_tile_kernel<BF, D, false, true><<<grid, 64 * kWaves, 0, stream>>>(p);
+  else attention_tile_kernel<BF, D, false, false><<<grid, 64 * kWaves, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
 template <bool BF, int D>
 hipError_t launch_split(const AttentionArgs& a, hipStream_t stream) {
   const AttnPlan plan = attn_plan(a.B, a.Hq, a.Hkv, a.max_q, a.max_kv, device_topology());
@@ -399,19 +710,25 @@ hipError_t launch_split(const AttentionArgs& a, hipStream_t stream) {
 }  // namespace
 
 size_t attention_workspace(int B, int T, int Hq, int Hkv, int D, int max_q, int max_kv) {
+  if (use_tiles(B, Hq, Hkv, max_q, device_topology())) return 0;
   const AttnPlan p = attn_plan(B, Hq, Hkv, max_q, max_kv, device_topology());
   return p.split > 1 ? kWorkspaceHeader + p.tiles * p.split * kRows * (D + 2) * sizeof(float) : 0;
 }
 
-hipError_t launch_attention(const AttentionArgs& a, bool bf16, hipStream_t stream) {
-  if (bf16) {
-    if (a.D == 64) return launch_split<true, 64>(a, stream);
-    if (a.D == 128) return launch_split<true, 128>(a, stream);
-    return launch_split<true, 256>(a, stream);
+template <bool BF>
+hipError_t launch_dim(const AttentionArgs& a, hipStream_t stream) {
+  if (use_tiles(a.B, a.Hq, a.Hkv, a.max_q, device_topology())) {
+    if (a.D == 64) return launch_tiles<BF, 64>(a, stream);
+    if (a.D == 128) return launch_tiles<BF, 128>(a, stream);
+    return launch_tiles<BF, 256>(a, stream);
   }
-  if (a.D == 64) return launch_split<false, 64>(a, stream);
-  if (a.D == 128) return launch_split<false, 128>(a, stream);
-  return launch_split<false, 256>(a, stream);
+  if (a.D == 64) return launch_split<BF, 64>(a, stream);
+  if (a.D == 128) return launch_split<BF, 128>(a, stream);
+  return launch_split<BF, 256>(a, stream);
+}
+
+hipError_t launch_attention(const AttentionArgs& a, bool bf16, hipStream_t stream) {
+  return bf16 ? launch_dim<true>(a, stream) : launch_dim<false>(a, stream);
 }
 
 }  // namespace qmm
