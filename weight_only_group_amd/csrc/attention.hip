@@ -533,31 +533,32 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
         st[u] = mfma32<BF>(*reinterpret_cast<const u32x4*>(ks + k_at[s] + u * 32 * D * 2), q[s], st[u]);
     const bool whole = key0 >= all_lo && key0 + BN <= all_hi;
     auto key_of = [&](int u, int i) { return key0 + 32 * u + 8 * (i >> 2) + 4 * kg + (i & 3); };
-    auto sees = [&](int u, int i) { return key_of(u, i) >= row.lo && key_of(u, i) < row.hi; };
     // The largest score of the row; without a distance bias that of the largest product.
     float best = -INFINITY;
-    bool some = whole;
+    uint32_t seen = ~0u;  // bit 16 u + i: the row sees key_of(u, i)
     if (SLOPES) {
 #pragma unroll
       for (int u = 0; u < SUB; ++u)
 #pragma unroll
         for (int i = 0; i < 16; ++i) st[u][i] = rule.template score<CAP, true>(st[u][i], row.pos, key_of(u, i));
     }
-    if (whole) {
-#pragma unroll
-      for (int u = 0; u < SUB; ++u)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) best = fmaxf(best, st[u][i]);
-    } else {
+    if (!whole) {
+      seen = 0;
 #pragma unroll
       for (int u = 0; u < SUB; ++u)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          best = fmaxf(best, sees(u, i) ? st[u][i] : -INFINITY);
-          some |= sees(u, i);
+          const bool in = (uint32_t)(key_of(u, i) - row.lo) < (uint32_t)max(row.hi - row.lo, 0);
+          seen |= in ? 1u << (16 * u + i) : 0u;
+          best = fmaxf(best, in ? st[u][i] : -INFINITY);
         }
+    } else {
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) best = fmaxf(best, st[u][i]);
     }
-    if (!SLOPES) best = some ? rule.template score<CAP, false>(best, 0, 0) : -INFINITY;
+    if (!SLOPES) best = seen ? rule.template score<CAP, false>(best, 0, 0) : -INFINITY;
     best = fmaxf(best, __shfl_xor(best, 32));
     // A row's maximum is left where it is while no weight passes 2^8: rescaling is rare.
     if (__any(best > mx + 8)) {
@@ -590,7 +591,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
 #pragma unroll
       for (int u = 0; u < SUB; ++u)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) st[u][i] = sees(u, i) ? st[u][i] : -INFINITY;
+        for (int i = 0; i < 16; ++i) st[u][i] = seen >> (16 * u + i) & 1 ? st[u][i] : -INFINITY;
     }
     u32x4 w[BN / 16];
 #pragma unroll
@@ -601,34 +602,28 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
         w[g][x] = pack_pair<BF>(__builtin_amdgcn_exp2f(st[g >> 1][i]), __builtin_amdgcn_exp2f(st[g >> 1][i + 1]));
         sum = add_pair<BF>(w[g][x], sum);  // the rounded weights make the denominator too
       }
-    auto add_values = [&](auto cut) {
-#pragma unroll
-      for (int g = 0; g < BN / 16; ++g)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const u32x2 x = read_transposed(vs + v_at[m][0] + g * 16 * D * 2), y = read_transposed(vs + v_at[m][1] + g * 16 * D * 2);
-          u32x4 v = {x[0], x[1], y[0], y[1]};
-          if constexpr (decltype(cut)::value) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] &= (not_finite<BF>(v[i]) ? 0u : 0xFFFFu) | (not_finite<BF>(v[i] >> 16) ? 0u : 0xFFFF0000u);
-          }
-          o[m] = mfma32<BF>(v, w[g], o[m]);
-        }
-    };
-    bool bad = false;
     if (!whole) {
-      // A value that is not finite must not reach rows that do not see it: see the split kernel.
+      // A value that is not finite must not reach rows that do not see it (0 times it is
+      // NaN): the rare step that holds one leaves its values to the end.
+      bool bad = false;
 #pragma unroll 4
       for (int i = lane; i < BN * D / 8; i += 64) {
         const u32x4 x = reinterpret_cast<const u32x4*>(vs)[i];
 #pragma unroll
         for (int y = 0; y < 4; ++y) bad |= (int)not_finite<BF>(x[y]) | (int)not_finite<BF>(x[y] >> 16);
       }
-      bad = __any(bad);
-      any_bad |= bad;
+      if (__any(bad)) {
+        any_bad = true;
+        continue;
+      }
     }
-    if (__builtin_expect(bad, 0)) add_values(std::true_type{});
-    else add_values(std::false_type{});
+#pragma unroll
+    for (int g = 0; g < BN / 16; ++g)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const u32x2 x = read_transposed(vs + v_at[m][0] + g * 16 * D * 2), y = read_transposed(vs + v_at[m][1] + g * 16 * D * 2);
+        o[m] = mfma32<BF>(u32x4{x[0], x[1], y[0], y[1]}, w[g], o[m]);
+      }
   }
 
   // Results leave by LDS, 32 dimensions at a time, each wave for its own rows.
@@ -637,26 +632,35 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
   __syncthreads();
   float* so = reinterpret_cast<float*>(&kvs[0][0][0]) + wave * 32 * LDO;
   const Row mine = row_of(p, r0 + (lane >> 1), q0, q1, kv, hk);
+  // Rare: dimensions 32 m on of the steps left out above, key by key, with their scores anew.
+  auto add_left_out = [&](int m) {
+    for (int t = t0; t < t1; ++t) {
+      const int key0 = t * BN;
+      if (key0 + BN <= lo || key0 >= hi || (key0 >= all_lo && key0 + BN <= all_hi)) continue;
+      const uint32_t here = key_row(key0 + (lane & (BN - 1)));
+      bool bad = false;
+      for (int d = lane / BN; d < D; d += 64 / BN) bad |= not_finite<BF>(a.v_cache[(size_t)here * D + d]);
+      if (!__any(bad)) continue;
+      for (int key = 0; key < BN; ++key) {
+        const size_t at = (size_t)__shfl(here, key) * D;
+        const bool in = key0 + key >= row.lo && key0 + key < row.hi;
+        if (!in) continue;
+        const uint16_t* qr = a.q + row.token * a.q_stride + (long long)row.head * D;
+        float dot = 0;
+        for (int d = 0; d < D; ++d) dot += bits_to_float<BF>((uint16_t)(qr[d] ^ q_sign)) * bits_to_float<BF>(a.k_cache[at + d]);
+        const float s = rule.template score<CAP, SLOPES>(dot, row.pos, key0 + key);
+        const float weight = bits_to_float<BF>(float_to_bits<BF>(__builtin_amdgcn_exp2f(s - (mx == -INFINITY ? 0.f : mx))));
+        for (int d = kg; d < 32; d += 2) so[n * LDO + d] += weight * inv * bits_to_float<BF>(a.v_cache[at + 32 * m + d]);
+      }
+    }
+  };
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
 #pragma unroll
     for (int g = 0; g < 4; ++g)
       *reinterpret_cast<f32x4*>(so + n * LDO + 8 * g + 4 * kg) =
           f32x4{o[m][4 * g] * inv, o[m][4 * g + 1] * inv, o[m][4 * g + 2] * inv, o[m][4 * g + 3] * inv};
-    if (any_bad) {
-      // Rare: the values left out above, to the rows that see them.
-      for (int t = t0; t < t1; ++t) {
-        const int key0 = t * BN;
-        if (key0 + BN <= lo || key0 >= hi || (key0 >= all_lo && key0 + BN <= all_hi)) continue;
-        const uint32_t here = key_row(key0 + (lane & (BN - 1)));
-        for (int key = 0; key < BN; ++key) {
-          const uint16_t* src = a.v_cache + (size_t)__shfl(here, key) * D + 32 * m;
-          if (key0 + key < row.lo || key0 + key >= row.hi) continue;
-          for (int d = kg; d < 32; d += 2)
-            if (not_finite<BF>(src[d])) so[n * LDO + d] += bits_to_float<BF>(src[d]);
-        }
-      }
-    }
+    if (any_bad) add_left_out(m);
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     if (mine.token >= 0) {
