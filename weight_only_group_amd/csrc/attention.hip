@@ -525,12 +525,23 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
     if (key0 + BN <= lo || key0 >= hi) continue;  // nothing for this wave's rows
     const char* ks = reinterpret_cast<const char*>(kvs[t & 1][0]);
     const char* vs = reinterpret_cast<const char*>(kvs[t & 1][1]);
+    // Products of keys and queries, the keys' pieces read kAhead steps before.
+    constexpr int kAhead = 3;
     f32x16 st[SUB] = {};
+    u32x4 kf[kAhead + 1][SUB];
+    auto read_keys = [&](int s) {
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s)
+      for (int u = 0; u < SUB; ++u) kf[s % (kAhead + 1)][u] = *reinterpret_cast<const u32x4*>(ks + k_at[s] + u * 32 * D * 2);
+    };
 #pragma unroll
-      for (int u = 0; u < SUB; ++u)
-        st[u] = mfma32<BF>(*reinterpret_cast<const u32x4*>(ks + k_at[s] + u * 32 * D * 2), q[s], st[u]);
+    for (int s = 0; s < kAhead; ++s) read_keys(s);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      if (s + kAhead < STEPS) read_keys(s + kAhead);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) st[u] = mfma32<BF>(kf[s % (kAhead + 1)][u], q[s], st[u]);
+    }
     const bool whole = key0 >= all_lo && key0 + BN <= all_hi;
     auto key_of = [&](int u, int i) { return key0 + 32 * u + 8 * (i >> 2) + 4 * kg + (i & 3); };
     // The largest score of the row; without a distance bias that of the largest product.
@@ -593,15 +604,6 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
 #pragma unroll
         for (int i = 0; i < 16; ++i) st[u][i] = seen >> (16 * u + i) & 1 ? st[u][i] : -INFINITY;
     }
-    u32x4 w[BN / 16];
-#pragma unroll
-    for (int g = 0; g < BN / 16; ++g)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int i = 8 * (g & 1) + 2 * x;
-        w[g][x] = pack_pair<BF>(__builtin_amdgcn_exp2f(st[g >> 1][i]), __builtin_amdgcn_exp2f(st[g >> 1][i + 1]));
-        sum = add_pair<BF>(w[g][x], sum);  // the rounded weights make the denominator too
-      }
     if (!whole) {
       // A value that is not finite must not reach rows that do not see it (0 times it is
       // NaN): the rare step that holds one leaves its values to the end.
@@ -614,16 +616,54 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
       }
       if (__any(bad)) {
         any_bad = true;
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+          for (int i = 0; i < 16; i += 2)
+            sum = add_pair<BF>(pack_pair<BF>(__builtin_amdgcn_exp2f(st[u][i]), __builtin_amdgcn_exp2f(st[u][i + 1])), sum);
         continue;
       }
     }
-#pragma unroll
-    for (int g = 0; g < BN / 16; ++g)
+    // Weights and their products with the values, sixteen keys at a time: the next ones'
+    // exponentials and reads go between the matrix operations.
+    constexpr int GROUPS = BN / 16;
+    u32x4 vf[2][MT], w[2];
+    auto read_values = [&](int g) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const u32x2 x = read_transposed(vs + v_at[m][0] + g * 16 * D * 2), y = read_transposed(vs + v_at[m][1] + g * 16 * D * 2);
-        o[m] = mfma32<BF>(u32x4{x[0], x[1], y[0], y[1]}, w[g], o[m]);
+        vf[g & 1][m] = u32x4{x[0], x[1], y[0], y[1]};
       }
+    };
+    auto weigh = [&](int g) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int i = 8 * (g & 1) + 2 * x;
+        w[g & 1][x] = pack_pair<BF>(__builtin_amdgcn_exp2f(st[g >> 1][i]), __builtin_amdgcn_exp2f(st[g >> 1][i + 1]));
+        sum = add_pair<BF>(w[g & 1][x], sum);  // the rounded weights make the denominator too
+      }
+    };
+    read_values(0);
+    weigh(0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+      if (g + 1 < GROUPS) {
+        read_values(g + 1);
+        weigh(g + 1);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) o[m] = mfma32<BF>(vf[g & 1][m], w[g & 1], o[m]);
+      if (g + 1 < GROUPS) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 2 * MT, 0);  // LDS reads
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);               // a matrix operation
+          __builtin_amdgcn_sched_group_barrier(0x402, (16 + MT - 1) / MT, 0);  // vector operations
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
 
   // Results leave by LDS, 32 dimensions at a time, each wave for its own rows.
