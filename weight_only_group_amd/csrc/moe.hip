@@ -16,7 +16,7 @@ namespace {
 
 // ---- routing -------------------------------------------------------------------
 
-constexpr int kRouteWaves = 8;
+constexpr int kRouteBatch = 8;  // units of H whose loads a wave has on the way together
 
 // The largest of a wave's values in every lane (bit patterns in the floats' order).
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
@@ -88,9 +88,9 @@ __device__ void route_top(const RouteArgs& a, int t, int lane) {
 // Block: the logits of 16 experts for 16 tokens, its waves over H; the block that
 // ends a token tile's logits chooses for its tokens. Bound: latency (a few hundred
 // KiB of router weights over the CUs).
-template <bool BF>
-__global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs a) {
-  __shared__ float part[kRouteWaves][16][17];
+template <bool BF, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES) route_kernel(RouteArgs a) {
+  __shared__ float part[WAVES][16][17];
   __shared__ int s_last;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, kg = lane >> 4;
   const int e = min((int)blockIdx.x * 16 + n, a.E - 1), t0 = blockIdx.y * 16, t = min(t0 + n, a.T - 1);
@@ -98,18 +98,17 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs a) {
   const u32x4* r = reinterpret_cast<const u32x4*>(a.router + (size_t)e * a.H + kg * 8);
   f32x4 acc = {};
   const int units = a.H / 32;
-  constexpr int kBatch = 4;  // units whose loads go out together
-  for (int u0 = wave; u0 < units; u0 += kBatch * kRouteWaves) {
-    u32x4 xv[kBatch], rv[kBatch];
+  for (int u0 = wave; u0 < units; u0 += kRouteBatch * WAVES) {
+    u32x4 xv[kRouteBatch], rv[kRouteBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int u = min(u0 + i * kRouteWaves, units - 1);
+    for (int i = 0; i < kRouteBatch; ++i) {
+      const int u = min(u0 + i * WAVES, units - 1);
       xv[i] = x[u * 4];
       rv[i] = r[u * 4];
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (u0 + i * kRouteWaves < units) acc = mfma16<BF>(xv[i], rv[i], acc);
+    for (int i = 0; i < kRouteBatch; ++i)
+      if (u0 + i * WAVES < units) acc = mfma16<BF>(xv[i], rv[i], acc);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) part[wave][4 * kg + i][n] = acc[i];
@@ -118,12 +117,12 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_kernel(RouteArgs a) {
     const int row = tid >> 4, col = tid & 15;
     float s = 0;
 #pragma unroll
-    for (int w = 0; w < kRouteWaves; ++w) s += part[w][row][col];
+    for (int w = 0; w < WAVES; ++w) s += part[w][row][col];
     if (t0 + row < a.T && (int)blockIdx.x * 16 + col < a.E)
       handoff_store(&a.logits[(size_t)(t0 + row) * a.E + blockIdx.x * 16 + col], s);
   }
   if (!handoff_last(&a.counters[blockIdx.y], gridDim.x, &s_last)) return;
-  for (int i = t0 + wave; i < min(t0 + 16, a.T); i += kRouteWaves) {
+  for (int i = t0 + wave; i < min(t0 + 16, a.T); i += WAVES) {
     if (a.E <= 64) route_top<1>(a, i, lane);
     else if (a.E <= 128) route_top<2>(a, i, lane);
     else if (a.E <= 256) route_top<4>(a, i, lane);
@@ -302,7 +301,8 @@ __device__ __forceinline__ void cut_units(u32x4 (&a)[kUnits], int c, int units) 
 
 // ---- gate and up products --------------------------------------------------------------
 
-constexpr int kGateWaves = 8;
+constexpr int kGateWaves = 4;
+static_assert(64 * kGateWaves == 256, "a thread per element of a block's result");
 
 // The experts in use are numbered by slots: with fewer assignments than experts
 // a slot is an assignment (in use where it is the first of its expert), else an
@@ -315,7 +315,7 @@ struct Slots {
 
 struct MoeKernelArgs {
   MoeArgs a;
-  FixedDiv by_upg_h, by_upg_i, by_top_k;  // 32-row units per group of both products; choices per token
+  FixedDiv by_upg_h, by_upg_i, by_top_k, by_runs;  // units per group of both products; choices per token; runs per expert of the second
   Slots slots;
   uint16_t* h;  // (assignments, 2, I) bf16: high and low parts, each unit in operand order
   int strips;
@@ -378,7 +378,7 @@ __device__ __forceinline__ void gate_up_rows(const MoeKernelArgs& p, int e, int 
 #pragma unroll
     for (int r = 0; r < 4; ++r) sums[wave][v][4 * j + r][n] = total[v][r];
   __syncthreads();
-  if (tid < 256 && base + (tid >> 4) < rows) {
+  if (base + (tid >> 4) < rows) {  // a thread per element of 16 x 16
     const int row = tid >> 4, cc = tid & 15;
     float g = 0, u = 0;
 #pragma unroll
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(64 * kDownWaves) down_kernel(MoeKernelArgs p) 
     int u, c0;
   };
   auto item = [&](int it) {
-    const int u = it / runs;
+    const int u = p.by_runs(it);
     return Item{u, (it - u * runs) * kRun<BITS>};
   };
   Chunk<BITS> run[kRun<BITS>];
@@ -609,8 +609,13 @@ size_t moe_route_workspace(int T, int H, int E) { return kWorkspaceHeader; }
 
 hipError_t launch_moe_route(const RouteArgs& a, bool bf16, hipStream_t stream) {
   const dim3 grid((unsigned)(a.E + 15) / 16, (unsigned)(a.T + 15) / 16);
-  if (bf16) route_kernel<true><<<grid, 64 * kRouteWaves, 0, stream>>>(a);
-  else route_kernel<false><<<grid, 64 * kRouteWaves, 0, stream>>>(a);
+  // Eight waves where a batch of each covers H, else sixteen (whose join takes longer:
+  // 7.0 against 9.3 us at one token and H 2048, 11.7 against 10.4 at 13 and 4096).
+  const bool few = a.H <= 8 * 32 * kRouteBatch;
+  if (bf16 && few) route_kernel<true, 8><<<grid, 512, 0, stream>>>(a);
+  else if (bf16) route_kernel<true, 16><<<grid, 1024, 0, stream>>>(a);
+  else if (few) route_kernel<false, 8><<<grid, 512, 0, stream>>>(a);
+  else route_kernel<false, 16><<<grid, 1024, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -620,7 +625,8 @@ size_t moe_workspace(int T, int H, int I, int E, int top_k) {
 }
 
 hipError_t launch_moe(const MoeArgs& a, int bits, bool bf16, bool strips, hipStream_t stream) {
-  MoeKernelArgs p = {a, fixed_div(a.gs_h / 32), fixed_div(a.gs_i / 32), fixed_div(a.top_k), {}, nullptr, strips};
+  const int run = 4 / (bits == 3 || bits == 8 ? 2 : 1), chunks = (a.I / 32 + 3) / 4;
+  MoeKernelArgs p = {a, fixed_div(a.gs_h / 32), fixed_div(a.gs_i / 32), fixed_div(a.top_k), fixed_div((chunks + run - 1) / run), {}, nullptr, strips};
   p.slots.count = cmin(a.E, a.T * a.top_k);
   char* at = a.workspace + kWorkspaceHeader;
   p.h = reinterpret_cast<uint16_t*>(at);

@@ -57,24 +57,22 @@ def declare(lib):
     return lib
 
 
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev} (got {t.device})")
-
-
-def _array(t, name, dtype, shape):
-    """A contiguous GPU tensor of exactly this type and shape."""
+def _array(t, name, dtype, shape, dev):
+    """A contiguous tensor on `dev` of exactly this type and shape."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t
     _qmm._gpu(t, name, dtype, ndim=len(shape))
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {tuple(shape)} (got {tuple(t.shape)})")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev} (got {t.device})")
     return t
 
 
 def _result(out, name, dtype, shape, dev):
     if out is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    return _array(out, name, dtype, shape)
+    return _array(out, name, dtype, shape, dev)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -113,13 +111,10 @@ def qmm_moe_route(x, router, top_k: int, renormalize: bool = True, workspace=Non
     (T, top_k) float32, and the ``logits`` (T, E) float32 = x @ router.T. ``router`` is (E, H)."""
     dt = _qmm._data_dtype(x, "x")
     _qmm._gpu(x, "x", dt)
-    _qmm._gpu(router, "router", dt)
     T, H = x.shape
-    E = router.shape[0]
-    if router.shape[1] != H:
-        raise ValueError(f"router must be (E, {H}) (got {tuple(router.shape)})")
     dev = x.device
-    _same_device(dev, router=router)
+    E = router.shape[0] if isinstance(router, torch.Tensor) and router.dim() else 0
+    _array(router, "router", dt, (E, H), dev)
     k = max(0, top_k)
     ids = torch.empty((T, k), dtype=torch.int32, device=dev)
     weights = torch.empty((T, k), dtype=torch.float32, device=dev)
@@ -136,15 +131,14 @@ def _experts(w, name, E, K, N, bits, group_size, dt, strips, dev):
         shapes = _qmm.packed_shapes(K, N, bits)
         if strips:
             shapes = tuple(s and _qmm.strips_shape(s[0], N) for s in shapes)
-        _array(qw, f"{name} qweight", torch.int32, (E, *shapes[0]))
+        _array(qw, f"{name} qweight", torch.int32, (E, *shapes[0]), dev)
         if bits == 3:
             if qlo is None:
                 raise ValueError(f"{name}: 3-bit weights need qweight_lo (the 1-bit plane)")
-            _array(qlo, f"{name} qweight_lo", torch.int32, (E, *shapes[1]))
+            _array(qlo, f"{name} qweight_lo", torch.int32, (E, *shapes[1]), dev)
         groups = 1 if group_size == -1 else K // group_size
-        _array(zeros, f"{name} zeros", dt, (E, groups, N))
-        _array(scales, f"{name} scales", dt, (E, groups, N))
-        _same_device(dev, qweight=qw, qweight_lo=qlo if bits == 3 else None, zeros=zeros, scales=scales)
+        _array(zeros, f"{name} zeros", dt, (E, groups, N), dev)
+        _array(scales, f"{name} scales", dt, (E, groups, N), dev)
     return Experts(*(None if t is None else t.data_ptr() for t in (qw, qlo if bits == 3 else None, zeros, scales)))
 
 
@@ -157,11 +151,9 @@ def qmm_moe(x, ids, weights, gate_up, down, bits: int, group_size: int, strips: 
     _qmm._gpu(x, "x", dt)
     T, H = x.shape
     dev = x.device
-    _qmm._gpu(ids, "ids", torch.int32)
-    k = ids.shape[1]
-    _array(ids, "ids", torch.int32, (T, k))
-    _array(weights, "weights", torch.float32, (T, k))
-    _same_device(dev, ids=ids, weights=weights)
+    k = ids.shape[1] if isinstance(ids, torch.Tensor) and ids.dim() == 2 else 0
+    _array(ids, "ids", torch.int32, (T, k), dev)
+    _array(weights, "weights", torch.float32, (T, k), dev)
     if down[2].dim() != 3 or gate_up[2].dim() != 3 or gate_up[2].shape[2] % 2:
         raise ValueError("zeros must be (E, G, 2 I) for gate_up and (E, G, H) for down")
     E, _, N = gate_up[2].shape
@@ -174,26 +166,28 @@ def qmm_moe(x, ids, weights, gate_up, down, bits: int, group_size: int, strips: 
 
 
 def _heads(t, name, dt):
-    """(T, heads, D) with dense heads; the token stride is free (a view of a product's rows)."""
+    """(T, heads, D) with dense heads; the token stride is free (a view of a product's rows).
+    Returns T, heads, D and that stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU (got {t.device})")
-    if t.dtype != dt:
+    if t.dtype is not dt:
         raise TypeError(f"{name} must be {dt} (got {t.dtype})")
-    if t.dim() != 3 or (t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]))):
-        raise ValueError(f"{name} must be (tokens, heads, D) with dense heads (got shape {tuple(t.shape)}, strides {t.stride()})")
-    # One token's stride is never used; a view may report any.
-    return t, t.shape[1] * t.shape[2] if t.shape[0] < 2 else t.stride(0)
+    if t.dim() == 3:
+        T, h, D = t.shape
+        st, sh, sd = t.stride()
+        if (sd == 1 and (h < 2 or sh == D)) or not T * h * D:
+            return T, h, D, h * D if T < 2 else st  # one token's stride is never used; a view may report any
+    raise ValueError(f"{name} must be (tokens, heads, D) with dense heads (got shape {tuple(t.shape)}, strides {t.stride()})")
 
 
-def _cache(k_cache, v_cache, Hkv, D, dt):
-    _qmm._gpu(k_cache, "k_cache", dt, ndim=4)
-    _array(v_cache, "v_cache", dt, k_cache.shape)
-    pages, hkv, page_size, d = k_cache.shape
-    if d != D or (Hkv is not None and hkv != Hkv):
-        raise ValueError(f"k_cache must be (pages, Hkv, page_size, {D}) (got {tuple(k_cache.shape)})")
-    return pages, hkv, page_size
+def _cache(k_cache, v_cache, D, dt, dev):
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4 or k_cache.shape[3] != D:
+        raise ValueError(f"k_cache must be a tensor (pages, Hkv, page_size, {D})")
+    _array(k_cache, "k_cache", dt, k_cache.shape, dev)
+    _array(v_cache, "v_cache", dt, k_cache.shape, dev)
+    return k_cache.shape
 
 
 def qmm_kv_append(q, k, v, cos, sin, positions, slots, k_cache, v_cache, adjacent: bool = False, out=None):
@@ -202,24 +196,25 @@ def qmm_kv_append(q, k, v, cos, sin, positions, slots, k_cache, v_cache, adjacen
     (pages, Hkv, page_size, D), and returns the rotated q. q, k and v may be views of one product's
     rows. ``adjacent``: pairs are (2i, 2i + 1), else (i, i + R / 2). cos None: no rotation."""
     dt = _qmm._data_dtype(q, "q")
-    q, qs = _heads(q, "q", dt)
-    k, ks = _heads(k, "k", dt)
-    v, vs = _heads(v, "v", dt)
-    T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    if tuple(k.shape) != (T, Hkv, D) or tuple(v.shape) != (T, Hkv, D):
+    T, Hq, D, qs = _heads(q, "q", dt)
+    Tk, Hkv, Dk, ks = _heads(k, "k", dt)
+    Tv, Hv, Dv, vs = _heads(v, "v", dt)
+    dev = q.device
+    if not (T == Tk == Tv and Hkv == Hv and D == Dk == Dv):
         raise ValueError(f"k and v must be ({T}, Hkv, {D}) (got {tuple(k.shape)}, {tuple(v.shape)})")
-    pages, _, page_size = _cache(k_cache, v_cache, Hkv, D, dt)
+    if k.device != dev or v.device != dev:
+        raise ValueError(f"k and v must be on {dev} (got {k.device}, {v.device})")
+    pages, hkv, page_size, _ = _cache(k_cache, v_cache, D, dt, dev)
+    if hkv != Hkv:
+        raise ValueError(f"k_cache has {hkv} heads, k has {Hkv}")
     P = R = 0
     if cos is not None:
-        _qmm._gpu(cos, "cos", torch.float32)
-        _array(sin, "sin", torch.float32, cos.shape)
-        _array(positions, "positions", torch.int32, (T,))
-        P, R = cos.shape[0], 2 * cos.shape[1]
-    _array(slots, "slots", torch.int64, (T,))
-    dev = q.device
-    _same_device(dev, k=k, v=v, cos=cos, sin=sin if R else None, positions=positions if R else None, slots=slots,
-                 k_cache=k_cache, v_cache=v_cache)
+        P, half = cos.shape if isinstance(cos, torch.Tensor) and cos.dim() == 2 else (0, 0)
+        _array(cos, "cos", torch.float32, (P, half), dev)
+        _array(sin, "sin", torch.float32, (P, half), dev)
+        _array(positions, "positions", torch.int32, (T,), dev)
+        R = 2 * half
+    _array(slots, "slots", torch.int64, (T,), dev)
     out = _result(out, "out", dt, (T, Hq, D), dev)
     flags = (QMM_BF16 if dt == torch.bfloat16 else 0) | (QMM_ADJACENT if adjacent else 0)
     turn = (_p(cos), _p(sin), R, P, _p(positions)) if R else (None, None, 0, 0, None)
@@ -235,24 +230,21 @@ def qmm_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q: int
     sees none gets 0. ``scale`` defaults to 1 / sqrt(D); ``softcap`` c > 0 takes c tanh(s / c) of the
     scores; ``slopes`` (Hq,) subtract slope * |p - key position|. max_q and max_kv bound the lengths."""
     dt = _qmm._data_dtype(q, "q")
-    q, qs = _heads(q, "q", dt)
-    T, Hq, D = q.shape
-    pages, Hkv, page_size = _cache(k_cache, v_cache, None, D, dt)
-    _qmm._gpu(page_table, "page_table", torch.int32)
-    B = page_table.shape[0]
-    _array(kv_lens, "kv_lens", torch.int32, (B,))
-    _array(q_starts, "q_starts", torch.int32, (B + 1,))
-    if first is not None:
-        _array(first, "first", torch.int32, (T,))
-    if end is not None:
-        _array(end, "end", torch.int32, (T,))
-    if slopes is not None:
-        _array(slopes, "slopes", torch.float32, (Hq,))
+    T, Hq, D, qs = _heads(q, "q", dt)
     dev = q.device
-    _same_device(dev, k_cache=k_cache, v_cache=v_cache, page_table=page_table, kv_lens=kv_lens, q_starts=q_starts,
-                 first=first, end=end, slopes=slopes)
+    pages, Hkv, page_size, _ = _cache(k_cache, v_cache, D, dt, dev)
+    B, table_stride = page_table.shape if isinstance(page_table, torch.Tensor) and page_table.dim() == 2 else (0, 0)
+    _array(page_table, "page_table", torch.int32, (B, table_stride), dev)
+    _array(kv_lens, "kv_lens", torch.int32, (B,), dev)
+    _array(q_starts, "q_starts", torch.int32, (B + 1,), dev)
+    if first is not None:
+        _array(first, "first", torch.int32, (T,), dev)
+    if end is not None:
+        _array(end, "end", torch.int32, (T,), dev)
+    if slopes is not None:
+        _array(slopes, "slopes", torch.float32, (Hq,), dev)
     out = _result(out, "out", dt, (T, Hq, D), dev)
-    args = (_p(q), qs, T, Hq, Hkv, D, _p(k_cache), _p(v_cache), pages, page_size, _p(page_table), page_table.shape[1],
+    args = (_p(q), qs, T, Hq, Hkv, D, _p(k_cache), _p(v_cache), pages, page_size, _p(page_table), table_stride,
             _p(kv_lens), _p(q_starts), B, max_q, max_kv, _p(first), _p(end), 1.0 / math.sqrt(D) if scale is None else scale,
             softcap, _p(slopes), QMM_BF16 if dt == torch.bfloat16 else 0, _p(out))
     return _launch("qmm_attention", dev, args, out, workspace, (B, T, Hq, Hkv, D, max_q, max_kv))
@@ -274,8 +266,7 @@ def qmm_logprobs(logits, targets=None, top: int = 0, workspace=None):
     stride = V if M < 2 else logits.stride(0)
     dev = logits.device
     if targets is not None:
-        _array(targets, "targets", torch.int64, (M,))
-        _same_device(dev, targets=targets)
+        _array(targets, "targets", torch.int64, (M,), dev)
     new = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
     n = max(0, top)
     logprob, entropy = new(M) if targets is not None else None, new(M)
