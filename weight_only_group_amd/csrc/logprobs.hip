@@ -19,7 +19,9 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 256, kWaves = kThreads / 64;
-constexpr int kPerBytes = 64;  // of logits per thread and step
+// Bytes of logits per thread and step: 64, or 16 where the blocks of the wider step
+// would leave CUs idle (one row of 32000: see the plan).
+constexpr int kWide = 64, kNarrow = 16;
 constexpr int kList = 1024;    // keys a wave's list holds
 constexpr int kMaxSplit = 64;
 constexpr int kMaxKeys = 512;  // keys of a block's waves before their last selection
@@ -128,9 +130,9 @@ struct LogprobKernelArgs {
 // Block: `steps` steps of one row; with several blocks per row the last to arrive
 // joins them. Bound: HBM, each logit is read once (a row that is not finite again,
 // per alternative).
-template <LogitType TYPE>
+template <LogitType TYPE, int BYTES>
 __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(LogprobKernelArgs p) {
-  constexpr int SIZE = logit_size(TYPE), VEC = 16 / SIZE, PER = kPerBytes / SIZE, STEP = kThreads * PER, BITS = order_bits(TYPE);
+  constexpr int SIZE = logit_size(TYPE), VEC = 16 / SIZE, PER = BYTES / SIZE, STEP = kThreads * PER, BITS = order_bits(TYPE);
   constexpr int LOADS = PER / VEC;
   __shared__ __attribute__((aligned(16))) uint64_t list[kWaves][kList];
   __shared__ uint64_t best[kMaxTop], first_least, wave_least[kWaves];
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(LogprobKernelArgs
       }
       least_logit = order_float((uint32_t)(least >> 32));
 #pragma unroll
-      for (int g = 0; g < PER; g += 8) {
+      for (int g = 0; g < PER; g += (PER < 8 ? PER : 8)) {
         if (listed > kList - 8 * 64) {
           const uint64_t t = shrink_list<BITS>(list[wave], listed, top, lane);
           listed = top;
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(LogprobKernelArgs
           least_logit = order_float((uint32_t)(least >> 32));
         }
 #pragma unroll
-        for (int i = g; i < g + 8; ++i) {
+        for (int i = g; i < g + (PER < 8 ? PER : 8); ++i) {
           if (!__any(l[i] >= least_logit)) continue;
           const uint64_t key = make_key(l[i], index(i));
           const bool in = key >= least && (unsigned)index(i) < (unsigned)a.V;
@@ -378,18 +380,21 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(LogprobKernelArgs
 
 struct LogprobPlan {
   int split, steps;
+  bool narrow;
 };
 LogprobPlan logprob_plan(int M, int V, int top, LogitType type, DeviceTopo topo) {
   // Blocks enough for four per CU, a step each at least; the joining block's lists hold all parts' keys.
-  const int step = kThreads * kPerBytes / logit_size(type);
-  const long long places = (long long)V + 16 / logit_size(type) - 1, most = (places + step - 1) / step;
+  const long long places = (long long)V + 16 / logit_size(type) - 1;
+  const bool narrow = (long long)M * places * logit_size(type) < (long long)topo.cus * kThreads * kWide;
+  const int step = kThreads * (narrow ? kNarrow : kWide) / logit_size(type);
+  const long long most = (places + step - 1) / step;
   long long split = 4ll * topo.cus / M;
   if (split > kMaxSplit) split = kMaxSplit;
   if (top > 0 && split > kWaves * kList / top) split = kWaves * kList / top;
   if (split > most) split = most;
   if (split < 1 || M > kGemvMaxStrips) split = 1;
   const long long steps = (most + split - 1) / split;
-  return {(int)((most + steps - 1) / steps), (int)steps};
+  return {(int)((most + steps - 1) / steps), (int)steps, narrow};
 }
 
 }  // namespace
@@ -411,9 +416,10 @@ hipError_t launch_logprobs(const LogprobArgs& a, LogitType type, hipStream_t str
     p.keys = reinterpret_cast<uint64_t*>(p.sums + (size_t)a.M * plan.split * 4);
   }
   const dim3 grid((unsigned)(a.M * plan.split));
-  if (type == LogitType::kFp32) logprobs_kernel<LogitType::kFp32><<<grid, kThreads, 0, stream>>>(p);
-  else if (type == LogitType::kBf16) logprobs_kernel<LogitType::kBf16><<<grid, kThreads, 0, stream>>>(p);
-  else logprobs_kernel<LogitType::kFp16><<<grid, kThreads, 0, stream>>>(p);
+  const auto run = [&](auto kernel) { kernel<<<grid, kThreads, 0, stream>>>(p); };
+  if (type == LogitType::kFp32) run(plan.narrow ? logprobs_kernel<LogitType::kFp32, kNarrow> : logprobs_kernel<LogitType::kFp32, kWide>);
+  else if (type == LogitType::kBf16) run(plan.narrow ? logprobs_kernel<LogitType::kBf16, kNarrow> : logprobs_kernel<LogitType::kBf16, kWide>);
+  else run(plan.narrow ? logprobs_kernel<LogitType::kFp16, kNarrow> : logprobs_kernel<LogitType::kFp16, kWide>);
   return hipGetLastError();
 }
 
