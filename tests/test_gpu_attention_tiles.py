@@ -52,6 +52,15 @@ def test_masks(w, kind, D):  # noqa: F811
     assert not f64(out)[np.maximum(first, 0) >= np.minimum(end, kv)].any()
 
 
+@pytest.mark.parametrize("kv,q_lens", [(KV, PART), ([200, 33], [3, 1])], ids=["tiles", "split"])
+def test_ranges_at_the_ends_of_32_bits(w, kv, q_lens):  # noqa: F811
+    T = sum(q_lens)
+    r = np.random.default_rng(6)
+    first = r.choice([-2**31, -1, 0, 5, 40, 2**31 - 1], T)
+    end = r.choice([-2**31, -2**31 + 1, -7, 0, 60, 2**31 - 1], T)
+    run(w, kv, q_lens, 6, 6, 64, 16, "fp16", first=first, end=end)
+
+
 def test_all_rows_empty(w):  # noqa: F811
     T = sum(PART)
     out = run(w, KV, PART, 6, 6, 128, 16, "fp16", first=np.full(T, 30), end=np.full(T, 30))

@@ -89,7 +89,7 @@ __device__ __forceinline__ Row row_of(const AttnKernelArgs& p, int r, int q0, in
   w.head = hk * p.group + r - i * p.group;
   w.pos = kv - (q1 - q0) + i;
   w.lo = a.first ? max(a.first[w.token], 0) : 0;
-  w.hi = min(a.end ? a.end[w.token] : w.pos + 1, kv);
+  w.hi = max(min(a.end ? a.end[w.token] : w.pos + 1, kv), 0);  // not below 0: hi - lo does not overflow
   return w;
 }
 
@@ -587,11 +587,26 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
 #pragma unroll
       for (int u = 0; u < SUB; ++u) st[u] -= off;
     } else if (CAP) {
+      // Stage by stage over sixteen: left to itself the compiler takes two at a time, each
+      // waiting for its own exponential and reciprocal.
 #pragma unroll
-      for (int u = 0; u < SUB; ++u)
+      for (int u = 0; u < SUB; ++u) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          st[u][i] = fmaf(-2 * rule.cap, __builtin_amdgcn_rcpf(1 + __builtin_amdgcn_exp2f(st[u][i] * rule.scale)), rule.cap - off);
+        for (int i = 0; i < 16; ++i) st[u][i] *= rule.scale;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st[u][i] = __builtin_amdgcn_exp2f(st[u][i]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st[u][i] += 1;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st[u][i] = __builtin_amdgcn_rcpf(st[u][i]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st[u][i] = fmaf(-2 * rule.cap, st[u][i], rule.cap - off);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     } else {
 #pragma unroll
       for (int u = 0; u < SUB; ++u)
