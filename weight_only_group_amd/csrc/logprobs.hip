@@ -20,7 +20,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 // Bytes of logits per thread and step: 64, or 16 where the blocks of the wider step
-// would leave CUs idle (one row of 32000: see the plan).
+// would leave CUs idle (one row of 32000 fp16: 10.6 us in 16 blocks, 11.6 us in 4).
 constexpr int kWide = 64, kNarrow = 16;
 constexpr int kList = 1024;    // keys a wave's list holds
 constexpr int kMaxSplit = 64;
@@ -128,8 +128,10 @@ struct LogprobKernelArgs {
 };
 
 // Block: `steps` steps of one row; with several blocks per row the last to arrive
-// joins them. Bound: HBM, each logit is read once (a row that is not finite again,
-// per alternative).
+// joins them. Bound: HBM for many rows, each logit is read once (a row that is not finite
+// again, per alternative): 4096 rows of 50257 fp32 in 200 us, 4.1 TB/s. The selection of
+// alternatives and the hand-over for few: 96 rows of 128257 bf16 with 20 alternatives
+// 23.8 us, one row of 32000 fp16 with 5 10.6 us.
 template <LogitType TYPE, int BYTES>
 __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(LogprobKernelArgs p) {
   constexpr int SIZE = logit_size(TYPE), VEC = 16 / SIZE, PER = BYTES / SIZE, STEP = kThreads * PER, BITS = order_bits(TYPE);
