@@ -59,8 +59,11 @@ def declare(lib):
 
 def _array(t, name, dtype, shape, dev):
     """A contiguous tensor on `dev` of exactly this type and shape."""
-    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
-        return t
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+            return t
+    except AttributeError:  # no tensor: the checks below say so
+        pass
     _qmm._gpu(t, name, dtype, ndim=len(shape))
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {tuple(shape)} (got {tuple(t.shape)})")
@@ -69,10 +72,11 @@ def _array(t, name, dtype, shape, dev):
     return t
 
 
-def _result(out, name, dtype, shape, dev):
+def _result(out, like, shape):
+    """`out`, checked, or a new tensor of `like`'s type and device."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    return _array(out, name, dtype, shape, dev)
+        return like.new_empty(shape)
+    return _array(out, "out", like.dtype, shape, like.device)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -83,7 +87,7 @@ def _need(name, *shape):
 
 def _launch(name, dev, args, out=(), workspace=None, shape=None):
     """Calls the entry point on the device's current stream; with `shape`, a workspace goes before the stream."""
-    here = torch.cuda.current_device()
+    here = torch._C._cuda_getDevice()
     if here != dev.index:
         with torch.cuda.device(dev):
             return _launch(name, dev, args, out, workspace, shape)
@@ -94,9 +98,13 @@ def _launch(name, dev, args, out=(), workspace=None, shape=None):
             workspace = _qmm._workspaces.get((here, stream))
             if need and (workspace is None or workspace.numel() < need):
                 workspace = _qmm.gemv_workspace(dev, need)
-        ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-        args = (*args, *ws)
-    status = getattr(_qmm._lib or _qmm.library(), name)(*args, stream)
+        if workspace is None:
+            args += (None, 0, stream)
+        else:
+            args += (workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream)
+    else:
+        args += (stream,)
+    status = getattr(_qmm._lib or _qmm.library(), name)(*args)
     if status:
         _qmm._check(status, name)
     return out
@@ -118,7 +126,7 @@ def qmm_moe_route(x, router, top_k: int, renormalize: bool = True, workspace=Non
     k = max(0, top_k)
     ids = torch.empty((T, k), dtype=torch.int32, device=dev)
     weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+    logits = weights.new_empty((T, E))
     flags = (QMM_BF16 if dt == torch.bfloat16 else 0) | (QMM_RENORMALIZE if renormalize else 0)
     return _launch("qmm_moe_route", dev, (_p(x), T, H, _p(router), E, top_k, flags, _p(ids), _p(weights), _p(logits)),
                    (ids, weights, logits), workspace, (T, H, E))
@@ -160,7 +168,7 @@ def qmm_moe(x, ids, weights, gate_up, down, bits: int, group_size: int, strips: 
     I = N // 2
     gu = _experts(gate_up, "gate_up", E, H, N, bits, group_size, dt, strips, dev)
     dn = _experts(down, "down", E, I, H, bits, group_size, dt, strips, dev)
-    y = _result(out, "out", dt, (T, H), dev)
+    y = _result(out, x, (T, H))
     return _launch("qmm_moe", dev, (_p(x), T, H, I, E, k, _p(ids), _p(weights), ctypes.byref(gu), ctypes.byref(dn), bits,
                                     group_size, _qmm._flags(dt, strips), _p(y)), y, workspace, (T, H, I, E, k))
 
@@ -215,7 +223,7 @@ def qmm_kv_append(q, k, v, cos, sin, positions, slots, k_cache, v_cache, adjacen
         _array(positions, "positions", torch.int32, (T,), dev)
         R = 2 * half
     _array(slots, "slots", torch.int64, (T,), dev)
-    out = _result(out, "out", dt, (T, Hq, D), dev)
+    out = _result(out, q, (T, Hq, D))
     flags = (QMM_BF16 if dt == torch.bfloat16 else 0) | (QMM_ADJACENT if adjacent else 0)
     turn = (_p(cos), _p(sin), R, P, _p(positions)) if R else (None, None, 0, 0, None)
     return _launch("qmm_kv_append", dev, (_p(q), qs, _p(k), ks, _p(v), vs, T, Hq, Hkv, D, *turn, _p(slots), _p(out),
@@ -243,7 +251,7 @@ def qmm_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q: int
         _array(end, "end", torch.int32, (T,), dev)
     if slopes is not None:
         _array(slopes, "slopes", torch.float32, (Hq,), dev)
-    out = _result(out, "out", dt, (T, Hq, D), dev)
+    out = _result(out, q, (T, Hq, D))
     args = (_p(q), qs, T, Hq, Hkv, D, _p(k_cache), _p(v_cache), pages, page_size, _p(page_table), table_stride,
             _p(kv_lens), _p(q_starts), B, max_q, max_kv, _p(first), _p(end), 1.0 / math.sqrt(D) if scale is None else scale,
             softcap, _p(slopes), QMM_BF16 if dt == torch.bfloat16 else 0, _p(out))
@@ -267,10 +275,11 @@ def qmm_logprobs(logits, targets=None, top: int = 0, workspace=None):
     dev = logits.device
     if targets is not None:
         _array(targets, "targets", torch.int64, (M,), dev)
-    new = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
     n = max(0, top)
-    logprob, entropy = new(M) if targets is not None else None, new(M)
-    top_logprobs, top_ids = new(M, n), new(M, n, dtype=torch.int32)
+    entropy = torch.empty(M, dtype=torch.float32, device=dev)
+    logprob = None if targets is None else entropy.new_empty(M)
+    top_logprobs = entropy.new_empty((M, n))
+    top_ids = torch.empty((M, n), dtype=torch.int32, device=dev)
     flags = {torch.float16: 0, torch.bfloat16: QMM_BF16, torch.float32: QMM_FP32}[logits.dtype]
     return _launch("qmm_logprobs", dev, (_p(logits), stride, M, V, _p(targets), top, flags, _p(logprob), _p(entropy),
                                          _p(top_logprobs), _p(top_ids)),
