@@ -335,12 +335,16 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) attentio
   if (p.split > 1) {
     // Partial sums of the parts, joined in order by the block that arrives last.
     const size_t tile = ((size_t)b * a.Hkv + hk) * p.rtiles + rt;
-    float* po = p.part + ((tile * p.split + part) * kRows + r) * D + d0;
+    // A thread's pairs lie 256 pairs apart: the threads of a store write whole lines. Rows past the
+    // sequence's last (12 of 16 with four heads a group and one query) are left out.
+    float* po = p.part + (tile * p.split + part) * kRows * D + 2 * tid;
+    if (mine.token >= 0) {
 #pragma unroll
-    for (int e = 0; e < E; e += 2) handoff_store(po + e, o[e], o[e + 1]);
-    if ((tid & 15) == 0) handoff_store(p.part_ml + ((tile * p.split + part) * kRows + r) * 2, m, l);
-    if (!handoff_last(&p.counters[tile], (uint32_t)p.split, &s_last)) return;
-    const float* qo = p.part + (tile * p.split * kRows + r) * D + d0;
+      for (int e = 0; e < E; e += 2) handoff_store(po + e * 256, o[e], o[e + 1]);
+      if ((tid & 15) == 0) handoff_store(p.part_ml + ((tile * p.split + part) * kRows + r) * 2, m, l);
+    }
+    if (!handoff_last(&p.counters[tile], (uint32_t)p.split, &s_last) || mine.token < 0) return;
+    const float* qo = p.part + tile * p.split * kRows * D + 2 * tid;
     const float* qm = p.part_ml + (tile * p.split * kRows + r) * 2;
     // Four parts' loads at a time; places past the last part repeat it with a factor of 0.
     constexpr int kBatch = 4;
@@ -365,7 +369,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) attentio
         ms[s] = ml.a;
         ls[s] = ml.b;
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) os[s][e] = handoff_load_pair(qo + (size_t)at * kRows * D + 2 * e);
+        for (int e = 0; e < E / 2; ++e) os[s][e] = handoff_load_pair(qo + (size_t)at * kRows * D + 512 * e);
       }
 #pragma unroll
       for (int s = 0; s < kBatch; ++s) {
