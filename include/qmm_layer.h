@@ -140,7 +140,9 @@ qmm_status qmm_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* k,
  *           [i page_size, (i + 1) page_size) of sequence b at [b, i]
  *   kv_lens (B,), q_starts (B + 1,), first, end (T,) int32; slopes (Hq,) fp32
  *   max_q, max_kv: no sequence has more queries and keys than these; further ones are left out
- * Query head h reads key head h / (Hq / Hkv). Scores, softmax and sums are fp32;
+ * Query head h reads key head h / (Hq / Hkv). Scores, softmax and sums are fp32
+ * (with a softcap of up to 64 a score may be off by softcap * 2^-22, with a larger
+ * one by a few roundings of its own size);
  * the weights exp(s) are rounded to the data type for the product with v, and
  * the same rounded weights make the denominator.
  * Requirements: D 64, 128 or 256; Hq % Hkv == 0; page_size >= 1; q_stride % 8

@@ -126,8 +126,9 @@ def attention(q, k_cache, v_cache, table, kv_lens, q_starts, scale, softcap=0.0,
                 s = scale * (K @ qh)
                 err = (D + 4) * F32 * abs(scale) * (np.abs(K) @ np.abs(qh))
                 if softcap > 0:
+                    # A cap's own error goes with the score; up to a cap of 64 a few roundings of the cap may come on top.
                     s = softcap * np.tanh(s / softcap)
-                    err = err + 8 * F32 * softcap
+                    err = err + 16 * F32 * np.abs(s) + (4 * F32 * softcap if softcap <= 64 else 0.0)
                 if slopes is not None:
                     s = s - float(slopes[h]) * np.abs(pos - keys)
                     err = err + 4 * F32 * float(slopes[h]) * np.abs(pos - keys)

@@ -52,25 +52,44 @@ struct AttnKernelArgs {
   float* part_ml;
 };
 
+// How a cap is taken. Up to kSmallCap: cap - 2 cap / (1 + e^2x), x = s / cap, whose
+// error is a few roundings of the cap's size, 4 cap 2^-24 (2^-16 at 64: a sixteenth of
+// the weights' own rounding in fp16). For larger caps, where that would reach the
+// weights, a series for |x| < 1/4 and the quotient beyond, so that the error goes with
+// the score. In blocks of 128 rows it takes longer, hence the two: a prompt of 8192, 32/8
+// heads of 128, 700 us with a small cap, 945 us with a larger one.
+enum Cap { kNoCap, kSmallCap, kAnyCap };
+constexpr float kSmallCapMost = 64.f;
+
 // The score, times log2(e), of a raw product.
 struct ScoreRule {
-  float scale;       // without a cap: factor; with one: 2 log2(e) scale / cap, of the exponential in tanh
-  float cap;         // cap log2(e), or 0
-  float slope;       // slope log2(e) of this lane's head
-  template <bool CAP, bool SLOPES>
+  float scale;    // a product's factor: of the score, with a small cap of the exponent 2x log2(e)
+  float inverse;  // any cap: of x
+  float cap, slope;
+  template <Cap CAP, bool SLOPES>
   __device__ __forceinline__ float score(float dot, int pos, int key) const {
-    // cap tanh(x) = cap - 2 cap / (1 + e^2x): cap at x = inf, -cap at -inf
-    const float s = CAP ? cap - 2 * cap * __builtin_amdgcn_rcpf(1 + __builtin_amdgcn_exp2f(dot * scale)) : dot * scale;
+    float s = dot * scale;
+    if (CAP == kSmallCap) s = cap - 2 * cap * __builtin_amdgcn_rcpf(1 + __builtin_amdgcn_exp2f(s));  // cap at x = inf, -cap at -inf
+    if (CAP == kAnyCap) {
+      // tanh x = x (1 - x^2/3 + 2 x^4/15 - 17 x^6/315 + 62 x^8/2835 - ...), the next term below 2^-26 x at 1/4.
+      const float x = dot * inverse, u = x * x;
+      const float series = fmaf(u, fmaf(u, fmaf(u, fmaf(u, 62.f / 2835, -17.f / 315), 2.f / 15), -1.f / 3), 1.f);
+      const float far = cap * fmaf(-2, __builtin_amdgcn_rcpf(1 + __builtin_amdgcn_exp2f(2 * kLog2e * x)), 1.f);
+      s = fabsf(x) < 0.25f ? s * series : far;
+    }
     return SLOPES ? s - slope * fabsf((float)(pos - key)) : s;
-  }
-  __device__ __forceinline__ float operator()(float dot, int pos, int key) const {
-    return cap > 0 ? score<true, true>(dot, pos, key) : score<false, true>(dot, pos, key);
   }
 };
 
+inline __host__ __device__ Cap cap_kind(float softcap) {
+  return !(softcap > 0) ? kNoCap : softcap <= kSmallCapMost ? kSmallCap : kAnyCap;
+}
+
 __device__ __forceinline__ ScoreRule score_rule(const AttentionArgs& a, int head) {
   ScoreRule r;
-  r.scale = a.softcap > 0 ? 2 * kLog2e * a.scale / a.softcap : kLog2e * a.scale;
+  // (kept finite where a tiny cap's inverse is not: 0 times it is 0)
+  r.inverse = fminf(fmaxf(a.scale / a.softcap, -1e38f), 1e38f);
+  r.scale = cap_kind(a.softcap) == kSmallCap ? 2 * kLog2e * r.inverse : kLog2e * a.scale;
   r.cap = kLog2e * a.softcap;
   r.slope = a.slopes ? kLog2e * a.slopes[head] : 0.f;
   return r;
@@ -112,7 +131,7 @@ __device__ __forceinline__ bool not_finite(uint32_t v) {
 // left operand wants eight keys of one dimension per lane: a lane loads 8 (or 4)
 // dimensions of its eight keys, whole cache lines per 16 lanes, and pairs them up
 // with byte permutes; dimension d = 8 m + i is row m of product i.
-template <bool BF, int D>
+template <bool BF, int D, Cap CAP>
 __global__ void __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) attention_split_kernel(AttnKernelArgs p) {
   constexpr int STEPS = D / 32;
   constexpr int CH = D >= 128 ? 8 : 4;  // dimensions per lane and half
@@ -213,7 +232,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) attentio
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
       const int j = j0 + 16 * (x >> 2) + (x & 3);
-      s[x] = rule(st[x >> 2][x & 3], row.pos, j);
+      s[x] = rule.template score<CAP, true>(st[x >> 2][x & 3], row.pos, j);
       if (!whole) s[x] = j >= row.lo && j < row.hi ? s[x] : -INFINITY;
       best = fmaxf(best, s[x]);
     }
@@ -425,7 +444,7 @@ template <int D> constexpr int kTileKeys = D == 256 ? 32 : 64;  // keys per step
 // they are, for the four neighbouring keys that a transposed LDS read of V gives.
 // The 16-byte pieces of an LDS row are reordered by the row (an exclusive or), so
 // that both the rows' reads and the transposed reads fall on distinct banks.
-template <bool BF, int D, bool CAP, bool SLOPES>
+template <bool BF, int D, Cap CAP, bool SLOPES>
 __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(AttnKernelArgs p) {
   constexpr int BN = kTileKeys<D>, SUB = BN / 32, PIECES = D / 8, STEPS = D / 16, MT = D / 32;
   constexpr int OWN = BN / kWaves, LOADS = OWN * D * 2 / 1024, PER_LOAD = 512 / D;  // keys a wave loads, in how many loads
@@ -448,6 +467,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
   ScoreRule rule = score_rule(a, row.head);
   const uint32_t q_sign = rule.scale < 0 ? 0x80008000u : 0u;
   rule.scale = fabsf(rule.scale);
+  rule.inverse = fabsf(rule.inverse);
 
   // Keys that any row of the wave sees, and those that all see; the block's from the waves'.
   int lo = row.lo < row.hi ? row.lo : INT32_MAX, hi = row.lo < row.hi ? row.hi : 0;
@@ -551,14 +571,16 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
     }
     const bool whole = key0 >= all_lo && key0 + BN <= all_hi;
     auto key_of = [&](int u, int i) { return key0 + 32 * u + 8 * (i >> 2) + 4 * kg + (i & 3); };
-    // The largest score of the row; without a distance bias that of the largest product.
+    // The largest score of the row; where a score is more than a multiply-add or a small cap of its
+    // product the scores are taken first, else only that of the largest product.
+    constexpr bool FIRST = SLOPES || CAP == kAnyCap;
     float best = -INFINITY;
     uint32_t seen = ~0u;  // bit 16 u + i: the row sees key_of(u, i)
-    if (SLOPES) {
+    if (FIRST) {
 #pragma unroll
       for (int u = 0; u < SUB; ++u)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) st[u][i] = rule.template score<CAP, true>(st[u][i], row.pos, key_of(u, i));
+        for (int i = 0; i < 16; ++i) st[u][i] = rule.template score<CAP, SLOPES>(st[u][i], row.pos, key_of(u, i));
     }
     if (!whole) {
       seen = 0;
@@ -576,7 +598,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
 #pragma unroll
         for (int i = 0; i < 16; ++i) best = fmaxf(best, st[u][i]);
     }
-    if (!SLOPES) best = seen ? rule.template score<CAP, false>(best, 0, 0) : -INFINITY;
+    if (!FIRST) best = seen ? rule.template score<CAP, false>(best, 0, 0) : -INFINITY;
     best = fmaxf(best, __shfl_xor(best, 32));
     // A row's maximum is left where it is while no weight passes 2^8: rescaling is rare.
     if (__any(best > mx + 8)) {
@@ -590,10 +612,10 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
     const float off = mx == -INFINITY ? 0.f : mx;
     // Exponents: the scores less the maximum, in one multiply-add of the product (or, with a cap, of
     // the reciprocal in the tanh).
-    if (SLOPES) {
+    if (FIRST) {
 #pragma unroll
       for (int u = 0; u < SUB; ++u) st[u] -= off;
-    } else if (CAP) {
+    } else if (CAP == kSmallCap) {
       // Stage by stage over sixteen: left to itself the compiler takes two at a time, each
       // waiting for its own exponential and reciprocal.
 #pragma unroll
@@ -754,10 +776,12 @@ hipError_t launch_tiles(const AttentionArgs& a, hipStream_t stream) {
   const long long blocks = ((long long)a.B * a.Hkv + 7) / 8 * 8 * rtiles;
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks);
-  if (a.softcap > 0 && a.slopes) attention_tile_kernel<BF, D, true, true><<<grid, 64 * kWaves, 0, stream>>>(p);
-  else if (a.softcap > 0) attention_tile_kernel<BF, D, true, false><<<grid, 64 * kWaves, 0, stream>>>(p);
-  else if (a.slopes) attention_tile_kernel<BF, D, false, true><<<grid, 64 * kWaves, 0, stream>>>(p);
-  else attention_tile_kernel<BF, D, false, false><<<grid, 64 * kWaves, 0, stream>>>(p);
+  const auto run = [&](auto kernel) { kernel<<<grid, 64 * kWaves, 0, stream>>>(p); };
+  switch (cap_kind(a.softcap)) {
+    case kNoCap: run(a.slopes ? attention_tile_kernel<BF, D, kNoCap, true> : attention_tile_kernel<BF, D, kNoCap, false>); break;
+    case kSmallCap: run(a.slopes ? attention_tile_kernel<BF, D, kSmallCap, true> : attention_tile_kernel<BF, D, kSmallCap, false>); break;
+    case kAnyCap: run(a.slopes ? attention_tile_kernel<BF, D, kAnyCap, true> : attention_tile_kernel<BF, D, kAnyCap, false>); break;
+  }
   return hipGetLastError();
 }
 
@@ -771,7 +795,12 @@ hipError_t launch_split(const AttentionArgs& a, hipStream_t stream) {
   }
   const long long units = (long long)a.B * a.Hkv * plan.split, blocks = (units + 7) / 8 * 8 * plan.rtiles;
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
-  attention_split_kernel<BF, D><<<dim3((unsigned)blocks), 64 * kWaves, 0, stream>>>(p);
+  const auto run = [&](auto kernel) { kernel<<<dim3((unsigned)blocks), 64 * kWaves, 0, stream>>>(p); };
+  switch (cap_kind(a.softcap)) {
+    case kNoCap: run(attention_split_kernel<BF, D, kNoCap>); break;
+    case kSmallCap: run(attention_split_kernel<BF, D, kSmallCap>); break;
+    case kAnyCap: run(attention_split_kernel<BF, D, kAnyCap>); break;
+  }
   return hipGetLastError();
 }
 
