@@ -133,28 +133,40 @@ __global__ void __launch_bounds__(64 * WAVES) route_kernel(RouteArgs a) {
 
 // ---- codes as matrix operands --------------------------------------------------------
 
-// Eight codes of lane group j, in decode8's element order, as 16-bit numbers:
-// fp16: q 2^-24 (a subnormal half, exact); bf16: 128 + q for up to 4 bits (the
-// code in the mantissa's low bits), q for 8 bits (exact in 8 significant bits).
+// Eight codes of lane group j, in decode8's element order, as 16-bit numbers. bf16:
+// 128 + q for up to 4 bits (the code in the mantissa's low bits), q for 8 bits (exact in
+// 8 significant bits). fp16: q 2^(kPlace - 24), the code at bits kPlace on of a half whose
+// bits up to 10 read as a plain number (subnormals, and the first normals behind them).
+//
+// The matrix cores place a product by its operands' exponent fields: of the products of
+// a subnormal with nine leading zeros nine bits are cut off at the far end, always
+// downwards (sums of 4096 products with codes 0 and 1 at 2^-24: 4.6e-5 off, all to one
+// side; at 2^-20 4.2e-7; at 2^-15 and above 7e-8, a rounding in fp32). So the code goes
+// as far up as it gets without another operation, and at the top for the narrow ones.
 //
 // The masks are made once and kept in vector registers, the bits put around the code
 // (nothing for fp16) in a scalar one, so that inserting is one operation.
+template <int BITS, bool BF> constexpr int kPlace = BF || BITS == 8 ? 0 : BITS == 4 ? 4 : 11 - BITS;
 template <int BITS, bool BF> struct CodeMasks {
   uint32_t code, low, around;
   __device__ __forceinline__ CodeMasks()
-      : code(BITS == 4 ? 0x000F000Fu : BITS == 3 ? 0x00060006u : BITS == 2 ? 0x00030003u : 0x00010001u), low(0x00010001u),
-        around(BF ? 0x43004300u : 0u) {
+      : code((BITS == 4 ? 0x000F000Fu : BITS == 3 ? 0x00060006u : BITS == 2 ? 0x00030003u : 0x00010001u) << kPlace<BITS, BF>),
+        low(0x00010001u << kPlace<BITS, BF>), around(BF ? 0x43004300u : 0u) {
     if (BITS != 8) asm("" : "+v"(code));
     if (BITS == 3) asm("" : "+v"(low));
     if (BF && BITS != 8) asm("" : "+s"(around));
   }
 };
+__device__ __forceinline__ uint32_t rotate_right(uint32_t w, int n) { return __builtin_amdgcn_alignbit(w, w, (uint32_t)n); }  // by n mod 32
+// w moved up by n bits, down for n < 0.
+__device__ __forceinline__ uint32_t moved_up(uint32_t w, int n) { return n >= 0 ? w << n : w >> -n; }
 template <int BITS, bool BF>
 __device__ __forceinline__ u32x4 codes8(uint32_t w0, uint32_t w1, int j, const CodeMasks<BITS, BF>& m) {
+  constexpr int PLACE = kPlace<BITS, BF>;
   u32x4 b;
   if constexpr (BITS == 4) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) b[p] = ((w0 >> (4 * p)) & m.code) | m.around;
+    for (int p = 0; p < 4; ++p) b[p] = (moved_up(w0, PLACE - 4 * p) & m.code) | m.around;
   } else if constexpr (BITS == 8) {
     if constexpr (BF) {
 #pragma unroll
@@ -170,19 +182,21 @@ __device__ __forceinline__ u32x4 codes8(uint32_t w0, uint32_t w1, int j, const C
       b[3] = __builtin_amdgcn_perm(0u, w1, 0x0C030C02u);
     }
   } else if constexpr (BITS == 2) {
-    const uint32_t t = w0 >> (8 * (j & 1));
+    // Pair p at bits 2 p of t, or (fp16) 2 p + 3: pair 3 is where it goes then.
+    const uint32_t t = BF ? w0 >> (8 * (j & 1)) : rotate_right(w0, 8 * (j & 1) - 3);
 #pragma unroll
-    for (int p = 0; p < 4; ++p) b[p] = ((t >> (2 * p)) & m.code) | m.around;
+    for (int p = 0; p < 4; ++p) b[p] = (moved_up(t, BF ? -2 * p : 6 - 2 * p) & m.code) | m.around;
   } else if constexpr (BITS == 3) {
-    const uint32_t h = w0 >> (8 * (j & 1));
+    const uint32_t h = BF ? w0 >> (8 * (j & 1)) : rotate_right(w0, 8 * (j & 1) - 3);
     const uint32_t t = w1 >> (16 * (j >> 1) + 4 * (j & 1));
-    const uint32_t l = __builtin_amdgcn_perm(0u, t, 0x0C010C00u);  // bytes (0, -, 1, -) of t
+    const uint32_t l = __builtin_amdgcn_perm(0u, t, BF ? 0x0C010C00u : 0x010C000Cu);  // byte 0 of t in one half, 1 in the other
 #pragma unroll
-    for (int p = 0; p < 4; ++p) b[p] = ((l >> p) & m.low) | (((p == 0 ? h << 1 : h >> (2 * p - 1)) & m.code) | m.around);
+    for (int p = 0; p < 4; ++p) b[p] = ((l >> p) & m.low) | ((moved_up(h, BF ? 1 - 2 * p : 6 - 2 * p) & m.code) | m.around);
   } else {
-    const uint32_t t = (w0 >> (8 * j)) & 0xFFu, both = t | (t << 12);  // slots p and p + 4 sixteen bits apart
+    // Slots p and p + 4 sixteen bits apart, p at bit p, or (fp16) 7 + p.
+    const uint32_t t = BF ? (w0 >> (8 * j)) & 0xFFu : rotate_right(w0, 8 * j - 7) & 0x7F80u, both = t | (t << 12);
 #pragma unroll
-    for (int p = 0; p < 4; ++p) b[p] = ((both >> p) & m.code) | m.around;
+    for (int p = 0; p < 4; ++p) b[p] = (moved_up(both, BF ? -p : 3 - p) & m.code) | m.around;
   }
   return b;
 }
@@ -260,7 +274,7 @@ template <int BITS, bool BF, bool SBF, int COLS, Groups G>
 __device__ __forceinline__ void chunk_product(f32x4 (&total)[COLS], const u32x4 (&a)[kUnits], const Chunk<BITS>* const (&w)[COLS], int c,
                                               int upg, FixedDiv by_upg, int j, int n, const CodeMasks<BITS, BF>& masks) {
   constexpr uint32_t kOne = BF ? 0x3F803F80u : 0x3C003C00u;
-  constexpr float kUp = BF ? 1.f : 16777216.f;
+  constexpr float kUp = BF ? 1.f : 1 << (24 - kPlace<BITS, BF>);
   f32x4 acc[COLS] = {}, as = {};
   int in_group = G == kAnywhere ? c * kUnits - by_upg(c * kUnits) * upg : 0;
 #pragma unroll
