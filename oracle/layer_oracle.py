@@ -29,13 +29,13 @@ def moe_route(x, router, top_k, renormalize):
     return ids, chosen / (chosen if renormalize else e).sum(axis=1, keepdims=True), logits
 
 
-def expert_weight(planes, e, K, bits, group_size):
-    """Expert e's dequantised weight (K, N) and |s| (q + |z| + 128), which bounds what a kernel may form of a code."""
+def expert_weight(planes, e, K, bits, group_size, offset=128.0):
+    """Expert e's dequantised weight (K, N) and |s| (q + |z| + offset), which bounds what a kernel may form of a code."""
     qw, qlo, zeros, scales = planes
     codes = unpack(qw[e], None if qlo is None else qlo[e], bits, K)
     s, z = scales[e].astype(np.float64), zeros[e].astype(np.float64)
     g = np.zeros(K, int) if group_size == -1 else np.arange(K) // group_size
-    return s[g] * (codes.astype(np.float64) - z[g]), np.abs(s[g]) * (codes + np.abs(z[g]) + 128.0)
+    return s[g] * (codes.astype(np.float64) - z[g]), np.abs(s[g]) * (codes + np.abs(z[g]) + offset)
 
 
 def silu(g):
@@ -71,7 +71,7 @@ def rounded(v, dtype):
     return v.astype(np.float16).astype(np.float64) if dtype == "fp16" else bf16_to_f64(f64_to_bf16(v))
 
 
-def moe_hidden(x, ids, gate_up, bits, group_size):
+def moe_hidden(x, ids, gate_up, bits, group_size, offset=128.0):
     """h of every (token, choice), (T, top_k, I), and per choice the root mean square of a weight and of what a
     kernel may form of one (0 for a choice outside)."""
     x = x.astype(np.float64)
@@ -81,7 +81,7 @@ def moe_hidden(x, ids, gate_up, bits, group_size):
     for e in np.unique(ids):
         if not 0 <= e < len(gate_up[0]):
             continue
-        w, formed = expert_weight(gate_up, e, x.shape[1], bits, group_size)
+        w, formed = expert_weight(gate_up, e, x.shape[1], bits, group_size, offset)
         t, j = np.nonzero(ids == e)
         both = x[t] @ w
         h[t, j] = silu(both[:, :I]) * both[:, I:]
@@ -108,10 +108,10 @@ def moe_norm(x, ids, weights, gate_up, down, bits, group_size, dtype):
 
     Four independent parts. The result's rounding: that of y itself. h in 16 significant bits: 2^-17 of each. The
     fp32 sums of the two products: a chain of up to 128 sums of formed weights (code, zero point and a kernel's offset
-    of up to 128) in random directions errs by 2^-24 of each partial sum, together 2^-24 sqrt(128^2 / 2) of one term
+    of up to 128; none in the gate and up products of fp16 data, whose codes are halves as they are) in random directions errs by 2^-24 of each partial sum, together 2^-24 sqrt(128^2 / 2) of one term
     where the products' sum is sqrt(128) of one, so 8 2^-24 of the ratio of formed weights to weights; g and u pass
     that on with a slope of 1.1 and 1, so 1.5 times. A tenth on top for what random directions leave open."""
-    h, sizes = moe_hidden(x, ids, gate_up, bits, group_size)
+    h, sizes = moe_hidden(x, ids, gate_up, bits, group_size, 0.0 if dtype == "fp16" else 128.0)
     y, down_ratio = moe_down(h, ids, weights, down, bits, group_size)
     gate_ratio = np.max(sizes[..., 1] / np.maximum(sizes[..., 0], 1e-300))
     own = np.linalg.norm(rounded(y, dtype) - y) / np.linalg.norm(y)
