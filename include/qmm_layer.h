@@ -139,7 +139,8 @@ qmm_status qmm_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* k,
  *   k_cache, v_cache as above; page_table (B, table_stride) int32: page of tokens
  *           [i page_size, (i + 1) page_size) of sequence b at [b, i]
  *   kv_lens (B,), q_starts (B + 1,), first, end (T,) int32; slopes (Hq,) fp32
- *   max_q, max_kv: no sequence has more queries and keys than these; further ones are left out
+ *   max_q, max_kv: bounds of the sequences' queries and keys. Of a sequence with more, the further
+ *           queries are left out and the further keys not seen; positions go by all of them
  * Query head h reads key head h / (Hq / Hkv). Scores, softmax and sums are fp32
  * (with a softcap of up to 64 a score may be off by softcap * 2^-22, with a larger
  * one by a few roundings of its own size);

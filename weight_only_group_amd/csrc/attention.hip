@@ -95,20 +95,35 @@ __device__ __forceinline__ ScoreRule score_rule(const AttentionArgs& a, int head
   return r;
 }
 
+// A sequence's query rows [q0, q1) and keys [0, kv) that take part, cut to the call's
+// bounds, and its first query's position, which goes by all its queries and keys.
+struct Span {
+  int q0, q1, kv, first;
+};
+__device__ __forceinline__ Span span_of(const AttentionArgs& a, int b) {
+  Span s;
+  s.q0 = min(max(a.q_starts[b], 0), a.T);
+  const int queries = min(max(a.q_starts[b + 1], s.q0), a.T) - s.q0, keys = max(a.kv_lens[b], 0);
+  s.q1 = s.q0 + min(queries, a.max_q);
+  s.kv = min(keys, a.max_kv);
+  s.first = keys - queries;
+  return s;
+}
+
 // One row's token (-1: none), head and range of keys.
 struct Row {
   int token, head, pos, lo, hi;
 };
-__device__ __forceinline__ Row row_of(const AttnKernelArgs& p, int r, int q0, int q1, int kv, int hk) {
+__device__ __forceinline__ Row row_of(const AttnKernelArgs& p, int r, const Span& s, int hk) {
   const AttentionArgs& a = p.a;
   Row w = {-1, 0, 0, 0, 0};
   const int i = p.by_group(r);
-  if (i >= q1 - q0) return w;
-  w.token = q0 + i;
+  if (i >= s.q1 - s.q0) return w;
+  w.token = s.q0 + i;
   w.head = hk * p.group + r - i * p.group;
-  w.pos = kv - (q1 - q0) + i;
+  w.pos = s.first + i;
   w.lo = a.first ? max(a.first[w.token], 0) : 0;
-  w.hi = max(min(a.end ? a.end[w.token] : w.pos + 1, kv), 0);  // not below 0: hi - lo does not overflow
+  w.hi = max(min(a.end ? a.end[w.token] : w.pos + 1, s.kv), 0);  // not below 0: hi - lo does not overflow
   return w;
 }
 
@@ -146,11 +161,10 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) attentio
   const int rt = w8 / 8, unit = blockIdx.x / per * 8 + w8 % 8;
   if (unit >= a.B * a.Hkv * p.split) return;
   const int part = unit % p.split, hk = unit / p.split % a.Hkv, b = unit / p.split / a.Hkv;
-  const int q0 = min(max(a.q_starts[b], 0), a.T), q1 = min(max(a.q_starts[b + 1], q0), min(a.T, q0 + a.max_q));
-  const int kv = min(max(a.kv_lens[b], 0), a.max_kv);
-  if (rt * kRows >= (q1 - q0) * p.group) return;
+  const Span span = span_of(a, b);
+  if (rt * kRows >= (span.q1 - span.q0) * p.group) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 15, kg = lane >> 4;
-  const Row row = row_of(p, rt * kRows + n, q0, q1, kv, hk);
+  const Row row = row_of(p, rt * kRows + n, span, hk);
   const ScoreRule rule = score_rule(a, row.head);
 
   // The keys that any row sees, and those that all see.
@@ -350,7 +364,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) attentio
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] += so[w][r][d0 + e] * f;
   }
-  const Row mine = row_of(p, rt * kRows + r, q0, q1, kv, hk);
+  const Row mine = row_of(p, rt * kRows + r, span, hk);
   if (p.split > 1) {
     // Partial sums of the parts, joined in order by the block that arrives last.
     const size_t tile = ((size_t)b * a.Hkv + hk) * p.rtiles + rt;
@@ -457,12 +471,11 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
   const int rt = p.rtiles - 1 - w8 / 8, unit = blockIdx.x / per * 8 + w8 % 8;  // the longest rows of a causal mask first
   if (unit >= a.B * a.Hkv) return;
   const int hk = unit % a.Hkv, b = unit / a.Hkv;
-  const int q0 = min(max(a.q_starts[b], 0), a.T), q1 = min(max(a.q_starts[b + 1], q0), min(a.T, q0 + a.max_q));
-  const int kv = min(max(a.kv_lens[b], 0), a.max_kv);
-  if ((long long)rt * kTileRows >= (long long)(q1 - q0) * p.group) return;
+  const Span span = span_of(a, b);
+  if ((long long)rt * kTileRows >= (long long)(span.q1 - span.q0) * p.group) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 31, kg = lane >> 5;
   const int r0 = rt * kTileRows + wave * 32;
-  const Row row = row_of(p, r0 + n, q0, q1, kv, hk);
+  const Row row = row_of(p, r0 + n, span, hk);
   // A negative scale turns the queries' signs instead: products are then in the scores' order.
   ScoreRule rule = score_rule(a, row.head);
   const uint32_t q_sign = rule.scale < 0 ? 0x80008000u : 0u;
@@ -715,7 +728,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
   const float inv = row.lo < row.hi ? 1 / sum : 0.f;
   __syncthreads();
   float* so = reinterpret_cast<float*>(&kvs[0][0][0]) + wave * 32 * LDO;
-  const Row mine = row_of(p, r0 + (lane >> 1), q0, q1, kv, hk);
+  const Row mine = row_of(p, r0 + (lane >> 1), span, hk);
   // Rare: dimensions 32 m on of the steps left out above, key by key, with their scores anew.
   auto add_left_out = [&](int m) {
     for (int t = t0; t < t1; ++t) {
