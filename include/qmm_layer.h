@@ -141,6 +141,8 @@ qmm_status qmm_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* k,
  *   kv_lens (B,), q_starts (B + 1,), first, end (T,) int32; slopes (Hq,) fp32
  *   max_q, max_kv: bounds of the sequences' queries and keys. Of a sequence with more, the further
  *           queries are left out and the further keys not seen; positions go by all of them
+ * A token that is left out, or of no sequence (before the first, behind the last: q_starts must
+ * not fall), gets 0. With B or max_q 0 nothing is written.
  * Query head h reads key head h / (Hq / Hkv). Scores, softmax and sums are fp32
  * (with a softcap of up to 64 a score may be off by softcap * 2^-22, with a larger
  * one by a few roundings of its own size);

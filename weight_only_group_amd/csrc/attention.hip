@@ -110,6 +110,25 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& a, int b) {
   return s;
 }
 
+// Zeroes one key head's results of the tokens that no row stands for: those of sequence
+// b past its bound, and those before the first sequence and behind the last. Shared out
+// over `workers` blocks of 256 threads; as a rule there are none.
+template <int D>
+__device__ __forceinline__ void zero_rest(const AttnKernelArgs& p, const Span& s, int b, int hk, int worker, int workers) {
+  const AttentionArgs& a = p.a;
+  const int next = b + 1 < a.B ? min(max(a.q_starts[b + 1], 0), a.T) : a.T;
+  if (next <= s.q1 && (b > 0 || s.q0 == 0)) return;
+  const int pieces = p.group * D / 8;  // of 16 bytes, per token
+  auto zero = [&](int from, int to) {
+    for (long long i = worker * 256ll + threadIdx.x; i < (long long)(to - from) * pieces; i += workers * 256ll) {
+      const long long t = from + i / pieces;
+      *reinterpret_cast<u32x4*>(a.out + (t * a.Hq + hk * p.group) * D + i % pieces * 8) = u32x4{0, 0, 0, 0};
+    }
+  };
+  zero(s.q1, next);
+  if (b == 0) zero(0, s.q0);
+}
+
 // One row's token (-1: none), head and range of keys.
 struct Row {
   int token, head, pos, lo, hi;
@@ -162,6 +181,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) attentio
   if (unit >= a.B * a.Hkv * p.split) return;
   const int part = unit % p.split, hk = unit / p.split % a.Hkv, b = unit / p.split / a.Hkv;
   const Span span = span_of(a, b);
+  zero_rest<D>(p, span, b, hk, rt * p.split + part, p.rtiles * p.split);
   if (rt * kRows >= (span.q1 - span.q0) * p.group) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 15, kg = lane >> 4;
   const Row row = row_of(p, rt * kRows + n, span, hk);
@@ -472,6 +492,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
   if (unit >= a.B * a.Hkv) return;
   const int hk = unit % a.Hkv, b = unit / a.Hkv;
   const Span span = span_of(a, b);
+  zero_rest<D>(p, span, b, hk, rt, p.rtiles);
   if ((long long)rt * kTileRows >= (long long)(span.q1 - span.q0) * p.group) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 31, kg = lane >> 5;
   const int r0 = rt * kTileRows + wave * 32;

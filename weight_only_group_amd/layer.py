@@ -235,7 +235,7 @@ def qmm_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q: int
     """Attention of the queries q (T, Hq, D) to the cached keys of their sequences. Sequence b has the
     rows q_starts[b] to q_starts[b + 1] and kv_lens[b] cached tokens, its new ones the last. A query at
     position p sees the keys from ``first`` (default 0) up to, without, ``end`` (default p + 1); one that
-    sees none gets 0. ``scale`` defaults to 1 / sqrt(D); ``softcap`` c > 0 takes c tanh(s / c) of the
+    sees none gets 0, and so does a token of no sequence. ``scale`` defaults to 1 / sqrt(D); ``softcap`` c > 0 takes c tanh(s / c) of the
     scores; ``slopes`` (Hq,) subtract slope * |p - key position|. max_q and max_kv bound the lengths."""
     dt = _qmm._data_dtype(q, "q")
     T, Hq, D, qs = _heads(q, "q", dt)
@@ -252,6 +252,8 @@ def qmm_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q: int
     if slopes is not None:
         _array(slopes, "slopes", torch.float32, (Hq,), dev)
     out = _result(out, q, (T, Hq, D))
+    if B == 0 or max_q == 0:  # tokens of no sequence: the call writes nothing then
+        out.zero_()
     args = (_p(q), qs, T, Hq, Hkv, D, _p(k_cache), _p(v_cache), pages, page_size, _p(page_table), table_stride,
             _p(kv_lens), _p(q_starts), B, max_q, max_kv, _p(first), _p(end), 1.0 / math.sqrt(D) if scale is None else scale,
             softcap, _p(slopes), QMM_BF16 if dt == torch.bfloat16 else 0, _p(out))
