@@ -346,12 +346,14 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(LogprobKernelArgs
     }
   }
 
-  const float ln_s = logf(sum.s), lse = sum.m + ln_s;
+  // l - lse as (l - m) - ln S: m + ln S would be rounded to m's size, 5e-4 for logits of 1e4.
+  const float ln_s = logf(sum.s);
+  auto log_prob = [&](long long i) { return (load_logit<TYPE>(row, i) - sum.m) - ln_s; };
   if (tid == 0) {
     a.entropy[m] = ln_s - kLn2 * sum.a / sum.s;
     if (a.targets) {
       const int64_t t = a.targets[m];
-      a.logprob[m] = t < 0 ? 0.f : t >= a.V ? NAN : load_logit<TYPE>(row, t) - lse;
+      a.logprob[m] = t < 0 ? 0.f : t >= a.V ? NAN : log_prob(t);
     }
   }
   if (top > 0 && !(sum.s == sum.s && sum.s > 0)) {
@@ -376,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(LogprobKernelArgs
   if (tid < top) {
     const int id = key_index(best[tid]);
     a.top_ids[(size_t)m * top + tid] = id;
-    a.top_logprobs[(size_t)m * top + tid] = load_logit<TYPE>(row, id) - lse;
+    a.top_logprobs[(size_t)m * top + tid] = log_prob(id);
   }
 }
 
