@@ -257,21 +257,59 @@ def gemm_plan_info(M: int, K: int, N: int, bits: int, group_size: int) -> dict:
     return dict(zip(GEMM_PLAN_FIELDS, list(info)))
 
 
-# Zero-filled GEMV workspaces, one per (device, stream); the kernels leave their
+# Zero-filled workspaces, one per (device, stream); the kernels leave their
 # counters at zero, so a workspace is reused call after call on its stream.
 _workspaces: dict = {}
+# The workspaces of the captures that streams are in: (device, stream) -> (capture id, tensor).
+_captured: dict = {}
+WORKSPACE_HEADER = 128 << 10  # bytes of arrival counters at its start: all that has to be zero
+
+
+def _capture_id(stream: int):
+    """Which graph capture the stream is in (None: in none)."""
+    status, ident = ctypes.c_int(), ctypes.c_ulonglong()
+    err = library().hipStreamGetCaptureInfo(ctypes.c_void_p(stream), ctypes.byref(status), ctypes.byref(ident))
+    if err:
+        raise RuntimeError(f"hipStreamGetCaptureInfo failed ({err})")
+    return ident.value if status.value == 1 else None  # hipStreamCaptureStatusActive
 
 
 def gemv_workspace(device, nbytes: int, stream=None) -> torch.Tensor | None:
+    """The workspace of the calls that are given none, for the current stream (or ``stream``) of the device.
+
+    Outside a graph capture one buffer per stream, zero-filled once, replaced by a larger one as calls need it. A
+    capture has its own, from the graph's memory, whose counters the graph itself zeroes ahead of the first call that
+    uses it: replays neither touch the stream's buffer nor depend on what it was when the graph was captured."""
     if nbytes == 0:
         return None
     dev = torch.device(device)
     s = torch.cuda.current_stream(dev) if stream is None else stream
-    key = (dev.index, s.cuda_stream)
+    key = (s.device.index, s.cuda_stream)
+    capture = _capture_id(s.cuda_stream) if s.cuda_stream else None  # (the null stream cannot be captured)
+    if capture is not None:
+        of, ws = _captured.get(key, (None, None))
+        if of != capture or ws.numel() < nbytes:
+            with torch.cuda.stream(s):
+                ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=s.device)
+                ws[:WORKSPACE_HEADER].zero_()
+            _captured[key] = (capture, ws)
+        return ws
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
+        with torch.cuda.stream(s):
+            ws = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=s.device)
         _workspaces[key] = ws
+    return ws
+
+
+def _given_workspace(ws, dev):
+    """A workspace that the caller gave: kernels write to it, so it has to be dense memory of the call's device."""
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if ws.device != dev:
+        raise ValueError(f"workspace must be on {dev} (got {ws.device})")
+    if not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     return ws
 
 
@@ -335,7 +373,7 @@ def qmm_gemv(x, qweight, qweight_lo, zeros, scales, bits: int, group_size: int, 
     dev = x.device
     y = _output(out, M, N, dt, dev)
     nbytes = workspace_bytes(M, K, N, bits, group_size) if M <= GEMV_MAX_M else 0
-    ws = workspace if workspace is not None else gemv_workspace(dev, nbytes)
+    ws = gemv_workspace(dev, nbytes) if workspace is None else _given_workspace(workspace, dev)
     with torch.cuda.device(dev):
         args = (_ptr(x), M, K, _ptr(qweight), _ptr(qweight_lo), _ptr(zeros), _ptr(scales), _ptr(bias), N, bits,
                 group_size)

@@ -9,7 +9,8 @@ marshalling over libqmm, in the manner of the products' binding.
 
 Work runs on the current stream of the tensors' device; results are new
 tensors unless ``out`` arguments are given. The workspace is the decode
-product's, one per device and stream, unless one is passed.
+product's, one per device and stream (in a graph capture one of the graph's
+own), unless one is passed; calls that share one must not overlap in time.
 """
 from __future__ import annotations
 
@@ -93,10 +94,12 @@ def _launch(name, dev, args, out=(), workspace=None, shape=None):
             return _launch(name, dev, args, out, workspace, shape)
     stream = torch._C._cuda_getCurrentRawStream(here)
     if shape is not None:
-        if workspace is None:
-            need = _need(name, here, *shape)
-            workspace = _qmm._workspaces.get((here, stream))
-            if need and (workspace is None or workspace.numel() < need):
+        if workspace is not None:
+            _qmm._given_workspace(workspace, dev)
+        elif need := _need(name, here, *shape):
+            if not torch.cuda.is_current_stream_capturing():
+                workspace = _qmm._workspaces.get((here, stream))
+            if workspace is None or workspace.numel() < need:
                 workspace = _qmm.gemv_workspace(dev, need)
         if workspace is None:
             args += (None, 0, stream)
