@@ -36,7 +36,7 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int max_q, int max_kv, DeviceTopo top
   p.rtiles = (int)(((long long)max_q * p.group + kRows - 1) / kRows);
   p.tiles = (size_t)B * Hkv * p.rtiles;
   const long long want = 4ll * topo.cus / (long long)p.tiles;
-  const long long most = (max_kv + kWaves * kChunk - 1) / (kWaves * kChunk);
+  const long long most = (max_kv + kWaves * kChunk - 1ll) / (kWaves * kChunk);
   p.split = (int)(want < most ? want : most);
   if (p.split > kMaxSplit) p.split = kMaxSplit;
   if (p.split < 1 || p.tiles > (size_t)kGemvMaxStrips) p.split = 1;
@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) attentio
   hi = __builtin_amdgcn_readfirstlane(hi);
   all_lo = __builtin_amdgcn_readfirstlane(all_lo);
   all_hi = __builtin_amdgcn_readfirstlane(all_hi);
-  const int c_first = lo < hi ? lo / kChunk : 0, chunks = lo < hi ? (hi + kChunk - 1) / kChunk - c_first : 0;
+  auto seen_by_all = [&](int c) { return c * kChunk >= all_lo && (uint32_t)(c + 1) * kChunk <= (uint32_t)all_hi; };
+  const int c_first = lo < hi ? lo / kChunk : 0, chunks = lo < hi ? (hi - 1) / kChunk + 1 - c_first : 0;
   const int c0 = c_first + (int)((long long)chunks * part / p.split), c1 = c_first + (int)((long long)chunks * (part + 1) / p.split);
 
   u32x4 q[STEPS];
@@ -212,8 +213,8 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) attentio
 
   // Row (of D values) of key lane & 31 of a chunk; keys past the last seen one repeat it.
   const int32_t* table = a.page_table + (long long)b * a.table_stride;
-  auto key_row = [&](int c) -> uint32_t {
-    const int j = min(max(c * kChunk + (lane & 31), lo), hi - 1);
+  auto key_row = [&](int c) -> uint32_t {  // (the chunks asked for ahead may lie past 2^31)
+    const int j = (int)min(max((uint32_t)c * kChunk + (lane & 31), (uint32_t)lo), (uint32_t)hi - 1);
     const int at = p.by_page(j);
     const int page = min(max(table[at], 0), a.pages - 1);
     return ((uint32_t)page * a.Hkv + hk) * a.page_size + (j - at * a.page_size);
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) attentio
     }
     // Scores: keys 32c + 16t + 4kg + r of row n.
     const int j0 = c * kChunk + 4 * kg;
-    const bool whole = c * kChunk >= all_lo && (c + 1) * kChunk <= all_hi;  // seen by every row
+    const bool whole = seen_by_all(c);
     float s[8], best = -INFINITY;
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) attentio
   if (any_bad) {
     // Rare: the values left out above, to the rows that see them.
     for (int c = c0 + wave; c < c1; c += kWaves) {
-      if (c * kChunk >= all_lo && (c + 1) * kChunk <= all_hi) continue;
+      if (seen_by_all(c)) continue;
       const uint32_t here = key_row(c);
       for (int key = 0; key < kChunk; ++key) {
         const int j = c * kChunk + key;
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
   for (int w = 0; w < kWaves; ++w) block_lo = min(block_lo, range[0][w]), block_hi = max(block_hi, range[1][w]);
   block_lo = __builtin_amdgcn_readfirstlane(block_lo);
   block_hi = __builtin_amdgcn_readfirstlane(block_hi);
-  const int t0 = block_lo < block_hi ? block_lo / BN : 0, t1 = block_lo < block_hi ? (block_hi + BN - 1) / BN : 0;
+  const int t0 = block_lo < block_hi ? block_lo / BN : 0, t1 = block_lo < block_hi ? (block_hi - 1) / BN + 1 : 0;
 
   u32x4 q[STEPS];
 #pragma unroll
@@ -538,13 +539,13 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
   // Reordering of row r's pieces.
   auto turn = [](int r) { return D == 64 ? ((r >> 1) & 1) << 2 | ((r >> 2) & 3) : (r & 3) << 2 | ((r >> 2) & 3); };
   const int32_t* table = a.page_table + (long long)b * a.table_stride;
-  auto key_row = [&](int j) -> uint32_t {  // keys past those seen repeat the nearest
-    j = min(max(j, block_lo), block_hi - 1);
+  auto key_row = [&](uint32_t key) -> uint32_t {  // keys past those seen repeat the nearest
+    const int j = (int)min(max(key, (uint32_t)block_lo), (uint32_t)block_hi - 1);
     const int at = p.by_page(j);
     const int page = min(max(table[at], 0), a.pages - 1);
     return ((uint32_t)page * a.Hkv + hk) * a.page_size + (j - at * a.page_size);
   };
-  auto own_rows = [&](int t) { return key_row(t * BN + wave * OWN + (lane & (OWN - 1))); };
+  auto own_rows = [&](int t) { return key_row((uint32_t)t * BN + wave * OWN + (lane & (OWN - 1))); };
   auto load_tile = [&](int buf, uint32_t rows) {
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
@@ -555,6 +556,9 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
       load_to_lds(lds_offset(kvs[buf][1]) + to, a.v_cache + at);
     }
   };
+  // Whether none of the wave's rows sees a key of the step that starts at key0, and whether all see all.
+  auto seen_by_none = [&](int key0) { return (uint32_t)key0 + BN <= (uint32_t)lo || key0 >= hi; };
+  auto seen_by_all = [&](int key0) { return key0 >= all_lo && (uint32_t)key0 + BN <= (uint32_t)all_hi; };
   // Byte offsets of this lane's reads: keys' pieces per step, values' per 32 dimensions and four keys.
   uint32_t k_at[STEPS], v_at[MT][2];
 #pragma unroll
@@ -586,7 +590,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
       rows = own_rows(t + 2);
     }
     const int key0 = t * BN;
-    if (key0 + BN <= lo || key0 >= hi) continue;  // nothing for this wave's rows
+    if (seen_by_none(key0)) continue;
     const char* ks = reinterpret_cast<const char*>(kvs[t & 1][0]);
     const char* vs = reinterpret_cast<const char*>(kvs[t & 1][1]);
     // Products of keys and queries, the keys' pieces read kAhead steps before.
@@ -606,7 +610,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
 #pragma unroll
       for (int u = 0; u < SUB; ++u) st[u] = mfma32<BF>(kf[s % (kAhead + 1)][u], q[s], st[u]);
     }
-    const bool whole = key0 >= all_lo && key0 + BN <= all_hi;
+    const bool whole = seen_by_all(key0);
     auto key_of = [&](int u, int i) { return key0 + 32 * u + 8 * (i >> 2) + 4 * kg + (i & 3); };
     // The largest score of the row; where a score is more than a multiply-add or a small cap of its
     // product the scores are taken first, else only that of the largest product.
@@ -757,7 +761,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
   auto add_left_out = [&](int m) {
     for (int t = t0; t < t1; ++t) {
       const int key0 = t * BN;
-      if (key0 + BN <= lo || key0 >= hi || (key0 >= all_lo && key0 + BN <= all_hi)) continue;
+      if (seen_by_none(key0) || seen_by_all(key0)) continue;
       const uint32_t here = key_row(key0 + (lane & (BN - 1)));
       bool bad = false;
       for (int d = lane / BN; d < D; d += 64 / BN) bad |= not_finite<BF>(a.v_cache[(size_t)here * D + d]);
