@@ -152,7 +152,8 @@ qmm_status qmm_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* k,
  * == 0 and >= Hq * D; scale and softcap finite, softcap >= 0; q, out, caches
  * and workspace 16-byte aligned, the int32 and fp32 arrays 4-byte;
  * max_kv <= table_stride * page_size < 2^31, T * Hq and max_q * Hq < 2^31, B <=
- * 65535, pages * Hkv * page_size < 2^31. Flags: QMM_BF16.
+ * 65535, pages * Hkv * page_size < 2^31, and B * Hkv * (max_q * Hq / Hkv / 16 + 1)
+ * below 2^24 (with more than 64 query rows per key head an eighth of it). Flags: QMM_BF16.
  * Page ids are cut to [0, pages). Equal inputs give equal bits.
  */
 size_t qmm_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int max_q, int max_kv);

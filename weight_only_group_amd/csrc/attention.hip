@@ -30,10 +30,14 @@ struct AttnPlan {
   size_t tiles;  // all row tiles
 };
 
+int row_tiles(int max_q, int group, int rows) { return (int)(((long long)max_q * group + rows - 1) / rows); }
+// Blocks of a grid with `rtiles` row tiles for each of B * per units, which come in eights.
+long long tile_blocks(int B, int per, int rtiles) { return ((long long)B * per + 7) / 8 * 8 * rtiles; }
+
 AttnPlan attn_plan(int B, int Hq, int Hkv, int max_q, int max_kv, DeviceTopo topo) {
   AttnPlan p;
   p.group = Hq / Hkv;
-  p.rtiles = (int)(((long long)max_q * p.group + kRows - 1) / kRows);
+  p.rtiles = row_tiles(max_q, p.group, kRows);
   p.tiles = (size_t)B * Hkv * p.rtiles;
   const long long want = 4ll * topo.cus / (long long)p.tiles;
   const long long most = (max_kv + kWaves * kChunk - 1ll) / (kWaves * kChunk);
@@ -812,11 +816,9 @@ bool use_tiles(int B, int Hq, int Hkv, int max_q, DeviceTopo topo) {
 
 template <bool BF, int D>
 hipError_t launch_tiles(const AttentionArgs& a, hipStream_t stream) {
-  const int group = a.Hq / a.Hkv, rtiles = (int)(((long long)a.max_q * group + kTileRows - 1) / kTileRows);
+  const int group = a.Hq / a.Hkv, rtiles = row_tiles(a.max_q, group, kTileRows);
   const AttnKernelArgs p = {a, fixed_div(a.page_size), fixed_div(group), group, rtiles, 1, nullptr, nullptr, nullptr};
-  const long long blocks = ((long long)a.B * a.Hkv + 7) / 8 * 8 * rtiles;
-  if (blocks > INT32_MAX) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)blocks);
+  const dim3 grid((unsigned)tile_blocks(a.B, a.Hkv, rtiles));
   const auto run = [&](auto kernel) { kernel<<<grid, 64 * kWaves, 0, stream>>>(p); };
   switch (cap_kind(a.softcap)) {
     case kNoCap: run(a.slopes ? attention_tile_kernel<BF, D, kNoCap, true> : attention_tile_kernel<BF, D, kNoCap, false>); break;
@@ -834,9 +836,8 @@ hipError_t launch_split(const AttentionArgs& a, hipStream_t stream) {
     p.part = reinterpret_cast<float*>(a.workspace + kWorkspaceHeader);
     p.part_ml = p.part + plan.tiles * plan.split * kRows * D;
   }
-  const long long units = (long long)a.B * a.Hkv * plan.split, blocks = (units + 7) / 8 * 8 * plan.rtiles;
-  if (blocks > INT32_MAX) return hipErrorInvalidValue;
-  const auto run = [&](auto kernel) { kernel<<<dim3((unsigned)blocks), 64 * kWaves, 0, stream>>>(p); };
+  const dim3 grid((unsigned)tile_blocks(a.B, a.Hkv * plan.split, plan.rtiles));
+  const auto run = [&](auto kernel) { kernel<<<grid, 64 * kWaves, 0, stream>>>(p); };
   switch (cap_kind(a.softcap)) {
     case kNoCap: run(attention_split_kernel<BF, D, kNoCap>); break;
     case kSmallCap: run(attention_split_kernel<BF, D, kSmallCap>); break;
@@ -851,6 +852,13 @@ size_t attention_workspace(int B, int T, int Hq, int Hkv, int D, int max_q, int 
   if (use_tiles(B, Hq, Hkv, max_q, device_topology())) return 0;
   const AttnPlan p = attn_plan(B, Hq, Hkv, max_q, max_kv, device_topology());
   return p.split > 1 ? kWorkspaceHeader + p.tiles * p.split * kRows * (D + 2) * sizeof(float) : 0;
+}
+
+long long attention_blocks(int B, int Hq, int Hkv, int max_q, int max_kv) {
+  const DeviceTopo topo = device_topology();
+  if (use_tiles(B, Hq, Hkv, max_q, topo)) return tile_blocks(B, Hkv, row_tiles(max_q, Hq / Hkv, kTileRows));
+  const AttnPlan p = attn_plan(B, Hq, Hkv, max_q, max_kv, topo);
+  return tile_blocks(B, Hkv * p.split, p.rtiles);
 }
 
 template <bool BF>

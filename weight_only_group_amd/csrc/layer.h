@@ -71,6 +71,7 @@ struct AttentionArgs {
   int T, Hq, Hkv, D, pages, page_size, table_stride, B, max_q, max_kv;
   float scale, softcap;
 };
+long long attention_blocks(int B, int Hq, int Hkv, int max_q, int max_kv);  // of the grid
 size_t attention_workspace(int B, int T, int Hq, int Hkv, int D, int max_q, int max_kv);
 hipError_t launch_attention(const AttentionArgs& a, bool bf16, hipStream_t stream);
 

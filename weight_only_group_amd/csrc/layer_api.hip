@@ -205,6 +205,10 @@ qmm_status qmm_attention(const uint16_t* q, int64_t q_stride, int T, int Hq, int
   if (table_stride < 1 || (long long)table_stride * page_size >= (1ll << 31) || max_kv > (long long)table_stride * page_size)
     return fail(QMM_ERR_SHAPE, "max_kv=%d must not exceed table_stride=%d * page_size=%d (below 2^31)", max_kv,
                 table_stride, page_size);
+  // A launch's threads (256 a block) are counted in 32 bits.
+  if (qmm::attention_blocks(B, Hq, Hkv, max_q, max_kv) >= (1ll << 24))
+    return fail(QMM_ERR_SHAPE, "B=%d, Hkv=%d and max_q=%d: 2^24 blocks and more; pass the long sequences in a call of their own", B,
+                Hkv, max_q);
   if (!q || !page_table || !kv_lens || !q_starts || !out) return fail(QMM_ERR_NULL, "a required pointer is NULL");
   if (!aligned16(q) || !aligned16(out)) return fail(QMM_ERR_ALIGN, "q and out must be 16-byte aligned");
   if (!aligned(page_table, 4) || !aligned(kv_lens, 4) || !aligned(q_starts, 4) || !aligned(first, 4) || !aligned(end, 4) ||

@@ -419,8 +419,19 @@ hipError_t launch_logprobs(const LogprobArgs& a, LogitType type, hipStream_t str
     p.sums = reinterpret_cast<float*>(a.workspace + kWorkspaceHeader);
     p.keys = reinterpret_cast<uint64_t*>(p.sums + (size_t)a.M * plan.split * 4);
   }
-  const dim3 grid((unsigned)(a.M * plan.split));
-  const auto run = [&](auto kernel) { kernel<<<grid, kThreads, 0, stream>>>(p); };
+  // A launch's threads are counted in 32 bits: more rows than this (never split) go in several.
+  constexpr int kMostRows = 1 << 22;
+  const auto run = [&](auto kernel) {
+    for (int m = 0; m < a.M; m += cmin(a.M - m, kMostRows)) {
+      p.l.logits = static_cast<const char*>(a.logits) + (long long)m * a.row_stride * logit_size(type);
+      p.l.targets = a.targets ? a.targets + m : nullptr;
+      p.l.logprob = a.targets ? a.logprob + m : nullptr;
+      p.l.entropy = a.entropy + m;
+      p.l.top_logprobs = a.top ? a.top_logprobs + (size_t)m * a.top : nullptr;
+      p.l.top_ids = a.top ? a.top_ids + (size_t)m * a.top : nullptr;
+      kernel<<<dim3((unsigned)(cmin(a.M - m, kMostRows) * plan.split)), kThreads, 0, stream>>>(p);
+    }
+  };
   if (type == LogitType::kFp32) run(plan.narrow ? logprobs_kernel<LogitType::kFp32, kNarrow> : logprobs_kernel<LogitType::kFp32, kWide>);
   else if (type == LogitType::kBf16) run(plan.narrow ? logprobs_kernel<LogitType::kBf16, kNarrow> : logprobs_kernel<LogitType::kBf16, kWide>);
   else run(plan.narrow ? logprobs_kernel<LogitType::kFp16, kNarrow> : logprobs_kernel<LogitType::kFp16, kWide>);
