@@ -18,6 +18,8 @@ namespace qmm {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// Exponents are cut here, where the power is 0 and times any sum of up to 2^30 finite.
+constexpr float kFar = -1e4f;
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 // Bytes of logits per thread and step: 64, or 16 where the blocks of the wider step
 // would leave CUs idle (one row of 32000 fp16: 10.6 us in 16 blocks, 11.6 us in 4).
@@ -110,7 +112,7 @@ struct Sums {
   float m, s, a;  // a in units of log2: sum p log2(p / e^0)
   __device__ __forceinline__ void join(const Sums& o) {
     const float n = fmaxf(m, o.m), off = n == -INFINITY ? 0.f : n;
-    const float d0 = fmaxf((m - off) * kLog2e, -1e30f), d1 = fmaxf((o.m - off) * kLog2e, -1e30f);
+    const float d0 = fmaxf((m - off) * kLog2e, kFar), d1 = fmaxf((o.m - off) * kLog2e, kFar);
     const float f0 = __builtin_amdgcn_exp2f(d0), f1 = __builtin_amdgcn_exp2f(d1);
     a = f0 * (a + d0 * s) + f1 * (o.a + d1 * o.s);
     s = f0 * s + f1 * o.s;
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(LogprobKernelArgs
     for (int i = 1; i < PER; ++i) lm = fmaxf(lm, l[i]);
     const float n = fmaxf(sum.m, lm), off = n == -INFINITY ? 0.f : n;
     if (n > sum.m) {
-      const float d = fmaxf((sum.m - off) * kLog2e, -1e30f), f = __builtin_amdgcn_exp2f(d);
+      const float d = fmaxf((sum.m - off) * kLog2e, kFar), f = __builtin_amdgcn_exp2f(d);
       sum.a = f * (sum.a + d * sum.s);
       sum.s *= f;
       sum.m = n;
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(LogprobKernelArgs
     for (int i = 0; i < PER; ++i) {
       const float d = (l[i] - off) * kLog2e, e = __builtin_amdgcn_exp2f(d);
       sum.s += e;
-      sum.a += e * fmaxf(d, -1e30f);  // 0 for a logit of -inf
+      sum.a += e * fmaxf(d, kFar);  // 0 for a logit of -inf
     }
     if (top == 0) continue;
     const uint64_t hot = __ballot(lm >= least_logit);
