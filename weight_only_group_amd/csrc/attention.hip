@@ -478,7 +478,7 @@ template <int D> constexpr int kTileKeys = D == 256 ? 32 : 64;  // keys per step
 // Block: 128 rows of one key head, all their keys in steps that go through two LDS
 // buffers, loaded straight from the cache a step ahead. Bound: the exponentials and
 // reciprocals (half the vector rate), above all with a cap, then the matrix cores: a
-// prompt of 8192 with a cap, 32/8 heads of 128, 680 us, 808 TFLOP/s. 32 rows a wave, so
+// prompt of 8192 with a cap, 32/8 heads of 128, 700 us, 786 TFLOP/s. 32 rows a wave, so
 // that two waves a SIMD fit the registers; 64 keys a step, 32 at D 256.
 //
 // As above K q^T is taken, whose result has a query per lane column: the softmax
@@ -806,9 +806,13 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) attention_tile_kernel(A
 }
 
 // Blocks of 128 rows where they are enough for a third of the CUs, else tiles of 16
-// split over the keys. A prompt of 8192 with a cap, 32/8 heads of 128: 680 us in blocks,
-// 2290 us in tiles; six documents of up to 2600 tokens, 24 heads of 64 (about 480
-// blocks, most of them short): 61 and 59 us.
+// split over the keys. The blocks' time over the tiles', causal prompts of 64 to 2048,
+// 32/8, 16/2 and 8/8 heads of 64, 128 and 256, 256 CUs: with 8 to 32 blocks 0.6 to 2.4,
+// above 1 in 23 cases of 27; with 64 0.4 to 1.4; with 128 0.3 to 1.2; with 256 and more
+// 0.3 to 0.7, a prompt of 8192 0.3. Few heads a key head are the tiles' side, many the
+// blocks'. Where most blocks are short the tiles win beyond that: six ragged sequences of
+// documents, 24 heads of 64, up to 2600 tokens 61 us in blocks, 55 in tiles; up to 512
+// tokens 15 and 9.
 bool use_tiles(int B, int Hq, int Hkv, int max_q, DeviceTopo topo) {
   const long long rows = (long long)max_q * (Hq / Hkv);
   return rows > 64 && (long long)B * Hkv * ((rows + kTileRows - 1) / kTileRows) * 3 >= topo.cus;
