@@ -283,9 +283,13 @@ def gemv_workspace(device, nbytes: int, stream=None) -> torch.Tensor | None:
     if nbytes == 0:
         return None
     dev = torch.device(device)
+    if stream is None and dev.index == torch._C._cuda_getDevice() and not torch.cuda.is_current_stream_capturing():
+        ws = _workspaces.get((dev.index, torch._C._cuda_getCurrentRawStream(dev.index)))
+        if ws is not None and ws.numel() >= nbytes:
+            return ws
     s = torch.cuda.current_stream(dev) if stream is None else stream
     key = (s.device.index, s.cuda_stream)
-    capture = _capture_id(s.cuda_stream) if s.cuda_stream else None  # (the null stream cannot be captured)
+    capture = _capture_id(s.cuda_stream) if s.cuda_stream else None  # (the null stream is never captured)
     if capture is not None:
         of, ws = _captured.get(key, (None, None))
         if of != capture or ws.numel() < nbytes:
