@@ -19,7 +19,9 @@ Functions mirror the C ABI (include/qmm.h):
 
 The operators of a decoder layer between the products (include/qmm_layer.h) are
 in ``layer`` and exported here: ``qmm_moe_route``, ``qmm_moe``, ``qmm_kv_append``,
-``qmm_attention``, ``qmm_logprobs``.
+``qmm_attention``, ``qmm_logprobs``. A key/value cache in 4 bits and the care of a cache's
+pages (include/qmm_cache.h) are in ``cache``: ``qmm_kv4_append``, ``qmm_kv4_gather``,
+``qmm_kv4_attention``, ``qmm_kv_copy_pages``, ``qmm_kv_compact``, ``kv4_page_bytes``.
 
 Bit widths 1, 2, 3, 4 and 8. The floating-point data (x, zeros, scales, bias,
 the result) are all float16 or all bfloat16; bfloat16 calls the ``_bf16``
@@ -104,6 +106,7 @@ def _declare(lib):
     lib.qmm_gemm_ex.restype = I
     lib.qmm_gemm_ex.argtypes = [P, I, I, P, P, P, P, P, I, I, I, U, P, P]
     layer.declare(lib)
+    cache.declare(lib)
     if lib.qmm_abi_version() != ABI_VERSION:
         raise RuntimeError(f"libqmm ABI version {lib.qmm_abi_version()} does not match the binding's {ABI_VERSION}")
     return lib
@@ -473,3 +476,6 @@ def quantized_matmul(x, qweight, qzeros, scales, bits: int, group_size: int, qwe
 
 from . import layer  # noqa: E402  (it uses the helpers above)
 from .layer import qmm_attention, qmm_kv_append, qmm_logprobs, qmm_moe, qmm_moe_route  # noqa: E402,F401
+from . import cache  # noqa: E402
+from .cache import (kv4_page_bytes, qmm_kv4_append, qmm_kv4_attention, qmm_kv4_gather, qmm_kv_compact,  # noqa: E402,F401
+                    qmm_kv_copy_pages)

@@ -1,0 +1,244 @@
+// The append to the 4-bit cache, and tokens of it as 16-bit values.
+//
+// A pair (a, b) of a head turns into (a c - b s, b c + a s); keys in fp64, rounded to fp32, so
+// that a code does not hang on the order of an fp32 sum. Of a group's values x: s =
+// fp16(bf16((hi - lo) / 15)), m = fp16(lo + 8 s), code 8 + rint((x - m) / s). The 8 bits
+// of s make s (c - 8) exact in fp16, which the attention builds on; m is the value of code 8,
+// so that what the codes add is of the size of the values' spread.
+#include "cache.h"
+#include "fixed_div.h"
+
+namespace qmm {
+namespace {
+
+constexpr float kLargest = kKv4Largest;
+
+// Eight values' scale, middle and codes (nibble e: code of x[e]); the group is
+// `lanes` neighbouring lanes, all of which come here.
+struct Quantised {
+  f16 s, m;
+  uint32_t codes;
+};
+__device__ __forceinline__ Quantised quantise(float (&x)[8], int lanes) {
+  float lo = INFINITY, hi = -INFINITY;
+  int nan = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    nan |= x[e] != x[e];
+    x[e] = fminf(fmaxf(x[e], -kLargest), kLargest);
+    lo = fminf(lo, x[e]);
+    hi = fmaxf(hi, x[e]);
+  }
+  for (int o = 1; o < lanes; o <<= 1) {
+    lo = fminf(lo, __shfl_xor(lo, o));
+    hi = fmaxf(hi, __shfl_xor(hi, o));
+    nan |= __shfl_xor(nan, o);
+  }
+  Quantised r;
+  r.s = (f16)(float)(bf16)((hi - lo) / 15.f);
+  const float s = (float)r.s;
+  r.m = (f16)(lo + 8 * s);
+  const float m = (float)r.m;
+  r.codes = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float c = s > 0 ? fminf(fmaxf(rintf((x[e] - m) / s), -8.f), 7.f) : 0.f;
+    r.codes |= (uint32_t)((int)c + 8) << (4 * e);
+  }
+  if (nan) {
+    r.s = r.m = (f16)NAN;
+    r.codes = 0x88888888u;
+  }
+  return r;
+}
+
+struct AppendKernelArgs {
+  AppendArgs a;
+  FixedDiv by_page;
+  int groups;
+  int group_lanes, group_shift;  // lanes per group; log2 of it
+};
+
+// Eight values of one head per thread. A thread of a rotated half loads its partner's
+// eight values too: a group's values then lie in neighbouring lanes.
+template <bool BF, bool ADJ>
+__global__ void __launch_bounds__(256) kv4_append_kernel(AppendKernelArgs p) {
+  const AppendArgs& a = p.a;
+  const int chunks = a.D / 8;
+  const int heads = a.Hq + 2 * a.Hkv;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int c = (int)(i % chunks);
+  const long long th = i / chunks;
+  const int h = (int)(th % heads);
+  const long long t = th / heads;
+  if (t >= a.T) return;
+
+  const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
+  const uint16_t* src;
+  uint8_t* block = nullptr;
+  int at = 0;
+  if (is_q) {
+    src = a.q + t * a.q_stride + (long long)h * a.D;
+  } else {
+    const int hk = is_v ? h - a.Hq - a.Hkv : h - a.Hq;
+    const int64_t slot = a.slots[t];
+    if (slot < 0 || slot >= (long long)a.pages * a.page_size) return;
+    const int page = p.by_page((int)slot);
+    at = (int)slot - page * a.page_size;
+    src = (is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride) + (long long)hk * a.D;
+    const long long row = ((long long)page * a.Hkv + hk) * a.page_size + at;
+    block = reinterpret_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + row / kBlockTokens * kv4_block_bytes(a.D, p.groups);
+    at %= kBlockTokens;
+  }
+
+  const u32x4 raw = *reinterpret_cast<const u32x4*>(src + 8 * c);
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = bits_to_float<BF>((uint16_t)(raw[e / 2] >> (16 * (e & 1))));
+  if (!is_v && 8 * c < a.R) {
+    const int pos = min(max(a.positions[t], 0), a.P - 1);
+    const float* cs = a.cos + (long long)pos * (a.R / 2);
+    const float* sn = a.sin + (long long)pos * (a.R / 2);
+    float y[8], co[8], si[8];  // partners (the second of a pair: with its sign), cosines and sines
+    if constexpr (ADJ) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] = e & 1 ? x[e - 1] : -x[e + 1];
+        co[e] = cs[4 * c + e / 2];
+        si[e] = sn[4 * c + e / 2];
+      }
+    } else {
+      const int half = a.R / 2;
+      const bool second = 8 * c >= half;
+      const u32x4 other = *reinterpret_cast<const u32x4*>(src + 8 * c + (second ? -half : half));
+      const int from = 8 * c - (second ? half : 0);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float o = bits_to_float<BF>((uint16_t)(other[e / 2] >> (16 * (e & 1))));
+        y[e] = second ? o : -o;
+        co[e] = cs[from + e];
+        si[e] = sn[from + e];
+      }
+    }
+    if (is_q) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = x[e] * co[e] + y[e] * si[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = (float)((double)x[e] * (double)co[e] + (double)y[e] * (double)si[e]);
+    }
+  }
+  if (is_q) {
+    u32x4 out = raw;
+    if (8 * c < a.R)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[e] = float_to_bits<BF>(x[2 * e]) | (uint32_t)float_to_bits<BF>(x[2 * e + 1]) << 16;
+    *reinterpret_cast<u32x4*>(a.q_out + (t * a.Hq + h) * a.D + 8 * c) = out;
+    return;
+  }
+  const Quantised z = quantise(x, p.group_lanes);
+  const int g = c >> p.group_shift;
+  const bool first = (c & (p.group_lanes - 1)) == 0;
+  f16* rest = reinterpret_cast<f16*>(block + 4 * a.D);
+  if (!is_v) {
+    // Nibbles of a word: the even channels, then the odd ones.
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w |= (z.codes >> (4 * e) & 15) << (4 * (e / 2 + 4 * (e & 1)));
+    reinterpret_cast<uint32_t*>(block)[at * chunks + (a.D / 32) * (c & 3) + c / 4] = w;
+    if (first) {
+      rest[at * 2 * p.groups + g] = z.s;
+      rest[at * 2 * p.groups + p.groups + g] = z.m;
+    }
+  } else {
+    uint16_t* codes = reinterpret_cast<uint16_t*>(block);
+    codes[(2 * c) * kBlockTokens + at] = (uint16_t)z.codes;
+    codes[(2 * c + 1) * kBlockTokens + at] = (uint16_t)(z.codes >> 16);
+    if (first) {
+      rest[g * 2 * kBlockTokens + at] = z.s;
+      rest[(g * 2 + 1) * kBlockTokens + at] = z.m;
+    }
+  }
+}
+
+struct GatherKernelArgs {
+  Kv4GatherArgs a;
+  FixedDiv by_page;
+  int group_shift;  // log2 of a group's threads
+};
+
+// Eight values of one head per thread, as for the append.
+template <bool BF>
+__global__ void __launch_bounds__(256) kv4_gather_kernel(GatherKernelArgs p) {
+  const Kv4GatherArgs& a = p.a;
+  const int chunks = a.D / 8;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int c = (int)(i % chunks);
+  const long long th = i / chunks;
+  const int h = (int)(th % (2 * a.Hkv));
+  const long long t = th / (2 * a.Hkv);
+  if (t >= a.T) return;
+  const bool is_v = h >= a.Hkv;
+  const int hk = is_v ? h - a.Hkv : h;
+  uint16_t* dst = (is_v ? a.v : a.k) + (t * a.Hkv + hk) * a.D + 8 * c;
+  const int64_t slot = a.slots[t];
+  if (slot < 0 || slot >= (long long)a.pages * a.page_size) {
+    *reinterpret_cast<u32x4*>(dst) = u32x4{0, 0, 0, 0};
+    return;
+  }
+  const int page = p.by_page((int)slot);
+  int at = (int)slot - page * a.page_size;
+  const int groups = a.D / a.group_size;
+  const long long row = ((long long)page * a.Hkv + hk) * a.page_size + at;
+  const uint8_t* block = (is_v ? a.v_cache : a.k_cache) + row / kBlockTokens * kv4_block_bytes(a.D, groups);
+  at %= kBlockTokens;
+  const int g = c >> p.group_shift;
+  const f16* rest = reinterpret_cast<const f16*>(block + 4 * a.D);
+  uint32_t w;
+  float s, m;
+  if (!is_v) {
+    w = reinterpret_cast<const uint32_t*>(block)[at * chunks + (a.D / 32) * (c & 3) + c / 4];
+    s = (float)rest[at * 2 * groups + g];
+    m = (float)rest[at * 2 * groups + groups + g];
+  } else {
+    const uint16_t* codes = reinterpret_cast<const uint16_t*>(block);
+    w = codes[(2 * c) * kBlockTokens + at] | (uint32_t)codes[(2 * c + 1) * kBlockTokens + at] << 16;
+    s = (float)rest[g * 2 * kBlockTokens + at];
+    m = (float)rest[(g * 2 + 1) * kBlockTokens + at];
+  }
+  if (!(fabsf(s) < INFINITY) || !(fabsf(m) < INFINITY)) s = m = NAN;
+  u32x4 out;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int lo = is_v ? 8 * x : 4 * x, hi = is_v ? 8 * x + 4 : 16 + 4 * x;
+    const float u = m + s * (float)((int)(w >> lo & 15) - 8), v = m + s * (float)((int)(w >> hi & 15) - 8);
+    out[x] = float_to_bits<BF>(u) | (uint32_t)float_to_bits<BF>(v) << 16;
+  }
+  *reinterpret_cast<u32x4*>(dst) = out;
+}
+
+int log2_of(int n) { return __builtin_ctz((unsigned)n); }
+
+}  // namespace
+
+hipError_t launch_kv4_append(const AppendArgs& a, int group_size, bool bf16, bool adjacent, hipStream_t stream) {
+  const long long n = (long long)a.T * (a.Hq + 2 * a.Hkv) * (a.D / 8);
+  const dim3 grid((unsigned)((n + 255) / 256));
+  const AppendKernelArgs p = {a, fixed_div(a.page_size), a.D / group_size, group_size / 8, log2_of(group_size / 8)};
+  if (bf16 && adjacent) kv4_append_kernel<true, true><<<grid, 256, 0, stream>>>(p);
+  else if (bf16) kv4_append_kernel<true, false><<<grid, 256, 0, stream>>>(p);
+  else if (adjacent) kv4_append_kernel<false, true><<<grid, 256, 0, stream>>>(p);
+  else kv4_append_kernel<false, false><<<grid, 256, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv4_gather(const Kv4GatherArgs& a, bool bf16, hipStream_t stream) {
+  const long long n = (long long)a.T * 2 * a.Hkv * (a.D / 8);
+  const dim3 grid((unsigned)((n + 255) / 256));
+  const GatherKernelArgs p = {a, fixed_div(a.page_size), log2_of(a.group_size / 8)};
+  if (bf16) kv4_gather_kernel<true><<<grid, 256, 0, stream>>>(p);
+  else kv4_gather_kernel<false><<<grid, 256, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace qmm

@@ -1,10 +1,8 @@
 // C ABI of the layer operators: argument validation and dispatch. Every check
 // runs on the host before anything is enqueued.
-#include <math.h>
-
 #include "../../include/qmm_layer.h"
+#include "checks.h"
 #include "layer.h"
-#include "status.h"
 
 namespace {
 
@@ -13,19 +11,13 @@ using qmm::aligned16;
 using qmm::fail;
 using qmm::from_hip;
 using qmm::ok;
-
-qmm_status check_flags(unsigned flags, unsigned known) {
-  if (flags & ~known) return fail(QMM_ERR_FLAGS, "flags=0x%x: bits other than 0x%x", flags, known);
-  return QMM_OK;
-}
-
-qmm_status check_workspace(const void* workspace, size_t bytes, size_t need) {
-  if (need == 0) return QMM_OK;
-  if (!workspace || bytes < need)
-    return fail(QMM_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? bytes : size_t(0));
-  if (!aligned16(workspace)) return fail(QMM_ERR_ALIGN, "workspace must be 16-byte aligned");
-  return QMM_OK;
-}
+using qmm::check_append_arrays;
+using qmm::check_append_shape;
+using qmm::check_attention_arrays;
+using qmm::check_attention_shape;
+using qmm::check_flags;
+using qmm::check_workspace;
+using qmm::attention_size_ok;
 
 // ---- mixture of experts ---------------------------------------------------------
 
@@ -55,33 +47,6 @@ qmm_status check_experts(const qmm_experts* w, const char* what, int bits) {
 qmm::ExpertPlanes planes(const qmm_experts* w) {
   return {reinterpret_cast<const uint32_t*>(w->qweight), reinterpret_cast<const uint32_t*>(w->qweight_lo), w->zeros,
           w->scales};
-}
-
-// ---- attention ------------------------------------------------------------------
-
-bool head_dim_ok(int D) { return D == 64 || D == 128 || D == 256; }
-
-qmm_status check_heads(int Hq, int Hkv, int D) {
-  if (!head_dim_ok(D)) return fail(QMM_ERR_SHAPE, "D=%d is not one of 64, 128, 256", D);
-  if (Hkv < 1 || Hq < Hkv || Hq % Hkv || Hq > 4096)
-    return fail(QMM_ERR_SHAPE, "Hq=%d (at most 4096) must be a positive multiple of Hkv=%d", Hq, Hkv);
-  return QMM_OK;
-}
-
-// The kernels number a cache's rows (a token of a head) with 32 bits.
-qmm_status check_cache(const void* k_cache, const void* v_cache, int pages, int Hkv, int page_size) {
-  if (pages < 1 || page_size < 1 || (long long)pages * page_size >= (1ll << 31) || (long long)pages * page_size * Hkv >= (1ll << 31))
-    return fail(QMM_ERR_SHAPE, "pages=%d and page_size=%d must be >= 1, pages * Hkv * page_size below 2^31", pages, page_size);
-  if (!k_cache || !v_cache) return fail(QMM_ERR_NULL, "k_cache or v_cache is NULL");
-  if (!aligned16(k_cache) || !aligned16(v_cache)) return fail(QMM_ERR_ALIGN, "k_cache and v_cache must be 16-byte aligned");
-  return QMM_OK;
-}
-
-bool stride_ok(long long stride, long long least) { return stride >= least && stride % 8 == 0 && stride < (1ll << 40); }
-
-bool attention_counts_ok(int B, int T, int Hq, int max_q, int max_kv) {
-  return B >= 0 && T >= 0 && (long long)T * Hq < (1ll << 31) && max_q >= 0 && max_kv >= 0 && B <= 65535 &&
-         (long long)max_q * Hq < (1ll << 31);
 }
 
 }  // namespace
@@ -153,34 +118,20 @@ qmm_status qmm_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* k,
                          int P, const int32_t* positions, const int64_t* slots, uint16_t* q_out, uint16_t* k_cache,
                          uint16_t* v_cache, int pages, int page_size, unsigned flags, hipStream_t stream) {
   qmm_status st = check_flags(flags, QMM_BF16 | QMM_ADJACENT);
-  if (st == QMM_OK) st = check_heads(Hq, Hkv, D);
   if (st != QMM_OK) return st;
-  if (T < 0 || (long long)T * Hq * D >= (1ll << 31)) return fail(QMM_ERR_SHAPE, "T=%d: T * Hq * D must be below 2^31", T);
-  if (R < 0 || R > D || R % 16) return fail(QMM_ERR_SHAPE, "R=%d must be a multiple of 16 in [0, D=%d]", R, D);
-  if (R > 0 && P < 1) return fail(QMM_ERR_SHAPE, "P=%d must be >= 1", P);
-  if (!stride_ok(q_stride, (long long)Hq * D) || !stride_ok(k_stride, (long long)Hkv * D) ||
-      !stride_ok(v_stride, (long long)Hkv * D))
-    return fail(QMM_ERR_SHAPE, "token strides must be multiples of 8 and at least a token's size");
-  if (T == 0) return ok();
-  st = check_cache(k_cache, v_cache, pages, Hkv, page_size);
-  if (st != QMM_OK) return st;
-  if (!q || !k || !v || !slots || !q_out || (R > 0 && (!cos || !sin || !positions)))
-    return fail(QMM_ERR_NULL, "a required pointer is NULL");
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out))
-    return fail(QMM_ERR_ALIGN, "q, k, v and q_out must be 16-byte aligned");
-  if (R > 0 && (!aligned16(cos) || !aligned16(sin) || !aligned(positions, 4)))
-    return fail(QMM_ERR_ALIGN, "cos and sin must be 16-byte, positions 4-byte aligned");
-  if (!aligned(slots, 8)) return fail(QMM_ERR_ALIGN, "slots must be 8-byte aligned");
   const qmm::AppendArgs a = {q, k, v, q_stride, k_stride, v_stride, T, Hq, Hkv, D, R, P, cos, sin, positions, slots,
                              q_out, k_cache, v_cache, pages, page_size};
+  st = check_append_shape(a);
+  if (st != QMM_OK) return st;
+  if (T == 0) return ok();
+  st = check_append_arrays(a);
+  if (st != QMM_OK) return st;
   return from_hip(qmm::launch_kv_append(a, (flags & QMM_BF16) != 0, (flags & QMM_ADJACENT) != 0, stream),
                   "qmm_kv_append launch");
 }
 
 size_t qmm_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int max_q, int max_kv) {
-  if (!head_dim_ok(D) || Hkv < 1 || Hq < Hkv || Hq % Hkv || Hq > 4096 || !attention_counts_ok(B, T, Hq, max_q, max_kv) ||
-      B < 1 || T < 1 || max_q < 1)
-    return 0;
+  if (!attention_size_ok(B, T, Hq, Hkv, D, max_q, max_kv)) return 0;
   return qmm::attention_workspace(B, T, Hq, Hkv, D, max_q, max_kv);
 }
 
@@ -190,35 +141,16 @@ qmm_status qmm_attention(const uint16_t* q, int64_t q_stride, int T, int Hq, int
                          const int32_t* first, const int32_t* end, float scale, float softcap, const float* slopes,
                          unsigned flags, uint16_t* out, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   qmm_status st = check_flags(flags, QMM_BF16);
-  if (st == QMM_OK) st = check_heads(Hq, Hkv, D);
-  if (st != QMM_OK) return st;
-  if (!attention_counts_ok(B, T, Hq, max_q, max_kv))
-    return fail(QMM_ERR_SHAPE, "B=%d (at most 65535), T=%d, max_q=%d and max_kv=%d must be >= 0, T * Hq and max_q * Hq below 2^31", B, T,
-                max_q, max_kv);
-  if (!stride_ok(q_stride, (long long)Hq * D))
-    return fail(QMM_ERR_SHAPE, "q_stride=%lld must be a multiple of 8, at least Hq * D", (long long)q_stride);
-  if (!isfinite(scale) || !isfinite(softcap) || softcap < 0)
-    return fail(QMM_ERR_SHAPE, "scale=%g and softcap=%g must be finite, softcap not negative", scale, softcap);
-  if (T == 0 || B == 0 || max_q == 0) return ok();
-  st = check_cache(k_cache, v_cache, pages, Hkv, page_size);
-  if (st != QMM_OK) return st;
-  if (table_stride < 1 || (long long)table_stride * page_size >= (1ll << 31) || max_kv > (long long)table_stride * page_size)
-    return fail(QMM_ERR_SHAPE, "max_kv=%d must not exceed table_stride=%d * page_size=%d (below 2^31)", max_kv,
-                table_stride, page_size);
-  // A launch's threads (256 a block) are counted in 32 bits.
-  if (qmm::attention_blocks(B, Hq, Hkv, max_q, max_kv) >= (1ll << 24))
-    return fail(QMM_ERR_SHAPE, "B=%d, Hkv=%d and max_q=%d: 2^24 blocks and more; pass the long sequences in a call of their own", B,
-                Hkv, max_q);
-  if (!q || !page_table || !kv_lens || !q_starts || !out) return fail(QMM_ERR_NULL, "a required pointer is NULL");
-  if (!aligned16(q) || !aligned16(out)) return fail(QMM_ERR_ALIGN, "q and out must be 16-byte aligned");
-  if (!aligned(page_table, 4) || !aligned(kv_lens, 4) || !aligned(q_starts, 4) || !aligned(first, 4) || !aligned(end, 4) ||
-      !aligned(slopes, 4))
-    return fail(QMM_ERR_ALIGN, "page_table, kv_lens, q_starts, first, end and slopes must be 4-byte aligned");
-  st = check_workspace(workspace, workspace_bytes, qmm::attention_workspace(B, T, Hq, Hkv, D, max_q, max_kv));
   if (st != QMM_OK) return st;
   const qmm::AttentionArgs a = {q, q_stride, k_cache, v_cache, page_table, kv_lens, q_starts, first, end, slopes, out,
                                 static_cast<char*>(workspace), T, Hq, Hkv, D, pages, page_size, table_stride, B, max_q,
                                 max_kv, scale, softcap};
+  st = check_attention_shape(a);
+  if (st != QMM_OK) return st;
+  if (T == 0 || B == 0 || max_q == 0) return ok();
+  st = check_attention_arrays(a, qmm::attention_blocks(B, Hq, Hkv, max_q, max_kv));
+  if (st == QMM_OK) st = check_workspace(workspace, workspace_bytes, qmm::attention_workspace(B, T, Hq, Hkv, D, max_q, max_kv));
+  if (st != QMM_OK) return st;
   return from_hip(qmm::launch_attention(a, (flags & QMM_BF16) != 0, stream), "qmm_attention launch");
 }
 
