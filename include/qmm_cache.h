@@ -72,7 +72,7 @@ qmm_status qmm_kv4_gather(const uint8_t* k_cache, const uint8_t* v_cache, int pa
  * qmm_kv4_attention -- qmm_attention to a 4-bit cache: the same formulas, masks,
  * arguments and requirements (and those above), with keys and values as the
  * cache's codes stand for, exactly. The weights exp(s) are rounded to fp16 (for
- * bf16 data too; keys below 2^-38 of a row's largest weight count as 0), the
+ * bf16 data too; weights below 2^-32 of a row's largest count as 0), the
  * same rounded weights make the denominator. A query with a value that is not finite gives
  * NaN where it sees a key.
  */

@@ -115,8 +115,8 @@ def attention(q, k_parts, v_parts, table, kv_lens, q_starts, scale, group, softc
 
     Scores: fp32 sums of D + 3 groups products of the parts' sizes; the query, scaled to a largest value in [1, 2), has
     fp16's spacing of 2^-24 where it is small, and so do its groups' sums. An error d of every score changes the result by
-    at most 2 d of sum p |v|. The weights' rounding by at most 2 half steps of that, and by 2^-39 of the largest
-    weight where they are small (2^14 stands for the largest, fp16's smallest step is 2^-24); fp32 sums of
+    at most 2 d of sum p |v|. The weights' rounding by at most 2 half steps of that, and by 2^-32 of the largest
+    weight where they are small (the largest is kept as 2^7 at least, half of fp16's smallest step is 2^-25); fp32 sums of
     the parts' sizes; one rounding of the result."""
     T, Hq, D = q.shape
     page, Hkv = k_parts[0].shape[2], k_parts[0].shape[1]
@@ -154,7 +154,7 @@ def attention(q, k_parts, v_parts, table, kv_lens, q_starts, scale, group, softc
                 moved = ((p * err) @ np.abs(V) + (p @ err) * size) * 1.1
                 whole = p @ (np.abs(vs) + np.abs(vm))
                 bound[t, h] = moved + 2 * WEIGHTS * size + len(keys) * F32 * 4 * whole
-                bound[t, h] += 2 * len(keys) * 2.0**-39 * np.abs(V).max() * p.max()
+                bound[t, h] += 2 * len(keys) * 2.0**-32 * np.abs(V).max() * p.max()
     return out, bound + ROUNDOFF[dtype] * (np.abs(out) + bound) + TINY[dtype]
 
 

@@ -10,6 +10,28 @@
 namespace qmm {
 namespace {
 
+constexpr int kMaxSplit = 64;
+
+struct AttnPlan {
+  int group;    // query heads per key head
+  int rtiles;   // row tiles of the longest sequence, per key head
+  int split;    // blocks along the keys
+  size_t tiles;  // all row tiles
+};
+
+AttnPlan attn_plan(int B, int Hq, int Hkv, int max_q, int max_kv, DeviceTopo topo) {
+  AttnPlan p;
+  p.group = Hq / Hkv;
+  p.rtiles = row_tiles(max_q, p.group, kRows);
+  p.tiles = (size_t)B * Hkv * p.rtiles;
+  const long long want = 4ll * topo.cus / (long long)p.tiles;
+  const long long most = (max_kv + kWaves * kChunk - 1ll) / (kWaves * kChunk);
+  p.split = (int)(want < most ? want : most);
+  if (p.split > kMaxSplit) p.split = kMaxSplit;
+  if (p.split < 1 || p.tiles > (size_t)kGemvMaxStrips) p.split = 1;
+  return p;
+}
+
 // Block: one tile of 16 rows, one part of its keys; its waves take the chunks of
 // the part in turn and meet in LDS. Bound: HBM, each key and value is read once
 // per tile: 48 queries on up to 8192 keys in a window of 4096, 32/8 heads of 128, 74 us,
@@ -232,7 +254,75 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) attentio
     }
   }
   __syncthreads();
-  join_rows<D>(p, so, sml, &s_last, span, b, hk, rt, part, [](float lo, float hi) { return pack_pair<BF>(lo, hi); });
+  // Thread: row tid / 16, D / 16 neighbouring dimensions.
+  constexpr int E = D / 16;
+  const int r = tid >> 4, d0 = (tid & 15) * E;
+  float m = -INFINITY, l = 0, o[E] = {};
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) m = fmaxf(m, sml[w][r][0]);
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    const float f = sml[w][r][0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(sml[w][r][0] - m);
+    l += sml[w][r][1] * f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] += so[w][r][d0 + e] * f;
+  }
+  const Row mine = row_of(p, rt * kRows + r, span, hk);
+  if (p.split > 1) {
+    // Partial sums of the parts, joined in order by the block that arrives last.
+    const size_t tile = ((size_t)b * a.Hkv + hk) * p.rtiles + rt;
+    // A thread's pairs lie 256 pairs apart: the threads of a store write whole lines. Rows past the
+    // sequence's last (12 of 16 with four heads a group and one query) are left out.
+    float* po = p.part + (tile * p.split + part) * kRows * D + 2 * tid;
+    if (mine.token >= 0) {
+#pragma unroll
+      for (int e = 0; e < E; e += 2) handoff_store(po + e * 256, o[e], o[e + 1]);
+      if ((tid & 15) == 0) handoff_store(p.part_ml + ((tile * p.split + part) * kRows + r) * 2, m, l);
+    }
+    if (!handoff_last(&p.counters[tile], (uint32_t)p.split, &s_last) || mine.token < 0) return;
+    const float* qo = p.part + tile * p.split * kRows * D + 2 * tid;
+    const float* qm = p.part_ml + (tile * p.split * kRows + r) * 2;
+    // Four parts' loads at a time; places past the last part repeat it with a factor of 0.
+    constexpr int kBatch = 4;
+    m = -INFINITY;
+    for (int s0 = 0; s0 < p.split; s0 += kBatch) {
+      float ms[kBatch];
+#pragma unroll
+      for (int s = 0; s < kBatch; ++s) ms[s] = handoff_load(qm + min(s0 + s, p.split - 1) * kRows * 2);
+#pragma unroll
+      for (int s = 0; s < kBatch; ++s) m = fmaxf(m, ms[s]);
+    }
+    l = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0;
+    for (int s0 = 0; s0 < p.split; s0 += kBatch) {
+      float ms[kBatch], ls[kBatch];
+      FloatPair os[kBatch][E / 2];
+#pragma unroll
+      for (int s = 0; s < kBatch; ++s) {
+        const int at = min(s0 + s, p.split - 1);
+        const FloatPair ml = handoff_load_pair(qm + at * kRows * 2);
+        ms[s] = ml.a;
+        ls[s] = ml.b;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) os[s][e] = handoff_load_pair(qo + (size_t)at * kRows * D + 512 * e);
+      }
+#pragma unroll
+      for (int s = 0; s < kBatch; ++s) {
+        const float f = s0 + s >= p.split || ms[s] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms[s] - m);
+        l += ls[s] * f;
+        // (a sum that is not finite goes with a finite maximum or a weight that is not: f is not 0 then)
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += f == 0.f ? 0.f : (e & 1 ? os[s][e / 2].b : os[s][e / 2].a) * f;
+      }
+    }
+  }
+  if (mine.token < 0) return;
+  const float inv = mine.lo < mine.hi ? 1 / l : 0.f;
+  uint16_t* dst = a.out + ((long long)mine.token * a.Hq + mine.head) * D + d0;
+#pragma unroll
+  for (int e = 0; e < E; e += 4)
+    *reinterpret_cast<u32x2*>(dst + e) = u32x2{pack_pair<BF>(o[e] * inv, o[e + 1] * inv), pack_pair<BF>(o[e + 2] * inv, o[e + 3] * inv)};
 }
 
 // Sixteen bytes per lane from its own address to LDS, lane l's to lds_addr + 16 l

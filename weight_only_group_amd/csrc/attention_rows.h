@@ -1,5 +1,5 @@
 // What the attention kernels over a paged cache have in common: the rows of a tile,
-// the keys that they see, the score of a product, the join of partial results.
+// the keys that they see, the score of a product.
 //
 // The rows of one key head are the (token, head of the group) pairs of a
 // sequence, i * G + g; sixteen rows make a tile, and a wave takes 32 keys of a
@@ -19,31 +19,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRows = 16;   // rows per tile
 constexpr int kChunk = 32;  // keys per wave and step
 constexpr int kWaves = 4;
-constexpr int kMaxSplit = 64;
-
-struct AttnPlan {
-  int group;    // query heads per key head
-  int rtiles;   // row tiles of the longest sequence, per key head
-  int split;    // blocks along the keys
-  size_t tiles;  // all row tiles
-};
 
 int row_tiles(int max_q, int group, int rows) { return (int)(((long long)max_q * group + rows - 1) / rows); }
 // Blocks of a grid with `rtiles` row tiles for each of B * per units, which come in eights.
 long long tile_blocks(int B, int per, int rtiles) { return ((long long)B * per + 7) / 8 * 8 * rtiles; }
-
-AttnPlan attn_plan(int B, int Hq, int Hkv, int max_q, int max_kv, DeviceTopo topo) {
-  AttnPlan p;
-  p.group = Hq / Hkv;
-  p.rtiles = row_tiles(max_q, p.group, kRows);
-  p.tiles = (size_t)B * Hkv * p.rtiles;
-  const long long want = 4ll * topo.cus / (long long)p.tiles;
-  const long long most = (max_kv + kWaves * kChunk - 1ll) / (kWaves * kChunk);
-  p.split = (int)(want < most ? want : most);
-  if (p.split > kMaxSplit) p.split = kMaxSplit;
-  if (p.split < 1 || p.tiles > (size_t)kGemvMaxStrips) p.split = 1;
-  return p;
-}
 
 struct AttnKernelArgs {
   AttentionArgs a;
@@ -112,6 +91,9 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& a, int b) {
   return s;
 }
 
+// Row tiles of a sequence.
+__device__ __forceinline__ int row_tiles_of(const Span& s, int group) { return ((s.q1 - s.q0) * group + kRows - 1) / kRows; }
+
 // Zeroes one key head's results of the tokens that no row stands for: those of sequence
 // b past its bound, and those before the first sequence and behind the last. Shared out
 // over `workers` blocks of 256 threads; as a rule there are none.
@@ -153,84 +135,6 @@ template <bool BF>
 __device__ __forceinline__ bool not_finite(uint32_t v) {
   constexpr uint32_t e = BF ? 0x7F80u : 0x7C00u;
   return (v & e) == e;
-}
-
-// The end of a block of 16 rows: its waves' sums (in LDS, with their maxima and
-// denominators) in wave order, then the parts along the keys, joined in order by the
-// block that arrives last, which writes the results. `pack` rounds two of them.
-template <int D, typename PACK>
-__device__ __forceinline__ void join_rows(const AttnKernelArgs& p, const float (*so)[kRows][D + 4], const float (*sml)[kRows][2],
-                                          int* s_last, const Span& span, int b, int hk, int rt, int part, PACK pack) {
-  // Thread: row tid / 16, D / 16 neighbouring dimensions.
-  constexpr int E = D / 16;
-  const int tid = threadIdx.x, r = tid >> 4, d0 = (tid & 15) * E;
-  float m = -INFINITY, l = 0, o[E] = {};
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) m = fmaxf(m, sml[w][r][0]);
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    const float f = sml[w][r][0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(sml[w][r][0] - m);
-    l += sml[w][r][1] * f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] += so[w][r][d0 + e] * f;
-  }
-  const AttentionArgs& a = p.a;
-  const Row mine = row_of(p, rt * kRows + r, span, hk);
-  if (p.split > 1) {
-    // Partial sums of the parts, joined in order by the block that arrives last.
-    const size_t tile = ((size_t)b * a.Hkv + hk) * p.rtiles + rt;
-    // A thread's pairs lie 256 pairs apart: the threads of a store write whole lines. Rows past the
-    // sequence's last (12 of 16 with four heads a group and one query) are left out.
-    float* po = p.part + (tile * p.split + part) * kRows * D + 2 * tid;
-    if (mine.token >= 0) {
-#pragma unroll
-      for (int e = 0; e < E; e += 2) handoff_store(po + e * 256, o[e], o[e + 1]);
-      if ((tid & 15) == 0) handoff_store(p.part_ml + ((tile * p.split + part) * kRows + r) * 2, m, l);
-    }
-    if (!handoff_last(&p.counters[tile], (uint32_t)p.split, s_last) || mine.token < 0) return;
-    const float* qo = p.part + tile * p.split * kRows * D + 2 * tid;
-    const float* qm = p.part_ml + (tile * p.split * kRows + r) * 2;
-    // Four parts' loads at a time; places past the last part repeat it with a factor of 0.
-    constexpr int kBatch = 4;
-    m = -INFINITY;
-    for (int s0 = 0; s0 < p.split; s0 += kBatch) {
-      float ms[kBatch];
-#pragma unroll
-      for (int s = 0; s < kBatch; ++s) ms[s] = handoff_load(qm + min(s0 + s, p.split - 1) * kRows * 2);
-#pragma unroll
-      for (int s = 0; s < kBatch; ++s) m = fmaxf(m, ms[s]);
-    }
-    l = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0;
-    for (int s0 = 0; s0 < p.split; s0 += kBatch) {
-      float ms[kBatch], ls[kBatch];
-      FloatPair os[kBatch][E / 2];
-#pragma unroll
-      for (int s = 0; s < kBatch; ++s) {
-        const int at = min(s0 + s, p.split - 1);
-        const FloatPair ml = handoff_load_pair(qm + at * kRows * 2);
-        ms[s] = ml.a;
-        ls[s] = ml.b;
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) os[s][e] = handoff_load_pair(qo + (size_t)at * kRows * D + 512 * e);
-      }
-#pragma unroll
-      for (int s = 0; s < kBatch; ++s) {
-        const float f = s0 + s >= p.split || ms[s] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms[s] - m);
-        l += ls[s] * f;
-        // (a sum that is not finite goes with a finite maximum or a weight that is not: f is not 0 then)
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += f == 0.f ? 0.f : (e & 1 ? os[s][e / 2].b : os[s][e / 2].a) * f;
-      }
-    }
-  }
-  if (mine.token < 0) return;
-  const float inv = mine.lo < mine.hi ? 1 / l : 0.f;
-  uint16_t* dst = a.out + ((long long)mine.token * a.Hq + mine.head) * D + d0;
-#pragma unroll
-  for (int e = 0; e < E; e += 4)
-    *reinterpret_cast<u32x2*>(dst + e) = u32x2{pack(o[e] * inv, o[e + 1] * inv), pack(o[e + 2] * inv, o[e + 3] * inv)};
 }
 
 }  // namespace

@@ -12,8 +12,8 @@
 // the value's middles gives the weights' sum.
 //
 // Queries are scaled by a power of two, so that a row's largest is in [1, 2) and fp16
-// holds them whatever their type. The weights p are fp16, 2^14 for a row's largest key so
-// far, so that those down to 2^-28 of it keep all their bits.
+// holds them whatever their type. The weights p are fp16, times 2^7.
+#include <algorithm>
 #include <type_traits>
 
 #include "attention_rows.h"
@@ -22,20 +22,59 @@
 namespace qmm {
 namespace {
 
-constexpr float kLift = 14.f;  // log2 of the largest weight
+// A row's maximum is left where it is while no weight passes 2^kSlack of it; weights are
+// kept times 2^kLift, so that they pass neither end of fp16.
+constexpr float kLift = 7.f, kSlack = 8.f;
 
-// Two of a word's codes, nibbles r and r + 4, as s (c - 8); c24 = -24 s.
+// The AND's and the OR's constant, in registers: as literals they would take an instruction each.
+struct DecodeMasks {
+  uint32_t code, sixteen;
+  __device__ __forceinline__ DecodeMasks() {
+    asm("s_mov_b32 %0, 0x03C003C0" : "=s"(code));
+    asm("v_mov_b32 %0, 0x4C004C00" : "=v"(sixteen));
+  }
+};
+
+// Two of a word's codes, nibbles R and R + 4, as s (c - 8); c24 = -24 s.
 template <int R>
-__device__ __forceinline__ uint32_t decode(uint32_t w, f16x2 s, f16x2 c24) {
-  constexpr uint32_t mask = 0x03C003C0u, sixteen = 0x4C004C00u;
+__device__ __forceinline__ uint32_t decode(uint32_t w, f16x2 s, f16x2 c24, const DecodeMasks& k) {
   const uint32_t at = R == 0 ? w << 6 : R == 1 ? w << 2 : R == 2 ? w >> 2 : w >> 6;
-  return as_u32(__builtin_elementwise_fma(as_f16x2((at & mask) | sixteen), s, c24));
+  return as_u32(__builtin_elementwise_fma(as_f16x2((at & k.code) | k.sixteen), s, c24));
 }
 __device__ __forceinline__ f16x2 times_24(f16x2 s) { return s * f16x2{(f16)-24.f, (f16)-24.f}; }  // exact: 10 bits
 
 // Whether a half of the pair is an infinity or a NaN, as a mask of those halves.
 __device__ __forceinline__ uint32_t not_finite_halves(uint32_t v) {
   return (not_finite<false>(v) ? 0xFFFFu : 0u) | (not_finite<false>(v >> 16) ? 0xFFFF0000u : 0u);
+}
+
+// Lane exchanges within rows of sixteen: a value of the lane R to the right (round the
+// row; or, of lanes past its end, anything).
+template <int R>
+__device__ __forceinline__ float rotated(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x120 + 16 - R, 0xF, 0xF, true));
+}
+template <int R>
+__device__ __forceinline__ uint32_t shifted(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x100 + R, 0xF, 0xF, true);
+}
+// Of the row's first four lanes a, b, c and d, side by side.
+__device__ __forceinline__ float spread(float a, float b, float c, float d) {
+  int v = __builtin_bit_cast(int, a);
+  v = __builtin_amdgcn_update_dpp(v, __builtin_bit_cast(int, b), 0x114, 0xF, 0x2, false);
+  v = __builtin_amdgcn_update_dpp(v, __builtin_bit_cast(int, c), 0x118, 0xF, 0x4, false);
+  v = __builtin_amdgcn_update_dpp(v, __builtin_bit_cast(int, d), 0x11C, 0xF, 0x8, false);
+  return __builtin_bit_cast(float, v);
+}
+__device__ __forceinline__ float sum_of_wave(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+// The largest of the four rows' values.
+__device__ __forceinline__ float max_of_rows(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
 }
 
 // BYTES (a multiple of 4, up to 32) from p as 32-bit words.
@@ -57,31 +96,276 @@ __device__ __forceinline__ void load_words(uint32_t (&to)[BYTES / 4], const uint
   }
 }
 
+// How many parts the keys of each tile are split into, so that the parts are alike
+// whatever the sequences' lengths: with c chunks a part, sum ceil(chunks / c) is at most sum chunks / c + tiles, so c =
+// sum chunks / parts gives no more blocks than parts + tiles. A sequence's chunks are those of its
+// first and last query.
+constexpr int kPerThread = 2, kMostSequences = 256 * kPerThread;  // of a split launch
+constexpr int kMostTiles = 4096;
+constexpr int kMostParts = 256;       // of a tile
+constexpr int kLeastChunks = kWaves;  // of a part
+
+// Blocks of a split launch that run at a time.
+inline int resident_blocks(int D, DeviceTopo topo) { return topo.cus * (D == 64 ? 4 : D == 128 ? 3 : 2); }
+
+struct Kv4Plan {
+  int group, rtiles;
+  int parts;  // parts wanted beyond one a tile; 0: one a tile
+  long long blocks;
+};
+#ifndef KV4_X
+#define KV4_X 4
+#endif
+Kv4Plan kv4_plan(int B, int Hq, int Hkv, int D, int max_q, int max_kv, DeviceTopo topo) {
+  Kv4Plan p;
+  p.group = Hq / Hkv;
+  p.rtiles = row_tiles(max_q, p.group, kRows);
+  const long long tiles = (long long)B * Hkv * p.rtiles;
+  const int fit = resident_blocks(D, topo);
+  p.parts = 0;
+  if (B <= kMostSequences && tiles <= kMostTiles && max_kv > kLeastChunks * kChunk) p.parts = (int)std::max(fit * KV4_X / 4 - tiles, fit * KV4_X / 8ll);
+  const long long most = ((long long)max_kv + kLeastChunks * kChunk - 1) / (kLeastChunks * kChunk);
+  p.blocks = p.parts ? std::min(tiles + p.parts, tiles * most) : tile_blocks(B, Hkv, p.rtiles);
+  return p;
+}
+
+struct Kv4KernelArgs {
+  AttnKernelArgs r;
+  int parts;
+  Cap cap;
+  bool bf16;
+};
+
+// A block's share: part `part` of `parts` of tile (b, hk, rt); first: the block of
+// the tile's part 0, step: blocks from part to part. b -1: none.
+struct Share {
+  int b, hk, rt, part, parts, first, step;
+  Span span;
+};
+
+// n / d rounded up, 0 <= n < 2^27 (d's inverse given), for quotients below 2^20.
+__device__ __forceinline__ int divided_up(int n, int d, float inverse) {
+  int q = (int)((float)n * inverse);  // off by one at most
+  q -= (long long)q * d > n;
+  q += (long long)q * d < n;
+  return q + ((long long)q * d < n);
+}
+
+// Blocks: per sequence its parts, of each the key heads, of each the row tiles. Scratch: 24 ints.
+__device__ __forceinline__ Share share_of(const Kv4KernelArgs& p, int* scratch) {
+  const AttentionArgs& a = p.r.a;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int per = a.B > 256 ? kPerThread : 1;
+  Span span[kPerThread];
+  int chunks[kPerThread], tiles[kPerThread];
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    chunks[i] = tiles[i] = 0;
+    const int b = tid * per + i;
+    if (i >= per || b >= a.B) continue;
+    const Span s = span[i] = span_of(a, b);
+    tiles[i] = max(row_tiles_of(s, p.r.group), 1) * a.Hkv;
+    int lo = 0, hi = s.kv;
+    if (s.q1 > s.q0) {
+      if (a.first) lo = max(min(a.first[s.q0], a.first[s.q1 - 1]), 0);
+      if (a.end) hi = min(max(a.end[s.q0], a.end[s.q1 - 1]), hi);
+    }
+    chunks[i] = s.q1 > s.q0 && lo < hi ? (hi - 1) / kChunk + 1 - lo / kChunk : 0;
+  }
+  float total = 0;
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) total += (float)tiles[i] * (float)chunks[i];
+  total = sum_of_wave(total);
+  float* wave_total = reinterpret_cast<float*>(scratch);
+  if (lane == 0) wave_total[wave] = total;
+  __syncthreads();
+  total = wave_total[0] + wave_total[1] + wave_total[2] + wave_total[3];
+  // (a little more than total / parts, so that the rounding of the sums does not make more parts)
+  const int c = max((int)(total / (float)p.parts * 1.00001f) + 1, kLeastChunks);
+  const float inverse = 1 / (float)c;
+  // The sequences' blocks, counted up.
+  int parts[kPerThread], blocks = 0;
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    parts[i] = min(max(divided_up(chunks[i], c, inverse), 1), kMostParts);
+    blocks += parts[i] * tiles[i];
+  }
+  int upto = blocks;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int up = __shfl_up(upto, o);
+    upto += lane >= o ? up : 0;
+  }
+  int* wave_blocks = scratch + 4;
+  int* found = scratch + 8;
+  if (lane == 63) wave_blocks[wave] = upto;
+  if (tid == 0) found[0] = -1;
+  __syncthreads();
+  int at = upto - blocks;
+  for (int w = 0; w < wave; ++w) at += wave_blocks[w];
+  const int id = blockIdx.x;
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const int n = parts[i] * tiles[i];
+    if (id >= at && id < at + n) {
+      found[0] = tid * per + i;
+      found[1] = id - at;
+      found[2] = parts[i];
+      found[3] = span[i].q0;
+      found[4] = span[i].q1;
+      found[5] = span[i].kv;
+      found[6] = span[i].first;
+    }
+    at += n;
+  }
+  __syncthreads();
+  auto get = [&](int i) { return __builtin_amdgcn_readfirstlane(found[i]); };
+  Share s;
+  s.b = get(0);
+  s.parts = get(2);
+  s.span = {get(3), get(4), get(5), get(6)};
+  const int off = get(1), rtiles = max(row_tiles_of(s.span, p.r.group), 1);
+  s.step = rtiles * a.Hkv;
+  s.part = off / s.step;
+  const int rest = off - s.part * s.step;
+  s.hk = rest / rtiles;
+  s.rt = rest - s.hk * rtiles;
+  s.first = id - s.part * s.step;
+  return s;
+}
+
+// Joins a tile's parts: the block that arrives last. `rows` live rows; scratch: LDS of
+// kMostParts * kRows + 256 * D / 16 + 2 * kWaves * kRows floats. A wave takes every fourth part, four rows at a time.
+template <int D, typename PACK>
+__device__ __forceinline__ void join_parts(const Kv4KernelArgs& p, const Share& sh, const Span& span, int rows, float* scratch, PACK pack) {
+  constexpr int E = D / 16, BATCH = D == 64 ? 8 : D == 128 ? 4 : 2;
+  const AttentionArgs& a = p.r.a;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  float* factor = scratch;                            // (part, row)
+  float* red = scratch + kMostParts * kRows;          // (wave, lane, E)
+  float* per_wave = red + 256 * E;                    // (wave, row): maxima, then sums
+  // Row tid % 16, every sixteenth part from tid / 16 on.
+  constexpr int kOwn = kMostParts / 16;
+  const int row = tid & 15, p0 = tid >> 4;
+  auto slot = [&](int part) { return (size_t)(sh.first + part * sh.step); };
+  float own_m = -INFINITY, own_l = 0;
+  if (row < rows) {
+#pragma unroll 4
+    for (int j = 0; j < kOwn; ++j) {
+      const int part = p0 + 16 * j;
+      if (part >= sh.parts) break;
+      const FloatPair ml = handoff_load_pair(p.r.part_ml + (slot(part) * kRows + row) * 2);
+      factor[part * kRows + row] = ml.a;
+      const float m = fmaxf(own_m, ml.a), off = m == -INFINITY ? 0.f : m;
+      own_l = own_l * __builtin_amdgcn_exp2f(own_m - off) + ml.b * __builtin_amdgcn_exp2f(ml.a - off);
+      own_m = m;
+    }
+  }
+  float m = fmaxf(own_m, __shfl_xor(own_m, 16));
+  m = fmaxf(m, __shfl_xor(m, 32));
+  if (lane < 16) per_wave[wave * kRows + row] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) m = fmaxf(m, per_wave[w * kRows + row]);
+  const float off = m == -INFINITY ? 0.f : m;
+  own_l *= __builtin_amdgcn_exp2f(own_m - off);
+  own_l += __shfl_xor(own_l, 16);
+  own_l += __shfl_xor(own_l, 32);
+  float* sums = per_wave + kWaves * kRows;
+  if (lane < 16) sums[wave * kRows + row] = own_l;
+  if (row < rows)
+    for (int part = p0; part < sh.parts; part += 16) factor[part * kRows + row] = __builtin_amdgcn_exp2f(factor[part * kRows + row] - off);
+  __syncthreads();
+  for (int r0 = 0; r0 < rows; r0 += 4) {
+    // Lane: row r0 + lane / 16, E neighbouring dimensions.
+    const int r = r0 + (lane >> 4);
+    const bool live = r < rows;
+    const float* from = p.r.part + (min(r, rows - 1) * 16 + (lane & 15)) * 2;
+    float o[E] = {};
+    for (int q0 = wave; q0 < sh.parts; q0 += kWaves * BATCH) {
+      FloatPair v[BATCH][E / 2];
+#pragma unroll
+      for (int y = 0; y < BATCH; ++y)
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e)
+          v[y][e] = handoff_load_pair(from + slot(min(q0 + y * kWaves, sh.parts - 1)) * kRows * D + 512 * e);
+#pragma unroll
+      for (int y = 0; y < BATCH; ++y) {
+        const int part = q0 + y * kWaves;
+        const float f = live && part < sh.parts ? factor[part * kRows + r] : 0.f;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          o[2 * e] += v[y][e].a * f;
+          o[2 * e + 1] += v[y][e].b * f;
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) red[(wave * E + e) * 64 + lane] = o[e];
+    __syncthreads();
+    constexpr int PER = E / 4 > 2 ? E / 4 : 2;  // dimensions a wave finishes
+    if (live && wave * PER < E) {
+      const Row mine = row_of(p.r, sh.rt * kRows + r, span, sh.hk);
+      const float l = sums[r] + sums[kRows + r] + sums[2 * kRows + r] + sums[3 * kRows + r];
+      const float inv = mine.lo < mine.hi ? 1 / l : 0.f;
+      uint16_t* dst = a.out + ((long long)mine.token * a.Hq + mine.head) * D + (lane & 15) * E + wave * PER;
+#pragma unroll
+      for (int e = 0; e < PER; e += 2) {
+        float x = 0, y = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          x += red[(w * E + wave * PER + e) * 64 + lane];
+          y += red[(w * E + wave * PER + e + 1) * 64 + lane];
+        }
+        *reinterpret_cast<uint32_t*>(dst + e) = pack(x * inv, y * inv);
+      }
+    }
+    __syncthreads();
+  }
+}
+
 // Block: one tile of 16 rows, one part of its keys, in chunks of 32 keys a wave, as for the
 // cache of 16-bit values. The products are K q^T and V^T p^T. Row i of a chunk's t-th
 // sixteen is key 8 (i / 4) + 4 t + i % 4, so that a lane's scores are those of one block of
 // eight tokens, whose values' words hold two tokens each: they need no exchange.
-template <int D, int G, Cap CAP>
-__global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(AttnKernelArgs p, bool bf16_data) {
+//
+// NARROW: no more than four rows (one token of up to four heads a key head). Twelve of
+// a product's sixteen columns are then free: the scores of the eight keys of a lane are spread
+// over them, two a lane, for the softmax.
+template <int D, int G, bool NARROW>
+__global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4KernelArgs k) {
   constexpr int STEPS = D / 32, U = D / 64, GS = D / G, BLOCK = kv4_block_bytes(D, G);
   constexpr int NS = GS == 32 ? U : G;  // sets of scales that a lane needs for its values
   constexpr int LD = D + 4;
-  __shared__ float so[kWaves][kRows][LD];
-  __shared__ float sml[kWaves][kRows][2];
+  constexpr int kJoin = kMostParts * kRows + 16 * D + 2 * kWaves * kRows, kMeet = kWaves * kRows * (LD + 2);
+  __shared__ __attribute__((aligned(16))) float shared[kJoin > kMeet ? kJoin : kMeet];
   __shared__ int s_last;
+  float (*so)[kRows][LD] = reinterpret_cast<float (*)[kRows][LD]>(shared);
+  float (*sml)[kRows][2] = reinterpret_cast<float (*)[kRows][2]>(shared + kWaves * kRows * LD);
+  const AttnKernelArgs& p = k.r;
   const AttentionArgs& a = p.a;
+  const bool bf16_data = k.bf16;
   const uint8_t* k_cache = reinterpret_cast<const uint8_t*>(a.k_cache);
   const uint8_t* v_cache = reinterpret_cast<const uint8_t*>(a.v_cache);
-  // Blocks of the row tiles that read the same keys follow each other on one XCD.
-  const int per = 8 * p.rtiles, w8 = blockIdx.x % per;
-  const int rt = w8 / 8, unit = blockIdx.x / per * 8 + w8 % 8;
-  if (unit >= a.B * a.Hkv * p.split) return;
-  const int part = unit % p.split, hk = unit / p.split % a.Hkv, b = unit / p.split / a.Hkv;
-  const Span span = span_of(a, b);
-  zero_rest<D>(p, span, b, hk, rt * p.split + part, p.rtiles * p.split);
-  if (rt * kRows >= (span.q1 - span.q0) * p.group) return;
+  Share share;
+  if (k.parts) {
+    __shared__ int scratch[16];
+    share = share_of(k, scratch);
+    if (share.b < 0) return;
+  } else {
+    // Blocks of the row tiles that read the same keys follow each other on one XCD.
+    const int per = 8 * p.rtiles, w8 = blockIdx.x % per, unit = blockIdx.x / per * 8 + w8 % 8;
+    if (unit >= a.B * a.Hkv) return;
+    share = {unit / a.Hkv, unit % a.Hkv, w8 / 8, 0, 1, 0, 0, span_of(a, unit / a.Hkv)};
+  }
+  const int b = share.b, hk = share.hk, rt = share.rt;
+  const Span span = share.span;
+  const int rtiles = max(row_tiles_of(span, p.group), 1);
+  zero_rest<D>(p, span, b, hk, rt * share.parts + share.part, rtiles * share.parts);
+  const int rows_left = (span.q1 - span.q0) * p.group - rt * kRows;
+  if (rows_left <= 0) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 15, kg = lane >> 4;
-  const Row row = row_of(p, rt * kRows + n, span, hk);
+  const Row row = row_of(p, rt * kRows + (NARROW ? n & 3 : n), span, hk);
   ScoreRule rule = score_rule(a, row.head);
 
   // The keys that any row sees, and those that all see.
@@ -100,7 +384,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(AttnKe
   all_hi = __builtin_amdgcn_readfirstlane(all_hi);
   auto seen_by_all = [&](int c) { return c * kChunk >= all_lo && (uint32_t)(c + 1) * kChunk <= (uint32_t)all_hi; };
   const int c_first = lo < hi ? lo / kChunk : 0, chunks = lo < hi ? (hi - 1) / kChunk + 1 - c_first : 0;
-  const int c0 = c_first + (int)((long long)chunks * part / p.split), c1 = c_first + (int)((long long)chunks * (part + 1) / p.split);
+  const int c0 = c_first + (int)((long long)chunks * share.part / share.parts), c1 = c_first + (int)((long long)chunks * (share.part + 1) / share.parts);
 
   // The row's query in fp16, and its groups' sums in three parts (lane group 0: the first, ...).
   u32x4 q[STEPS], qsum = {0, 0, 0, 0};
@@ -181,6 +465,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(AttnKe
     vm = *reinterpret_cast<const u32x4*>(vmiddles + at);
   };
 
+  const DecodeMasks masks;
   f32x4 acc[U][4] = {}, rest = {};  // rest: rows g the sums of p m_g, row 15 the sum of p
   float mx = -INFINITY;
   bool any_bad = false;
@@ -207,7 +492,8 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(AttnKe
         const f16 sg = as_f16x2(pair)[g % 2];
         const f16x2 ss = {sg, sg}, c24 = times_24(ss);
         const uint32_t w = kw[t][s];
-        st[t] = mfma16<false>(u32x4{decode<0>(w, ss, c24), decode<1>(w, ss, c24), decode<2>(w, ss, c24), decode<3>(w, ss, c24)}, q[s], st[t]);
+        st[t] = mfma16<false>(u32x4{decode<0>(w, ss, c24, masks), decode<1>(w, ss, c24, masks), decode<2>(w, ss, c24, masks),
+                                     decode<3>(w, ss, c24, masks)}, q[s], st[t]);
       }
     }
     if constexpr (MORE) {
@@ -219,21 +505,46 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(AttnKe
       load_k(blocks);
       __builtin_amdgcn_sched_barrier(0);
     }
-    // Scores: key 32 c + 8 kg + 4 t + r of row n.
-    const int j0 = c * kChunk + 8 * kg;
+    // Scores: key j0 + x of the row.
+    constexpr int NX = NARROW ? 2 : 8;
+    const int j0 = c * kChunk + 8 * kg + (NARROW ? 2 * (n >> 2) : 0);
     const bool whole = seen_by_all(c);
-    float s[8], best = -INFINITY;
+    float s[NX], best = -INFINITY;
+    if constexpr (NARROW) {
+      s[0] = spread(st[0][0], st[0][2], st[1][0], st[1][2]);
+      s[1] = spread(st[0][1], st[0][3], st[1][1], st[1][3]);
+    } else {
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      s[x] = rule.template score<CAP, true>(st[x >> 2][x & 3], row.pos, j0 + x);
-      if (!whole) s[x] = j0 + x >= row.lo && j0 + x < row.hi ? s[x] : -INFINITY;
-      best = fmaxf(best, s[x]);
+      for (int x = 0; x < NX; ++x) s[x] = st[x >> 2][x & 3];
     }
-    best = fmaxf(best, __shfl_xor(best, 16));
-    best = fmaxf(best, __shfl_xor(best, 32));
-    if (__any(best > mx)) {
-      const float m = fmaxf(mx, best);
-      const float f = mx == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx - m);
+    if (k.cap == kNoCap) {
+#pragma unroll
+      for (int x = 0; x < NX; ++x) s[x] = rule.template score<kNoCap, false>(s[x], 0, 0);
+    } else if (k.cap == kSmallCap) {
+#pragma unroll
+      for (int x = 0; x < NX; ++x) s[x] = rule.template score<kSmallCap, false>(s[x], 0, 0);
+    } else {
+#pragma unroll
+      for (int x = 0; x < NX; ++x) s[x] = rule.template score<kAnyCap, false>(s[x], 0, 0);
+    }
+    if (a.slopes) {
+#pragma unroll
+      for (int x = 0; x < NX; ++x) s[x] -= rule.slope * fabsf((float)(row.pos - (j0 + x)));
+    }
+    if (!whole) {
+#pragma unroll
+      for (int x = 0; x < NX; ++x) s[x] = j0 + x >= row.lo && j0 + x < row.hi ? s[x] : -INFINITY;
+    }
+#pragma unroll
+    for (int x = 0; x < NX; ++x) best = fmaxf(best, s[x]);
+    if (NARROW) {
+      best = fmaxf(best, rotated<4>(best));
+      best = fmaxf(best, rotated<8>(best));
+    }
+    best = max_of_rows(best);
+    if (__any(best > mx + kSlack)) {
+      const float m = best > mx + kSlack ? best : mx;
+      const float f = mx == m ? 1.f : __builtin_amdgcn_exp2f(mx - m);
       rest *= f;
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -244,8 +555,13 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(AttnKe
     const float off = mx == -INFINITY ? 0.f : mx - kLift;
     u32x4 w;
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+    for (int x = 0; x < NX / 2; ++x)
       w[x] = pack_pair<false>(__builtin_amdgcn_exp2f(s[2 * x] - off), __builtin_amdgcn_exp2f(s[2 * x + 1] - off));
+    if constexpr (NARROW) {  // (what columns past the fourth get is in no result)
+      w[1] = shifted<4>(w[0]);
+      w[2] = shifted<8>(w[0]);
+      w[3] = shifted<12>(w[0]);
+    }
     if (!whole) {
       // Places that no row sees may hold anything: their scales and middles count as 0. So do those
       // of a seen place that are not finite, as they must not reach the rows that do not see it (0
@@ -254,7 +570,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(AttnKe
       auto clean = [&](u32x4& v) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const int j = j0 + 2 * x;
+          const int j = c * kChunk + 8 * kg + 2 * x;
           const uint32_t in = (j >= lo && j < hi ? 0xFFFFu : 0u) | (j + 1 >= lo && j + 1 < hi ? 0xFFFF0000u : 0u);
           const uint32_t nf = not_finite_halves(v[x]) & in;
           bad |= nf;
@@ -285,7 +601,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(AttnKe
         constexpr int R = decltype(r)::value;
         u32x4 vt;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) vt[x] = decode<R>(vw[u][x], ss[x], c24[x]);
+        for (int x = 0; x < 4; ++x) vt[x] = decode<R>(vw[u][x], ss[x], c24[x], masks);
         acc[u][R] = mfma16<false>(vt, w, acc[u][R]);
       };
       product(std::integral_constant<int, 0>{});
@@ -321,6 +637,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(AttnKe
       constexpr int PER = GS / 64;
       middle = __shfl(rest[u / PER & 3], (u / PER >> 2) * 16 + n);
     }
+    if (NARROW && n >= 4) continue;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
       *reinterpret_cast<f32x4*>(&so[wave][n][u * 64 + kg * 16 + r * 4]) =
@@ -343,37 +660,67 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(AttnKe
     }
   }
   __syncthreads();
-  join_rows<D>(p, so, sml, &s_last, span, b, hk, rt, part, [=](float x, float y) { return bf16_data ? pack_pair<true>(x, y) : pack_pair<false>(x, y); });
+  // Thread: row tid / 16, D / 16 neighbouring dimensions.
+  const auto pack = [=](float x, float y) { return bf16_data ? pack_pair<true>(x, y) : pack_pair<false>(x, y); };
+  constexpr int E = D / 16;
+  const int r = tid >> 4, d0 = (tid & 15) * E, rows = min(rows_left, kRows);
+  float m = -INFINITY, l = 0, o[E] = {};
+  if (r < rows) {
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) m = fmaxf(m, sml[w][r][0]);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float f = sml[w][r][0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(sml[w][r][0] - m);
+      l += sml[w][r][1] * f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += so[w][r][d0 + e] * f;
+    }
+  }
+  if (share.parts > 1) {
+    if (r < rows) {
+      // A thread's pairs lie 256 pairs apart: the threads of a store write whole lines.
+      float* to = p.part + (size_t)blockIdx.x * kRows * D + 2 * tid;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) handoff_store(to + e * 256, o[e], o[e + 1]);
+      if ((tid & 15) == 0) handoff_store(p.part_ml + ((size_t)blockIdx.x * kRows + r) * 2, m, l);
+    }
+    const size_t tile = ((size_t)b * a.Hkv + hk) * p.rtiles + rt;
+    if (handoff_last(&p.counters[tile], (uint32_t)share.parts, &s_last)) join_parts<D>(k, share, span, rows, shared, pack);
+    return;
+  }
+  if (r >= rows) return;
+  const Row mine = row_of(p, rt * kRows + r, span, hk);
+  const float inv = mine.lo < mine.hi ? 1 / l : 0.f;
+  uint16_t* dst = a.out + ((long long)mine.token * a.Hq + mine.head) * D + d0;
+#pragma unroll
+  for (int e = 0; e < E; e += 4)
+    *reinterpret_cast<u32x2*>(dst + e) = u32x2{pack(o[e] * inv, o[e + 1] * inv), pack(o[e + 2] * inv, o[e + 3] * inv)};
 }
 
 template <int D, int G>
 hipError_t launch_split(const AttentionArgs& a, bool bf16, hipStream_t stream) {
-  const AttnPlan plan = attn_plan(a.B, a.Hq, a.Hkv, a.max_q, a.max_kv, device_topology());
-  AttnKernelArgs p = {a, fixed_div(a.page_size), fixed_div(plan.group), plan.group, plan.rtiles, plan.split, reinterpret_cast<uint32_t*>(a.workspace), nullptr, nullptr};
-  if (plan.split > 1) {
-    p.part = reinterpret_cast<float*>(a.workspace + kWorkspaceHeader);
-    p.part_ml = p.part + plan.tiles * plan.split * kRows * D;
+  const Kv4Plan plan = kv4_plan(a.B, a.Hq, a.Hkv, D, a.max_q, a.max_kv, device_topology());
+  Kv4KernelArgs p = {{a, fixed_div(a.page_size), fixed_div(plan.group), plan.group, plan.rtiles, 1, reinterpret_cast<uint32_t*>(a.workspace), nullptr, nullptr},
+                     plan.parts, cap_kind(a.softcap), bf16};
+  if (plan.parts) {
+    p.r.part = reinterpret_cast<float*>(a.workspace + kWorkspaceHeader);
+    p.r.part_ml = p.r.part + plan.blocks * kRows * D;
   }
-  const dim3 grid((unsigned)tile_blocks(a.B, a.Hkv * plan.split, plan.rtiles));
-  const auto run = [&](auto kernel) { kernel<<<grid, 64 * kWaves, 0, stream>>>(p, bf16); };
-  switch (cap_kind(a.softcap)) {
-    case kNoCap: run(kv4_split_kernel<D, G, kNoCap>); break;
-    case kSmallCap: run(kv4_split_kernel<D, G, kSmallCap>); break;
-    case kAnyCap: run(kv4_split_kernel<D, G, kAnyCap>); break;
-  }
+  const dim3 grid((unsigned)plan.blocks);
+  if ((long long)a.max_q * plan.group <= 4) kv4_split_kernel<D, G, true><<<grid, 64 * kWaves, 0, stream>>>(p);
+  else kv4_split_kernel<D, G, false><<<grid, 64 * kWaves, 0, stream>>>(p);
   return hipGetLastError();
 }
 
 }  // namespace
 
 size_t kv4_attention_workspace(int B, int T, int Hq, int Hkv, int D, int max_q, int max_kv) {
-  const AttnPlan p = attn_plan(B, Hq, Hkv, max_q, max_kv, device_topology());
-  return p.split > 1 ? kWorkspaceHeader + p.tiles * p.split * kRows * (D + 2) * sizeof(float) : 0;
+  const Kv4Plan p = kv4_plan(B, Hq, Hkv, D, max_q, max_kv, device_topology());
+  return p.parts ? kWorkspaceHeader + p.blocks * kRows * (D + 2) * sizeof(float) : 0;
 }
 
-long long kv4_attention_blocks(int B, int Hq, int Hkv, int max_q, int max_kv) {
-  const AttnPlan p = attn_plan(B, Hq, Hkv, max_q, max_kv, device_topology());
-  return tile_blocks(B, Hkv * p.split, p.rtiles);
+long long kv4_attention_blocks(int B, int Hq, int Hkv, int D, int max_q, int max_kv) {
+  return kv4_plan(B, Hq, Hkv, D, max_q, max_kv, device_topology()).blocks;
 }
 
 hipError_t launch_kv4_attention(const AttentionArgs& a, int group_size, bool bf16, hipStream_t stream) {
