@@ -66,10 +66,48 @@ __device__ __forceinline__ float spread(float a, float b, float c, float d) {
   v = __builtin_amdgcn_update_dpp(v, __builtin_bit_cast(int, d), 0x11C, 0xF, 0x8, false);
   return __builtin_bit_cast(float, v);
 }
+// Running sums over a wave's lanes.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int plus_dpp(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int running_sum(int v) {
+  v = plus_dpp<0x111, 0xF>(v);
+  v = plus_dpp<0x112, 0xF>(v);
+  v = plus_dpp<0x114, 0xF>(v);
+  v = plus_dpp<0x118, 0xF>(v);
+  v = plus_dpp<0x142, 0xA>(v);  // a row's last lane to the next row
+  return plus_dpp<0x143, 0xC>(v);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float plus_dpp(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xF, false));
+}
 __device__ __forceinline__ float sum_of_wave(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  v = plus_dpp<0x111, 0xF>(v);
+  v = plus_dpp<0x112, 0xF>(v);
+  v = plus_dpp<0x114, 0xF>(v);
+  v = plus_dpp<0x118, 0xF>(v);
+  v = plus_dpp<0x142, 0xA>(v);
+  v = plus_dpp<0x143, 0xC>(v);
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+// The least and the largest over a row's sixteen lanes, of integers.
+template <int CTRL>
+__device__ __forceinline__ int across(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
+}
+__device__ __forceinline__ int least_of_row(int v) {
+  v = min(v, across<0x128>(v));
+  v = min(v, across<0x124>(v));
+  v = min(v, across<0x122>(v));
+  return min(v, across<0x121>(v));
+}
+__device__ __forceinline__ int largest_of_row(int v) {
+  v = max(v, across<0x128>(v));
+  v = max(v, across<0x124>(v));
+  v = max(v, across<0x122>(v));
+  return max(v, across<0x121>(v));
 }
 // The largest of the four rows' values.
 __device__ __forceinline__ float max_of_rows(float v) {
@@ -100,7 +138,7 @@ __device__ __forceinline__ void load_words(uint32_t (&to)[BYTES / 4], const uint
 // whatever the sequences' lengths: with c chunks a part, sum ceil(chunks / c) is at most sum chunks / c + tiles, so c =
 // sum chunks / parts gives no more blocks than parts + tiles. A sequence's chunks are those of its
 // first and last query.
-constexpr int kPerThread = 2, kMostSequences = 256 * kPerThread;  // of a split launch
+constexpr int kMostSequences = 1024;  // of a split launch
 constexpr int kMostTiles = 4096;
 constexpr int kMostParts = 256;       // of a tile
 constexpr int kLeastChunks = kWaves;  // of a part
@@ -151,171 +189,150 @@ __device__ __forceinline__ int divided_up(int n, int d, float inverse) {
   return q + ((long long)q * d < n);
 }
 
-// Blocks: per sequence its parts, of each the key heads, of each the row tiles. Scratch: 24 ints.
-__device__ __forceinline__ Share share_of(const Kv4KernelArgs& p, int* scratch) {
-  const AttentionArgs& a = p.r.a;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int per = a.B > 256 ? kPerThread : 1;
-  Span span[kPerThread];
-  int chunks[kPerThread], tiles[kPerThread];
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    chunks[i] = tiles[i] = 0;
-    const int b = tid * per + i;
-    if (i >= per || b >= a.B) continue;
-    const Span s = span[i] = span_of(a, b);
-    tiles[i] = max(row_tiles_of(s, p.r.group), 1) * a.Hkv;
-    int lo = 0, hi = s.kv;
-    if (s.q1 > s.q0) {
-      if (a.first) lo = max(min(a.first[s.q0], a.first[s.q1 - 1]), 0);
-      if (a.end) hi = min(max(a.end[s.q0], a.end[s.q1 - 1]), hi);
-    }
-    chunks[i] = s.q1 > s.q0 && lo < hi ? (hi - 1) / kChunk + 1 - lo / kChunk : 0;
-  }
-  float total = 0;
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) total += (float)tiles[i] * (float)chunks[i];
-  total = sum_of_wave(total);
-  float* wave_total = reinterpret_cast<float*>(scratch);
-  if (lane == 0) wave_total[wave] = total;
-  __syncthreads();
-  total = wave_total[0] + wave_total[1] + wave_total[2] + wave_total[3];
-  // (a little more than total / parts, so that the rounding of the sums does not make more parts)
-  const int c = max((int)(total / (float)p.parts * 1.00001f) + 1, kLeastChunks);
-  const float inverse = 1 / (float)c;
-  // The sequences' blocks, counted up.
-  int parts[kPerThread], blocks = 0;
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    parts[i] = min(max(divided_up(chunks[i], c, inverse), 1), kMostParts);
-    blocks += parts[i] * tiles[i];
-  }
-  int upto = blocks;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int up = __shfl_up(upto, o);
-    upto += lane >= o ? up : 0;
-  }
-  int* wave_blocks = scratch + 4;
-  int* found = scratch + 8;
-  if (lane == 63) wave_blocks[wave] = upto;
-  if (tid == 0) found[0] = -1;
-  __syncthreads();
-  int at = upto - blocks;
-  for (int w = 0; w < wave; ++w) at += wave_blocks[w];
-  const int id = blockIdx.x;
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int n = parts[i] * tiles[i];
-    if (id >= at && id < at + n) {
-      found[0] = tid * per + i;
-      found[1] = id - at;
-      found[2] = parts[i];
-      found[3] = span[i].q0;
-      found[4] = span[i].q1;
-      found[5] = span[i].kv;
-      found[6] = span[i].first;
-    }
-    at += n;
-  }
-  __syncthreads();
-  auto get = [&](int i) { return __builtin_amdgcn_readfirstlane(found[i]); };
-  Share s;
-  s.b = get(0);
-  s.parts = get(2);
-  s.span = {get(3), get(4), get(5), get(6)};
-  const int off = get(1), rtiles = max(row_tiles_of(s.span, p.r.group), 1);
-  s.step = rtiles * a.Hkv;
-  s.part = off / s.step;
-  const int rest = off - s.part * s.step;
-  s.hk = rest / rtiles;
-  s.rt = rest - s.hk * rtiles;
-  s.first = id - s.part * s.step;
+struct Sequence {
+  Span span;
+  int tiles, chunks;  // tiles of all key heads
+};
+__device__ __forceinline__ Sequence sequence_of(const AttnKernelArgs& p, int b) {
+  const AttentionArgs& a = p.a;
+  Sequence s = {{0, 0, 0, 0}, 0, 0};
+  if (b >= a.B) return s;
+  s.span = span_of(a, b);
+  s.tiles = max(row_tiles_of(s.span, p.group), 1) * a.Hkv;
+  if (s.span.q1 == s.span.q0) return s;
+  int lo = 0, hi = s.span.kv;
+  if (a.first) lo = max(min(a.first[s.span.q0], a.first[s.span.q1 - 1]), 0);
+  if (a.end) hi = min(max(a.end[s.span.q0], a.end[s.span.q1 - 1]), hi);
+  s.chunks = lo < hi ? (hi - 1) / kChunk + 1 - lo / kChunk : 0;
   return s;
 }
 
-// Joins a tile's parts: the block that arrives last. `rows` live rows; scratch: LDS of
-// kMostParts * kRows + 256 * D / 16 + 2 * kWaves * kRows floats. A wave takes every fourth part, four rows at a time.
-template <int D, typename PACK>
-__device__ __forceinline__ void join_parts(const Kv4KernelArgs& p, const Share& sh, const Span& span, int rows, float* scratch, PACK pack) {
-  constexpr int E = D / 16, BATCH = D == 64 ? 8 : D == 128 ? 4 : 2;
+// Blocks: per sequence its parts, of each the key heads, of each the row tiles. Every wave finds the
+// block's share by itself.
+__device__ __forceinline__ Share share_of(const Kv4KernelArgs& p) {
   const AttentionArgs& a = p.r.a;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  float* factor = scratch;                            // (part, row)
-  float* red = scratch + kMostParts * kRows;          // (wave, lane, E)
-  float* per_wave = red + 256 * E;                    // (wave, row): maxima, then sums
-  // Row tid % 16, every sixteenth part from tid / 16 on.
-  constexpr int kOwn = kMostParts / 16;
-  const int row = tid & 15, p0 = tid >> 4;
-  auto slot = [&](int part) { return (size_t)(sh.first + part * sh.step); };
-  float own_m = -INFINITY, own_l = 0;
-  if (row < rows) {
-#pragma unroll 4
-    for (int j = 0; j < kOwn; ++j) {
-      const int part = p0 + 16 * j;
-      if (part >= sh.parts) break;
-      const FloatPair ml = handoff_load_pair(p.r.part_ml + (slot(part) * kRows + row) * 2);
-      factor[part * kRows + row] = ml.a;
-      const float m = fmaxf(own_m, ml.a), off = m == -INFINITY ? 0.f : m;
-      own_l = own_l * __builtin_amdgcn_exp2f(own_m - off) + ml.b * __builtin_amdgcn_exp2f(ml.a - off);
-      own_m = m;
-    }
+  const int lane = threadIdx.x & 63, id = blockIdx.x;
+  const int per = (a.B + 63) / 64;  // neighbouring sequences of a lane
+  Sequence own = sequence_of(p.r, lane * per);
+  float work = (float)own.tiles * (float)own.chunks;
+#pragma unroll 1
+  for (int i = 1; i < per; ++i) {
+    const Sequence s = sequence_of(p.r, lane * per + i);
+    work += (float)s.tiles * (float)s.chunks;
   }
-  float m = fmaxf(own_m, __shfl_xor(own_m, 16));
-  m = fmaxf(m, __shfl_xor(m, 32));
-  if (lane < 16) per_wave[wave * kRows + row] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) m = fmaxf(m, per_wave[w * kRows + row]);
-  const float off = m == -INFINITY ? 0.f : m;
-  own_l *= __builtin_amdgcn_exp2f(own_m - off);
-  own_l += __shfl_xor(own_l, 16);
-  own_l += __shfl_xor(own_l, 32);
-  float* sums = per_wave + kWaves * kRows;
-  if (lane < 16) sums[wave * kRows + row] = own_l;
-  if (row < rows)
-    for (int part = p0; part < sh.parts; part += 16) factor[part * kRows + row] = __builtin_amdgcn_exp2f(factor[part * kRows + row] - off);
-  __syncthreads();
+  work = sum_of_wave(work);
+  // (a little more than work / parts, so that the rounding of the sums does not make more parts)
+  const int c = max((int)(work / (float)p.parts * 1.00001f) + 1, kLeastChunks);
+  const float inverse = 1 / (float)c;
+  auto parts_of = [&](const Sequence& s) { return min(max(divided_up(s.chunks, c, inverse), 1), kMostParts); };
+  int parts = parts_of(own), blocks = parts * own.tiles;
+#pragma unroll 1
+  for (int i = 1; i < per; ++i) {
+    const Sequence s = sequence_of(p.r, lane * per + i);
+    blocks += parts_of(s) * s.tiles;
+  }
+  int at = running_sum(blocks) - blocks, b = lane * per;
+  const uint64_t here = __ballot(id >= at && id < at + blocks);
+  Share r;
+  r.b = -1;
+  if (here == 0) return r;
+#pragma unroll 1
+  for (int i = 1; i < per && id >= at + parts * own.tiles; ++i) {  // (the lane found gets to its sequence)
+    at += parts * own.tiles;
+    own = sequence_of(p.r, ++b);
+    parts = parts_of(own);
+  }
+  const int from = __builtin_ctzll(here);
+  auto get = [&](int v) { return __builtin_amdgcn_readlane(v, from); };
+  r.b = get(b);
+  r.parts = get(parts);
+  r.span = {get(own.span.q0), get(own.span.q1), get(own.span.kv), get(own.span.first)};
+  const int off = id - get(at), rtiles = get(own.tiles) / a.Hkv;
+  r.step = rtiles * a.Hkv;
+  r.part = off / r.step;
+  const int rest = off - r.part * r.step;
+  r.hk = rest / rtiles;
+  r.rt = rest - r.hk * rtiles;
+  r.first = id - r.part * r.step;
+  return r;
+}
+
+// What a tile's end needs to know of a row: where its result goes (the element's index; -1: no
+// such row), and whether it sees a key.
+struct RowEnd {
+  long long at;
+  int some;
+};
+
+// Joins a tile's parts: the block that arrives last. scratch: LDS of 16 D + 2 * kWaves * kRows floats.
+// A wave takes every fourth part, four rows at a time.
+template <int D, typename PACK>
+__device__ __forceinline__ void join_parts(const Kv4KernelArgs& p, const Share& sh, const RowEnd* ends, int rows, float* scratch, PACK pack) {
+  constexpr int E = D / 16, BATCH = 64 / E;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  float* red = scratch;             // (wave, E, lane)
+  float* wave_ml = scratch + 16 * D;  // (wave, row): maximum, sum
   for (int r0 = 0; r0 < rows; r0 += 4) {
-    // Lane: row r0 + lane / 16, E neighbouring dimensions.
+    // Lane: row r0 + lane / 16, E neighbouring dimensions; BATCH parts at a time.
     const int r = r0 + (lane >> 4);
     const bool live = r < rows;
-    const float* from = p.r.part + (min(r, rows - 1) * 16 + (lane & 15)) * 2;
-    float o[E] = {};
+    const int row = min(r, rows - 1);
+    float m = -INFINITY, l = 0, o[E] = {};
     for (int q0 = wave; q0 < sh.parts; q0 += kWaves * BATCH) {
-      FloatPair v[BATCH][E / 2];
-#pragma unroll
-      for (int y = 0; y < BATCH; ++y)
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e)
-          v[y][e] = handoff_load_pair(from + slot(min(q0 + y * kWaves, sh.parts - 1)) * kRows * D + 512 * e);
+      FloatPair v[BATCH][E / 2], ml[BATCH];
 #pragma unroll
       for (int y = 0; y < BATCH; ++y) {
-        const int part = q0 + y * kWaves;
-        const float f = live && part < sh.parts ? factor[part * kRows + r] : 0.f;
+        const int part = min(q0 + y * kWaves, sh.parts - 1);
+        const size_t slot = (size_t)(sh.first + part * sh.step) * kRows;
+        ml[y] = handoff_load_pair(p.r.part_ml + (slot + row) * 2);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) v[y][e] = handoff_load_pair(p.r.part + slot * D + (row * 16 + (lane & 15)) * 2 + 512 * e);
+      }
+      float n = m;
+#pragma unroll
+      for (int y = 0; y < BATCH; ++y) n = fmaxf(n, ml[y].a);
+      const float off = n == -INFINITY ? 0.f : n, f = __builtin_amdgcn_exp2f(m - off);
+      m = n;
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+      for (int y = 0; y < BATCH; ++y) {
+        if (q0 + y * kWaves >= sh.parts) break;  // (the last part again)
+        const float w = __builtin_amdgcn_exp2f(ml[y].a - off);
+        l += ml[y].b * w;
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) {
-          o[2 * e] += v[y][e].a * f;
-          o[2 * e + 1] += v[y][e].b * f;
+          o[2 * e] += v[y][e].a * w;
+          o[2 * e + 1] += v[y][e].b * w;
         }
       }
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) red[(wave * E + e) * 64 + lane] = o[e];
+    if ((lane & 15) == 0) wave_ml[(wave * 4 + (lane >> 4)) * 2] = m, wave_ml[(wave * 4 + (lane >> 4)) * 2 + 1] = l;
     __syncthreads();
     constexpr int PER = E / 4 > 2 ? E / 4 : 2;  // dimensions a wave finishes
     if (live && wave * PER < E) {
-      const Row mine = row_of(p.r, sh.rt * kRows + r, span, sh.hk);
-      const float l = sums[r] + sums[kRows + r] + sums[2 * kRows + r] + sums[3 * kRows + r];
-      const float inv = mine.lo < mine.hi ? 1 / l : 0.f;
-      uint16_t* dst = a.out + ((long long)mine.token * a.Hq + mine.head) * D + (lane & 15) * E + wave * PER;
+      float f[kWaves], n = -INFINITY, sum = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) n = fmaxf(n, wave_ml[(w * 4 + (lane >> 4)) * 2]);
+      const float off = n == -INFINITY ? 0.f : n;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        f[w] = __builtin_amdgcn_exp2f(wave_ml[(w * 4 + (lane >> 4)) * 2] - off);
+        sum += wave_ml[(w * 4 + (lane >> 4)) * 2 + 1] * f[w];
+      }
+      const RowEnd end = ends[r];
+      const float inv = end.some ? 1 / sum : 0.f;
+      uint16_t* dst = p.r.a.out + end.at + (lane & 15) * E + wave * PER;
 #pragma unroll
       for (int e = 0; e < PER; e += 2) {
         float x = 0, y = 0;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-          x += red[(w * E + wave * PER + e) * 64 + lane];
-          y += red[(w * E + wave * PER + e + 1) * 64 + lane];
+          x += red[(w * E + wave * PER + e) * 64 + lane] * f[w];
+          y += red[(w * E + wave * PER + e + 1) * 64 + lane] * f[w];
         }
         *reinterpret_cast<uint32_t*>(dst + e) = pack(x * inv, y * inv);
       }
@@ -337,8 +354,8 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4Ker
   constexpr int STEPS = D / 32, U = D / 64, GS = D / G, BLOCK = kv4_block_bytes(D, G);
   constexpr int NS = GS == 32 ? U : G;  // sets of scales that a lane needs for its values
   constexpr int LD = D + 4;
-  constexpr int kJoin = kMostParts * kRows + 16 * D + 2 * kWaves * kRows, kMeet = kWaves * kRows * (LD + 2);
-  __shared__ __attribute__((aligned(16))) float shared[kJoin > kMeet ? kJoin : kMeet];
+  __shared__ __attribute__((aligned(16))) float shared[kWaves * kRows * (LD + 2)];  // (the join of parts needs less)
+  __shared__ RowEnd ends[kRows];
   __shared__ int s_last;
   float (*so)[kRows][LD] = reinterpret_cast<float (*)[kRows][LD]>(shared);
   float (*sml)[kRows][2] = reinterpret_cast<float (*)[kRows][2]>(shared + kWaves * kRows * LD);
@@ -349,8 +366,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4Ker
   const uint8_t* v_cache = reinterpret_cast<const uint8_t*>(a.v_cache);
   Share share;
   if (k.parts) {
-    __shared__ int scratch[16];
-    share = share_of(k, scratch);
+    share = share_of(k);
     if (share.b < 0) return;
   } else {
     // Blocks of the row tiles that read the same keys follow each other on one XCD.
@@ -368,69 +384,23 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4Ker
   const Row row = row_of(p, rt * kRows + (NARROW ? n & 3 : n), span, hk);
   ScoreRule rule = score_rule(a, row.head);
 
-  // The keys that any row sees, and those that all see.
+  // The keys that any row sees, and those that all see (rows past the last count as seeing all).
   int lo = row.lo < row.hi ? row.lo : INT32_MAX, hi = row.lo < row.hi ? row.hi : 0;
-  int all_lo = row.token < 0 ? 0 : row.lo, all_hi = row.token < 0 ? INT32_MAX : row.hi;  // rows past the last count as seeing all
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
-    lo = min(lo, __shfl_xor(lo, o));
-    hi = max(hi, __shfl_xor(hi, o));
-    all_lo = max(all_lo, __shfl_xor(all_lo, o));
-    all_hi = min(all_hi, __shfl_xor(all_hi, o));
-  }
-  lo = __builtin_amdgcn_readfirstlane(lo);
-  hi = __builtin_amdgcn_readfirstlane(hi);
-  all_lo = __builtin_amdgcn_readfirstlane(all_lo);
-  all_hi = __builtin_amdgcn_readfirstlane(all_hi);
+  int all_lo = row.token < 0 ? 0 : row.lo, all_hi = row.token < 0 ? INT32_MAX : row.hi;
+  lo = __builtin_amdgcn_readfirstlane(least_of_row(lo));
+  hi = __builtin_amdgcn_readfirstlane(largest_of_row(hi));
+  all_lo = __builtin_amdgcn_readfirstlane(largest_of_row(all_lo));
+  all_hi = __builtin_amdgcn_readfirstlane(least_of_row(all_hi));
   auto seen_by_all = [&](int c) { return c * kChunk >= all_lo && (uint32_t)(c + 1) * kChunk <= (uint32_t)all_hi; };
   const int c_first = lo < hi ? lo / kChunk : 0, chunks = lo < hi ? (hi - 1) / kChunk + 1 - c_first : 0;
   const int c0 = c_first + (int)((long long)chunks * share.part / share.parts), c1 = c_first + (int)((long long)chunks * (share.part + 1) / share.parts);
 
-  // The row's query in fp16, and its groups' sums in three parts (lane group 0: the first, ...).
-  u32x4 q[STEPS], qsum = {0, 0, 0, 0};
-  {
-    u32x4 raw[STEPS];
-    uint32_t most = 0;  // of the values' bits without a sign: in the order of their sizes
+  // The row's query, asked for ahead of the keys that its use waits for too.
+  u32x4 raw[STEPS];
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      raw[s] = row.token < 0 ? u32x4{0, 0, 0, 0}
-                             : *reinterpret_cast<const u32x4*>(a.q + row.token * a.q_stride + (long long)row.head * D + s * 32 + kg * 8);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) most = max(most, max(raw[s][x] & 0x7FFFu, raw[s][x] >> 16 & 0x7FFFu));
-    }
-    most = max(most, (uint32_t)__shfl_xor((int)most, 16));
-    most = max(most, (uint32_t)__shfl_xor((int)most, 32));
-    const float largest = bf16_data ? bits_to_float<true>((uint16_t)most) : bits_to_float<false>((uint16_t)most);
-    const bool finite = largest < INFINITY;
-    const int up = min(max(254 - (int)(__builtin_bit_cast(uint32_t, largest) >> 23), 1), 253);  // exponent field of the factor
-    const float factor = finite ? __builtin_bit_cast(float, (uint32_t)up << 23) : NAN;
-    const float back = __builtin_bit_cast(float, (uint32_t)(254 - up) << 23);
-    rule.scale = fminf(fmaxf(rule.scale * back, -3e38f), 3e38f);
-    rule.inverse = fminf(fmaxf(rule.inverse * back, -3e38f), 3e38f);
-    float sums[G] = {};
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint16_t b0 = (uint16_t)raw[s][x], b1 = (uint16_t)(raw[s][x] >> 16);
-        const float f0 = bf16_data ? bits_to_float<true>(b0) : bits_to_float<false>(b0);
-        const float f1 = bf16_data ? bits_to_float<true>(b1) : bits_to_float<false>(b1);
-        const f16x2 h = {(f16)(f0 * factor), (f16)(f1 * factor)};
-        q[s][x] = as_u32(h);
-        sums[s * 32 / GS] += (float)h[0] + (float)h[1];
-      }
-    f16 part_of[8] = {};
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      float s = sums[g];
-      s += __shfl_xor(s, 16);
-      s += __shfl_xor(s, 32);
-      const f16 first = (f16)s, second = (f16)(s - (float)first), third = (f16)(s - (float)first - (float)second);
-      part_of[g] = kg == 0 ? first : kg == 1 ? second : kg == 2 ? third : (f16)0.f;
-    }
-#pragma unroll
-    for (int x = 0; x < 4; ++x) qsum[x] = as_u32(f16x2{part_of[2 * x], part_of[2 * x + 1]});
-  }
+  for (int s = 0; s < STEPS; ++s)
+    raw[s] = row.token < 0 ? u32x4{0, 0, 0, 0}
+                           : *reinterpret_cast<const u32x4*>(a.q + row.token * a.q_stride + (long long)row.head * D + s * 32 + kg * 8);
 
   // Number of the block of eight tokens that holds tokens 8 (lane & 3) on of a chunk; past
   // the seen keys' ends the nearest.
@@ -465,11 +435,69 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4Ker
     vm = *reinterpret_cast<const u32x4*>(vmiddles + at);
   };
 
+  uint32_t blocks = 0, blocks_next = 0;
+  int c = c0 + wave;
+  if (c < c1) {
+    blocks = token_block(c);
+    load_k(blocks);
+    load_v(blocks);
+    blocks_next = token_block(c + kWaves);
+  }
+
+  // The row's query in fp16, and its groups' sums in three parts (lane group 0: the first, ...).
+  u32x4 q[STEPS], qsum = {0, 0, 0, 0};
+  float back;  // what undoes the factor
+  {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 pairs = {0, 0};  // of the values' bits without a sign, in the order of their sizes
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) pairs = __builtin_elementwise_max(pairs, __builtin_bit_cast(u16x2, raw[s][x] & 0x7FFF7FFFu));
+    int most = max(pairs[0], pairs[1]);
+    most = max(most, __shfl_xor(most, 16));
+    most = max(most, __shfl_xor(most, 32));
+    // The factor's exponent; of fp16 data within fp16's.
+    if (bf16_data) {
+      const int up = min(max(254 - (most >> 7), 1), 253);
+      const float factor = most < 0x7F80 ? __builtin_bit_cast(float, (uint32_t)up << 23) : NAN;
+      back = __builtin_bit_cast(float, (uint32_t)(254 - up) << 23);
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          q[s][x] = pack_pair<false>(__builtin_bit_cast(float, raw[s][x] << 16) * factor, __builtin_bit_cast(float, raw[s][x] & 0xFFFF0000u) * factor);
+    } else {
+      const int up = min(max(30 - (most >> 10), 1), 30);
+      const f16 factor = most < 0x7C00 ? __builtin_bit_cast(f16, (uint16_t)(up << 10)) : (f16)NAN;
+      back = __builtin_bit_cast(float, (uint32_t)(127 + 15 - up) << 23);
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) q[s][x] = as_u32(as_f16x2(raw[s][x]) * f16x2{factor, factor});
+    }
+    rule.scale = fminf(fmaxf(rule.scale * back, -3e38f), 3e38f);
+    rule.inverse = fminf(fmaxf(rule.inverse * back, -3e38f), 3e38f);
+    // The sums: products with ones, in every lane of a column.
+    f16 part_of[8] = {};
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      constexpr uint32_t ones = 0x3C003C00u;
+      f32x4 sums = {};
+#pragma unroll
+      for (int s = g * GS / 32; s < (g + 1) * GS / 32; ++s) sums = mfma16<false>(u32x4{ones, ones, ones, ones}, q[s], sums);
+      const float s = sums[0];
+      const f16 first = (f16)s, second = (f16)(s - (float)first), third = (f16)(s - (float)first - (float)second);
+      part_of[g] = kg == 0 ? first : kg == 1 ? second : kg == 2 ? third : (f16)0.f;
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) qsum[x] = as_u32(f16x2{part_of[2 * x], part_of[2 * x + 1]});
+  }
+
   const DecodeMasks masks;
   f32x4 acc[U][4] = {}, rest = {};  // rest: rows g the sums of p m_g, row 15 the sum of p
   float mx = -INFINITY;
   bool any_bad = false;
-  uint32_t blocks = 0, blocks_next = 0;
   // One chunk; with MORE the next one's loads go out as the registers fall free.
   auto step = [&](int c, auto more) {
     constexpr bool MORE = decltype(more)::value;
@@ -615,12 +643,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4Ker
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  int c = c0 + wave;
   if (c < c1) {
-    blocks = token_block(c);
-    load_k(blocks);
-    load_v(blocks);
-    blocks_next = token_block(c + kWaves);
     for (; c + kWaves < c1; c += kWaves) step(c, std::true_type{});
     step(c, std::false_type{});
   }
@@ -644,6 +667,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4Ker
           f32x4{acc[u][0][r], acc[u][1][r], acc[u][2][r], acc[u][3][r]} + middle;
   }
   if (kg == 0) sml[wave][n][0] = mx, sml[wave][n][1] = sum;
+  if (tid < kRows) ends[tid] = {row.token < 0 ? -1 : ((long long)row.token * a.Hq + row.head) * D, row.lo < row.hi};
   if (any_bad) {
     // Rare: the groups left out above, to the rows that see them.
     for (int c = c0 + wave; c < c1; c += kWaves) {
@@ -685,13 +709,12 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4Ker
       if ((tid & 15) == 0) handoff_store(p.part_ml + ((size_t)blockIdx.x * kRows + r) * 2, m, l);
     }
     const size_t tile = ((size_t)b * a.Hkv + hk) * p.rtiles + rt;
-    if (handoff_last(&p.counters[tile], (uint32_t)share.parts, &s_last)) join_parts<D>(k, share, span, rows, shared, pack);
+    if (handoff_last(&p.counters[tile], (uint32_t)share.parts, &s_last)) join_parts<D>(k, share, ends, rows, shared, pack);
     return;
   }
   if (r >= rows) return;
-  const Row mine = row_of(p, rt * kRows + r, span, hk);
-  const float inv = mine.lo < mine.hi ? 1 / l : 0.f;
-  uint16_t* dst = a.out + ((long long)mine.token * a.Hq + mine.head) * D + d0;
+  const float inv = ends[r].some ? 1 / l : 0.f;
+  uint16_t* dst = a.out + ends[r].at + d0;
 #pragma unroll
   for (int e = 0; e < E; e += 4)
     *reinterpret_cast<u32x2*>(dst + e) = u32x2{pack(o[e] * inv, o[e + 1] * inv), pack(o[e + 2] * inv, o[e + 3] * inv)};
