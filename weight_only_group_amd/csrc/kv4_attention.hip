@@ -135,9 +135,10 @@ __device__ __forceinline__ void load_words(uint32_t (&to)[BYTES / 4], const uint
 }
 
 // How many parts the keys of each tile are split into, so that the parts are alike
-// whatever the sequences' lengths: with c chunks a part, sum ceil(chunks / c) is at most sum chunks / c + tiles, so c =
-// sum chunks / parts gives no more blocks than parts + tiles. A sequence's chunks are those of its
-// first and last query.
+// whatever the sequences' lengths, and so many as run at a time: a block's start and end
+// take 10 us. With c chunks a part, sum ceil(chunks / c) is at most sum chunks / c + tiles, so c =
+// sum chunks / parts gives no more blocks than parts + tiles; smaller ones are tried first.
+// A sequence's chunks are those of its first and last query.
 constexpr int kMostSequences = 1024;  // of a split launch
 constexpr int kMostTiles = 4096;
 constexpr int kMostParts = 256;       // of a tile
@@ -148,20 +149,18 @@ inline int resident_blocks(int D, DeviceTopo topo) { return topo.cus * (D == 64 
 
 struct Kv4Plan {
   int group, rtiles;
-  int parts;  // parts wanted beyond one a tile; 0: one a tile
+  int fit;    // blocks that run at a time
+  int parts;  // parts beyond one a tile that there may be; 0: one a tile
   long long blocks;
 };
-#ifndef KV4_X
-#define KV4_X 4
-#endif
 Kv4Plan kv4_plan(int B, int Hq, int Hkv, int D, int max_q, int max_kv, DeviceTopo topo) {
   Kv4Plan p;
   p.group = Hq / Hkv;
   p.rtiles = row_tiles(max_q, p.group, kRows);
   const long long tiles = (long long)B * Hkv * p.rtiles;
-  const int fit = resident_blocks(D, topo);
+  p.fit = resident_blocks(D, topo);
   p.parts = 0;
-  if (B <= kMostSequences && tiles <= kMostTiles && max_kv > kLeastChunks * kChunk) p.parts = (int)std::max(fit * KV4_X / 4 - tiles, fit * KV4_X / 8ll);
+  if (B <= kMostSequences && tiles <= kMostTiles && max_kv > kLeastChunks * kChunk) p.parts = (int)std::max(p.fit - tiles, p.fit / 2ll);
   const long long most = ((long long)max_kv + kLeastChunks * kChunk - 1) / (kLeastChunks * kChunk);
   p.blocks = p.parts ? std::min(tiles + p.parts, tiles * most) : tile_blocks(B, Hkv, p.rtiles);
   return p;
@@ -169,7 +168,7 @@ Kv4Plan kv4_plan(int B, int Hq, int Hkv, int D, int max_q, int max_kv, DeviceTop
 
 struct Kv4KernelArgs {
   AttnKernelArgs r;
-  int parts;
+  int fit, parts;
   Cap cap;
   bool bf16;
 };
@@ -221,15 +220,27 @@ __device__ __forceinline__ Share share_of(const Kv4KernelArgs& p) {
     work += (float)s.tiles * (float)s.chunks;
   }
   work = sum_of_wave(work);
-  // (a little more than work / parts, so that the rounding of the sums does not make more parts)
-  const int c = max((int)(work / (float)p.parts * 1.00001f) + 1, kLeastChunks);
-  const float inverse = 1 / (float)c;
+  // Chunks a part: from the fewest that fit on, as long as they make more blocks than run at a
+  // time; after some tries those that surely make few enough. (a little more than the quotient: the
+  // sums are rounded)
+  int c = 0, parts = 0, blocks = 0;
+  float inverse = 0, wanted = work / (float)p.fit;
   auto parts_of = [&](const Sequence& s) { return min(max(divided_up(s.chunks, c, inverse), 1), kMostParts); };
-  int parts = parts_of(own), blocks = parts * own.tiles;
 #pragma unroll 1
-  for (int i = 1; i < per; ++i) {
-    const Sequence s = sequence_of(p.r, lane * per + i);
-    blocks += parts_of(s) * s.tiles;
+  for (int i = 0; i < 5; ++i) {
+    if (i == 4) wanted = work / (float)p.parts;
+    c = max((int)(wanted * 1.00001f) + 1, kLeastChunks);
+    inverse = 1 / (float)c;
+    parts = parts_of(own);
+    blocks = parts * own.tiles;
+#pragma unroll 1
+    for (int i = 1; i < per; ++i) {
+      const Sequence s = sequence_of(p.r, lane * per + i);
+      blocks += parts_of(s) * s.tiles;
+    }
+    const int all = __builtin_amdgcn_readlane(running_sum(blocks), 63);
+    if (all <= p.fit) break;
+    wanted = (float)c * fmaxf((float)all / (float)p.fit, 1.03f);
   }
   int at = running_sum(blocks) - blocks, b = lane * per;
   const uint64_t here = __ballot(id >= at && id < at + blocks);
@@ -724,7 +735,7 @@ template <int D, int G>
 hipError_t launch_split(const AttentionArgs& a, bool bf16, hipStream_t stream) {
   const Kv4Plan plan = kv4_plan(a.B, a.Hq, a.Hkv, D, a.max_q, a.max_kv, device_topology());
   Kv4KernelArgs p = {{a, fixed_div(a.page_size), fixed_div(plan.group), plan.group, plan.rtiles, 1, reinterpret_cast<uint32_t*>(a.workspace), nullptr, nullptr},
-                     plan.parts, cap_kind(a.softcap), bf16};
+                     plan.fit, plan.parts, cap_kind(a.softcap), bf16};
   if (plan.parts) {
     p.r.part = reinterpret_cast<float*>(a.workspace + kWorkspaceHeader);
     p.r.part_ml = p.r.part + plan.blocks * kRows * D;
