@@ -18,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 SOURCES = ("api.hip", "pack.hip", "dequant.hip", "gemv.hip", "gemv_wave_b1.hip", "gemv_wave_b2.hip",
            "gemv_wave_b3.hip", "gemv_wave_b4.hip", "gemv_wave_b8.hip", "gemm.hip", "strips.hip",
            "layer_api.hip", "moe.hip", "kv_append.hip", "attention.hip", "logprobs.hip",
-           "cache_api.hip", "kv4_append.hip", "kv4_attention.hip", "kv_pages.hip")
+           "cache_api.hip", "kv4_append.hip", "kv4_attention.hip", "kv4_tile_64.hip",
+           "kv4_tile_128.hip", "kv4_tile_256.hip", "kv_pages.hip")
 LIB_NAME = "libqmm.so"
 # Reference kernels for measurement (empty launch, streaming read, MFMA loop);
 # a library of their own, outside the qmm ABI.

@@ -1,0 +1,104 @@
+// What the attention kernels over the 4-bit cache have in common.
+//
+// The formulas of the attention to a cache of 16-bit values, with k_j = m + s (c - 8) per
+// group of channels, taken apart so that what the matrix cores see is exact in fp16:
+//   q.k_j = sum_d q_d [s_j (c_jd - 8)] + sum_g m_jg Q_g,     Q_g = sum of the group's q_d
+//   sum_j p_j v_j = sum_j p_j [s_j (c_jd - 8)] + sum_j p_j m_jg
+// s has 8 significant bits and c - 8 three and a sign, so the brackets are fp16 numbers.
+// A code becomes one by an AND, an OR and half a packed multiply-add: the half 16 + c
+// has it in the top of its mantissa, and s (16 + c) - 24 s is rounded once, so not at all.
+// The second sums are one matrix operation more for all channels together, with
+// the middles as further channels; Q goes in three fp16 parts (33 bits). A row of ones among
+// the value's middles gives the weights' sum.
+//
+// Queries are scaled by a power of two, so that a row's largest is in [1, 2) and fp16
+// holds them whatever their type. The weights p are fp16, times 2^7.
+#pragma once
+
+#include "attention_rows.h"
+#include "cache.h"
+
+namespace qmm {
+namespace {
+
+// A row's maximum is left where it is while no weight passes 2^kSlack of it; weights are
+// kept times 2^kLift, so that they pass neither end of fp16.
+constexpr float kLift = 7.f, kSlack = 8.f;
+
+// The AND's and the OR's constant, in registers: as literals they would take an instruction each.
+struct DecodeMasks {
+  uint32_t code, sixteen;
+  __device__ __forceinline__ DecodeMasks() {
+    asm("s_mov_b32 %0, 0x03C003C0" : "=s"(code));
+    asm("v_mov_b32 %0, 0x4C004C00" : "=v"(sixteen));
+  }
+};
+
+// Two of a word's codes, nibbles R and R + 4, as s (c - 8); c24 = -24 s.
+template <int R>
+__device__ __forceinline__ uint32_t decode(uint32_t w, f16x2 s, f16x2 c24, const DecodeMasks& k) {
+  const uint32_t at = R == 0 ? w << 6 : R == 1 ? w << 2 : R == 2 ? w >> 2 : w >> 6;
+  return as_u32(__builtin_elementwise_fma(as_f16x2((at & k.code) | k.sixteen), s, c24));
+}
+__device__ __forceinline__ f16x2 times_24(f16x2 s) { return s * f16x2{(f16)-24.f, (f16)-24.f}; }  // exact: 10 bits
+
+// Whether a half of the pair is an infinity or a NaN, as a mask of those halves.
+__device__ __forceinline__ uint32_t not_finite_halves(uint32_t v) {
+  return (not_finite<false>(v) ? 0xFFFFu : 0u) | (not_finite<false>(v >> 16) ? 0xFFFF0000u : 0u);
+}
+
+// BYTES (a multiple of 4, up to 32) from p as 32-bit words.
+template <int BYTES>
+__device__ __forceinline__ void load_words(uint32_t* to, const uint8_t* p) {
+  if constexpr (BYTES % 16 == 0) {
+#pragma unroll
+    for (int i = 0; i < BYTES / 16; ++i) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(p + 16 * i);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) to[4 * i + x] = v[x];
+    }
+  } else if constexpr (BYTES == 8) {
+    const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+    to[0] = v[0];
+    to[1] = v[1];
+  } else {
+    to[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+constexpr uint32_t kOnes = 0x3C003C00u;  // two halves of 1
+
+// A row's query (N * 8 values in each of LANES lanes, 64 / LANES apart) as fp16, scaled by a
+// power of two; returns what undoes that. All NaN where a value is not finite.
+template <int LANES, int N>
+__device__ __forceinline__ float scale_query(u32x4 (&q)[N], bool bf16_data) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 pairs = {0, 0};  // of the values' bits without a sign, in the order of their sizes
+#pragma unroll
+  for (int s = 0; s < N; ++s)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) pairs = __builtin_elementwise_max(pairs, __builtin_bit_cast(u16x2, q[s][x] & 0x7FFF7FFFu));
+  int most = max(pairs[0], pairs[1]);
+  if (LANES == 4) most = max(most, __shfl_xor(most, 16));
+  most = max(most, __shfl_xor(most, 32));
+  if (bf16_data) {
+    const int up = min(max(254 - (most >> 7), 1), 253);  // the factor's exponent
+    const float factor = most < 0x7F80 ? __builtin_bit_cast(float, (uint32_t)up << 23) : NAN;
+#pragma unroll
+    for (int s = 0; s < N; ++s)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        q[s][x] = pack_pair<false>(__builtin_bit_cast(float, q[s][x] << 16) * factor, __builtin_bit_cast(float, q[s][x] & 0xFFFF0000u) * factor);
+    return __builtin_bit_cast(float, (uint32_t)(254 - up) << 23);
+  }
+  const int up = min(max(30 - (most >> 10), 1), 30);  // (within fp16's: tiny queries stay below 1)
+  const f16 factor = most < 0x7C00 ? __builtin_bit_cast(f16, (uint16_t)(up << 10)) : (f16)NAN;
+#pragma unroll
+  for (int s = 0; s < N; ++s)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) q[s][x] = as_u32(as_f16x2(q[s][x]) * f16x2{factor, factor});
+  return __builtin_bit_cast(float, (uint32_t)(127 + 15 - up) << 23);
+}
+
+}  // namespace
+}  // namespace qmm

@@ -1,52 +1,12 @@
-// Attention of new tokens to their sequences' cache in 4 bits.
-//
-// The formulas of the attention to a cache of 16-bit values, with k_j = m + s (c - 8) per
-// group of channels, taken apart so that what the matrix cores see is exact in fp16:
-//   q.k_j = sum_d q_d [s_j (c_jd - 8)] + sum_g m_jg Q_g,     Q_g = sum of the group's q_d
-//   sum_j p_j v_j = sum_j p_j [s_j (c_jd - 8)] + sum_j p_j m_jg
-// s has 8 significant bits and c - 8 three and a sign, so the brackets are fp16 numbers.
-// A code becomes one by an AND, an OR and half a packed multiply-add: the half 16 + c
-// has it in the top of its mantissa, and s (16 + c) - 24 s is rounded once, so not at all.
-// The second sums are one matrix operation more for all channels together, with
-// the middles as further channels; Q goes in three fp16 parts (33 bits). A row of ones among
-// the value's middles gives the weights' sum.
-//
-// Queries are scaled by a power of two, so that a row's largest is in [1, 2) and fp16
-// holds them whatever their type. The weights p are fp16, times 2^7.
+// Attention of new tokens to their sequences' cache in 4 bits: single tokens and few rows.
 #include <algorithm>
 #include <type_traits>
 
-#include "attention_rows.h"
-#include "cache.h"
+#include "kv4_attention.h"
+#include "kv4_tile.h"
 
 namespace qmm {
 namespace {
-
-// A row's maximum is left where it is while no weight passes 2^kSlack of it; weights are
-// kept times 2^kLift, so that they pass neither end of fp16.
-constexpr float kLift = 7.f, kSlack = 8.f;
-
-// The AND's and the OR's constant, in registers: as literals they would take an instruction each.
-struct DecodeMasks {
-  uint32_t code, sixteen;
-  __device__ __forceinline__ DecodeMasks() {
-    asm("s_mov_b32 %0, 0x03C003C0" : "=s"(code));
-    asm("v_mov_b32 %0, 0x4C004C00" : "=v"(sixteen));
-  }
-};
-
-// Two of a word's codes, nibbles R and R + 4, as s (c - 8); c24 = -24 s.
-template <int R>
-__device__ __forceinline__ uint32_t decode(uint32_t w, f16x2 s, f16x2 c24, const DecodeMasks& k) {
-  const uint32_t at = R == 0 ? w << 6 : R == 1 ? w << 2 : R == 2 ? w >> 2 : w >> 6;
-  return as_u32(__builtin_elementwise_fma(as_f16x2((at & k.code) | k.sixteen), s, c24));
-}
-__device__ __forceinline__ f16x2 times_24(f16x2 s) { return s * f16x2{(f16)-24.f, (f16)-24.f}; }  // exact: 10 bits
-
-// Whether a half of the pair is an infinity or a NaN, as a mask of those halves.
-__device__ __forceinline__ uint32_t not_finite_halves(uint32_t v) {
-  return (not_finite<false>(v) ? 0xFFFFu : 0u) | (not_finite<false>(v >> 16) ? 0xFFFF0000u : 0u);
-}
 
 // Lane exchanges within rows of sixteen: a value of the lane R to the right (round the
 // row; or, of lanes past its end, anything).
@@ -113,25 +73,6 @@ __device__ __forceinline__ int largest_of_row(int v) {
 __device__ __forceinline__ float max_of_rows(float v) {
   v = fmaxf(v, __shfl_xor(v, 16));
   return fmaxf(v, __shfl_xor(v, 32));
-}
-
-// BYTES (a multiple of 4, up to 32) from p as 32-bit words.
-template <int BYTES>
-__device__ __forceinline__ void load_words(uint32_t (&to)[BYTES / 4], const uint8_t* p) {
-  if constexpr (BYTES % 16 == 0) {
-#pragma unroll
-    for (int i = 0; i < BYTES / 16; ++i) {
-      const u32x4 v = *reinterpret_cast<const u32x4*>(p + 16 * i);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) to[4 * i + x] = v[x];
-    }
-  } else if constexpr (BYTES == 8) {
-    const u32x2 v = *reinterpret_cast<const u32x2*>(p);
-    to[0] = v[0];
-    to[1] = v[1];
-  } else {
-    to[0] = *reinterpret_cast<const uint32_t*>(p);
-  }
 }
 
 // How many parts the keys of each tile are split into, so that the parts are alike
@@ -457,46 +398,18 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4Ker
 
   // The row's query in fp16, and its groups' sums in three parts (lane group 0: the first, ...).
   u32x4 q[STEPS], qsum = {0, 0, 0, 0};
-  float back;  // what undoes the factor
   {
-    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-    u16x2 pairs = {0, 0};  // of the values' bits without a sign, in the order of their sizes
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) pairs = __builtin_elementwise_max(pairs, __builtin_bit_cast(u16x2, raw[s][x] & 0x7FFF7FFFu));
-    int most = max(pairs[0], pairs[1]);
-    most = max(most, __shfl_xor(most, 16));
-    most = max(most, __shfl_xor(most, 32));
-    // The factor's exponent; of fp16 data within fp16's.
-    if (bf16_data) {
-      const int up = min(max(254 - (most >> 7), 1), 253);
-      const float factor = most < 0x7F80 ? __builtin_bit_cast(float, (uint32_t)up << 23) : NAN;
-      back = __builtin_bit_cast(float, (uint32_t)(254 - up) << 23);
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          q[s][x] = pack_pair<false>(__builtin_bit_cast(float, raw[s][x] << 16) * factor, __builtin_bit_cast(float, raw[s][x] & 0xFFFF0000u) * factor);
-    } else {
-      const int up = min(max(30 - (most >> 10), 1), 30);
-      const f16 factor = most < 0x7C00 ? __builtin_bit_cast(f16, (uint16_t)(up << 10)) : (f16)NAN;
-      back = __builtin_bit_cast(float, (uint32_t)(127 + 15 - up) << 23);
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) q[s][x] = as_u32(as_f16x2(raw[s][x]) * f16x2{factor, factor});
-    }
+    for (int s = 0; s < STEPS; ++s) q[s] = raw[s];
+    const float back = scale_query<4>(q, bf16_data);
     rule.scale = fminf(fmaxf(rule.scale * back, -3e38f), 3e38f);
     rule.inverse = fminf(fmaxf(rule.inverse * back, -3e38f), 3e38f);
-    // The sums: products with ones, in every lane of a column.
     f16 part_of[8] = {};
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      constexpr uint32_t ones = 0x3C003C00u;
-      f32x4 sums = {};
+      f32x4 sums = {};  // in every lane of a column
 #pragma unroll
-      for (int s = g * GS / 32; s < (g + 1) * GS / 32; ++s) sums = mfma16<false>(u32x4{ones, ones, ones, ones}, q[s], sums);
+      for (int s = g * GS / 32; s < (g + 1) * GS / 32; ++s) sums = mfma16<false>(u32x4{kOnes, kOnes, kOnes, kOnes}, q[s], sums);
       const float s = sums[0];
       const f16 first = (f16)s, second = (f16)(s - (float)first), third = (f16)(s - (float)first - (float)second);
       part_of[g] = kg == 0 ? first : kg == 1 ? second : kg == 2 ? third : (f16)0.f;
@@ -624,7 +537,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4Ker
     {
       u32x4 m = vm;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) m[x] = n < G ? m[x] : n == 15 ? 0x3C003C00u : 0u;
+      for (int x = 0; x < 4; ++x) m[x] = n < G ? m[x] : n == 15 ? kOnes : 0u;
       rest = mfma16<false>(m, w, rest);
     }
 #pragma unroll
@@ -746,18 +659,40 @@ hipError_t launch_split(const AttentionArgs& a, bool bf16, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Blocks of many rows where there are enough of them.
+template <int D>
+bool use_tiles_of(int B, int group, int Hkv, int max_q, DeviceTopo topo) {
+  const long long rows = (long long)max_q * group;
+  return rows > 64 && (long long)B * Hkv * ((rows + kKv4TileRows<D> - 1) / kKv4TileRows<D>) * 4 >= topo.cus;
+}
+bool use_tiles(int B, int Hq, int Hkv, int D, int max_q, DeviceTopo topo) {
+  return D == 64 ? use_tiles_of<64>(B, Hq / Hkv, Hkv, max_q, topo)
+         : D == 128 ? use_tiles_of<128>(B, Hq / Hkv, Hkv, max_q, topo) : use_tiles_of<256>(B, Hq / Hkv, Hkv, max_q, topo);
+}
+
 }  // namespace
 
 size_t kv4_attention_workspace(int B, int T, int Hq, int Hkv, int D, int max_q, int max_kv) {
+  if (use_tiles(B, Hq, Hkv, D, max_q, device_topology())) return 0;
   const Kv4Plan p = kv4_plan(B, Hq, Hkv, D, max_q, max_kv, device_topology());
   return p.parts ? kWorkspaceHeader + p.blocks * kRows * (D + 2) * sizeof(float) : 0;
 }
 
 long long kv4_attention_blocks(int B, int Hq, int Hkv, int D, int max_q, int max_kv) {
+  if (use_tiles(B, Hq, Hkv, D, max_q, device_topology())) {
+    // (twice as many where a block has eight waves: the limit on blocks is one on threads)
+    const int rows = D == 256 ? kKv4TileRows<256> : kKv4TileRows<128>;
+    return tile_blocks(B, Hkv, row_tiles(max_q, Hq / Hkv, rows)) * (D == 256 ? 1 : 2);
+  }
   return kv4_plan(B, Hq, Hkv, D, max_q, max_kv, device_topology()).blocks;
 }
 
 hipError_t launch_kv4_attention(const AttentionArgs& a, int group_size, bool bf16, hipStream_t stream) {
+  if (use_tiles(a.B, a.Hq, a.Hkv, a.D, a.max_q, device_topology())) {
+    const Kv4TileArgs t = {a, bf16};
+    return a.D == 64 ? launch_kv4_tiles<64>(t, group_size, stream)
+           : a.D == 128 ? launch_kv4_tiles<128>(t, group_size, stream) : launch_kv4_tiles<256>(t, group_size, stream);
+  }
   if (a.D == 64) return group_size == 32 ? launch_split<64, 2>(a, bf16, stream) : launch_split<64, 1>(a, bf16, stream);
   if (a.D == 128)
     return group_size == 32 ? launch_split<128, 4>(a, bf16, stream)
