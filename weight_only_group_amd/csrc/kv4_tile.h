@@ -19,8 +19,20 @@ template <int D> constexpr int kKv4TileRows = 32 * kKv4TileWaves<D>;
 
 namespace {
 
+// (lambdas that hold registers by reference: left as calls they would put them to memory)
+#define QMM_INLINE __attribute__((always_inline))
+
 // How a score follows from its product: a factor; a small cap; a large cap or a distance bias too.
 enum ScoreKind { kPlainScore, kCappedScore, kAnyScore };
+
+// f of 0, 1, ... N - 1 as compile-time constants.
+template <int N, typename F>
+__device__ __forceinline__ void each(F f) {
+  if constexpr (N > 0) {
+    each<N - 1>(f);
+    f(std::integral_constant<int, N - 1>{});
+  }
+}
 
 struct Kv4TileKernelArgs {
   AttnKernelArgs r;
@@ -43,13 +55,13 @@ template <int D, int G, ScoreKind KIND>
 __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_tile_kernel(Kv4TileKernelArgs t) {
   constexpr int WAVES = kKv4TileWaves<D>, ROWS = kKv4TileRows<D>, GS = D / G, BLOCK = kv4_block_bytes(D, G);
   constexpr int BN = D == 256 ? 32 : 64, SUB = BN / 32, STEPS = D / 16, MT = D / 32, BLOCKS = BN / 8;
-  constexpr int QUADS = D / 4, UNITS = BLOCKS * QUADS;        // eight tokens of four channels
-  constexpr int HALF = 32 * WAVES, VU = (UNITS + HALF - 1) / HALF;  // threads of a half, units of one
-  static_assert(BN * 4 <= HALF, "a thread decodes a fourth of a key");
-  constexpr int K_BYTES = BN * D * 2, MID_BYTES = BN * 16, VM_BYTES = 8 * BN * 2, BUFFER = 2 * K_BYTES + MID_BYTES + VM_BYTES;
+  constexpr int THREADS = 64 * WAVES, KW = BN * D / 8 / THREADS;  // words of keys a thread decodes
+  constexpr int QUADS = D / 4, UNITS = 2 * BLOCKS * QUADS;       // of values: four tokens of four channels
+  constexpr int VU = (UNITS + THREADS - 1) / THREADS;            // of a thread
+  constexpr int K_BYTES = BN * D * 2, MID_BYTES = BN * 16, VM_BYTES = (G + 2) * BN * 2, BUFFER = 2 * K_BYTES + MID_BYTES + VM_BYTES;
   constexpr int LDO = 36, OUT_BYTES = ROWS * LDO * 4;
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * BUFFER > OUT_BYTES ? 2 * BUFFER : OUT_BYTES];
-  __shared__ int range[2][WAVES], s_bad;
+  __shared__ int range[4][WAVES], s_bad;
   const AttnKernelArgs& p = t.r;
   const AttentionArgs& a = p.a;
   const uint8_t* k_cache = reinterpret_cast<const uint8_t*>(a.k_cache);
@@ -80,14 +92,19 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
   hi = __builtin_amdgcn_readfirstlane(hi);
   all_lo = __builtin_amdgcn_readfirstlane(all_lo);
   all_hi = __builtin_amdgcn_readfirstlane(all_hi);
-  if (lane == 0) range[0][wave] = lo, range[1][wave] = hi;
+  if (lane == 0) range[0][wave] = lo, range[1][wave] = hi, range[2][wave] = all_lo, range[3][wave] = all_hi;
   if (tid == 0) s_bad = 0;
   __syncthreads();
-  int block_lo = INT32_MAX, block_hi = 0;
+  int block_lo = INT32_MAX, block_hi = 0, block_all_lo = 0, block_all_hi = INT32_MAX;
 #pragma unroll
-  for (int w = 0; w < WAVES; ++w) block_lo = min(block_lo, range[0][w]), block_hi = max(block_hi, range[1][w]);
+  for (int w = 0; w < WAVES; ++w) {
+    block_lo = min(block_lo, range[0][w]), block_hi = max(block_hi, range[1][w]);
+    block_all_lo = max(block_all_lo, range[2][w]), block_all_hi = min(block_all_hi, range[3][w]);
+  }
   block_lo = __builtin_amdgcn_readfirstlane(block_lo);
   block_hi = __builtin_amdgcn_readfirstlane(block_hi);
+  block_all_lo = __builtin_amdgcn_readfirstlane(block_all_lo);
+  block_all_hi = __builtin_amdgcn_readfirstlane(block_all_hi);
   const int t0 = block_lo < block_hi ? block_lo / BN : 0, t1 = block_lo < block_hi ? (block_hi - 1) / BN + 1 : 0;
 
   // The row's query, and its groups' sums in two parts (one a lane group).
@@ -119,112 +136,115 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
 
   // ---- decoding -----------------------------------------------------------------------
   const DecodeMasks masks;
-  const bool on_values = wave < WAVES / 2;
-  const int dt = tid & (HALF - 1);  // a thread's number within its half
   const int32_t* table = a.page_table + (long long)b * a.table_stride;
   // Number of the block of eight tokens, i in the step; past the seen keys' ends the nearest.
-  auto token_block = [&](int step, int i) -> uint32_t {
+  auto token_block = [&](int step, int i) QMM_INLINE -> uint32_t {
     const int j = (int)min(max((uint32_t)step * BN + 8 * i, (uint32_t)block_lo), (uint32_t)block_hi - 1);
     const int at = p.by_page(j);
     const int page = min(max(table[at], 0), a.pages - 1);
     return (((uint32_t)page * a.Hkv + hk) * a.page_size + (j - at * a.page_size)) / kBlockTokens;
   };
-  // Keys: thread 4 key + g has words (D / 32) g on of the key. Values: unit (block, quad), quads first.
-  constexpr int KW = D / 32;
-  const int key = dt >> 2, kquarter = dt & 3;
-  // What a thread has asked for: its key's words, then scales and middles; or per unit words, scales and middles.
-  constexpr int RAW = KW + G > 12 * VU ? KW + G : 12 * VU;
-  uint32_t raw[RAW], at_block[VU];  // at_block: of the next load
-  auto raw4 = [&](int i) { return u32x4{raw[4 * i], raw[4 * i + 1], raw[4 * i + 2], raw[4 * i + 3]}; };
-  auto find = [&](int step) {
-    if (on_values) {
+  // A thread's part of a step: KW neighbouring words of a key, and of the values units: words of four
+  // tokens (of a block's halves) of a quad of channels, with their scales and middles.
+  constexpr int PER_KEY = D / 8 / KW;  // threads of a key
+  const int key = tid / PER_KEY, word0 = tid % PER_KEY * KW;
+  auto unit_of = [&](int i) QMM_INLINE { return (tid + i * THREADS) % UNITS; };
+  // (of sixteen neighbouring pairs of threads eight quads of two blocks)
+  auto quad_of = [&](int i) QMM_INLINE { return (unit_of(i) >> 1 & 7) | unit_of(i) / (16 * BLOCKS) << 3; };
+  auto blk_of = [&](int i) QMM_INLINE { return (unit_of(i) >> 4) % BLOCKS; };
+  const bool no_values = UNITS < THREADS && tid >= UNITS;
+  uint32_t kw[KW], kp[G], vw[VU][2], vs[VU][2], vm[VU][2], k_block, v_block[VU];  // blocks: of the next load
+  auto find = [&](int step) QMM_INLINE {
+    k_block = token_block(step, key / 8);
 #pragma unroll
-      for (int i = 0; i < VU; ++i) at_block[i] = token_block(step, (dt + i * HALF) / QUADS % BLOCKS);
-    } else {
-      at_block[0] = token_block(step, key / 8 % BLOCKS);
+    for (int i = 0; i < VU; ++i) v_block[i] = token_block(step, blk_of(i));
+  };
+  auto load = [&]() QMM_INLINE {
+    const uint8_t* src = k_cache + (size_t)k_block * BLOCK;
+    load_words<4 * KW>(kw, src + (key & 7) * (D / 2) + word0 * 4);
+    load_words<4 * G>(kp, src + 4 * D + (key & 7) * 4 * G);
+#pragma unroll
+    for (int i = 0; i < VU; ++i) {
+      const int half = unit_of(i) & 1, quad = quad_of(i);
+      const uint8_t* from = v_cache + (size_t)v_block[i] * BLOCK + half * 8;
+      load_words<8>(vw[i], from + quad * 16);
+      load_words<8>(vs[i], from + 4 * D + quad * 4 / GS * 32);
+      load_words<8>(vm[i], from + 4 * D + quad * 4 / GS * 32 + 16);
     }
   };
-  auto load = [&]() {
-    if (on_values) {
-#pragma unroll
-      for (int i = 0; i < VU; ++i) {
-        const int quad = (dt + i * HALF) % QUADS;
-        const uint8_t* src = v_cache + (size_t)at_block[i] * BLOCK;
-        load_words<16>(raw + 12 * i, src + quad * 16);
-        load_words<32>(raw + 12 * i + 4, src + 4 * D + quad * 4 / GS * 32);
-      }
-    } else {
-      const uint8_t* src = k_cache + (size_t)at_block[0] * BLOCK + (key & 7) * (D / 2);
-      load_words<D / 8>(raw, src + kquarter * (D / 8));
-      load_words<4 * G>(raw + KW, k_cache + (size_t)at_block[0] * BLOCK + 4 * D + (key & 7) * 4 * G);
-    }
+  // Byte offsets in the buffer of piece (eight channels) `piece` of a key, and of block blk of a channel.
+  auto key_place = [](int k, int piece) {
+    const int turn = D == 64 ? (k >> 1 & 1) << 2 | (k >> 2 & 3) : (k & 3) << 2 | (k >> 2 & 3);
+    return k * (2 * D) + (piece ^ turn) * 16;
   };
-  auto key_turn = [](int k) { return (k >> 1 & 1) | (k >> 3 & 1) << 1 | (k & 1) << 2; };
-  auto channel_turn = [](int c) { return BN == 32 ? c >> 1 & 3 : ((c ^ c >> 3) & 3) | (c & 4); };
-  auto decode_step = [&](int step) {
-    uint8_t* buffer = lds + (step & 1) * BUFFER;
-    if (on_values) {
+  auto value_place = [](int c, int blk) {
+    if constexpr (BN == 32) return (c >> 2) * 256 + (((c & 3) ^ (c >> 4 & 1)) * 4 + (blk ^ (c >> 2 & 3))) * 16;
+    else return (c >> 1) * 256 + (((c ^ c >> 4) & 1) * 8 + (blk ^ (c >> 1 & 7))) * 16;
+  };
+  auto seen_by_whole_block = [&](int step) {
+    return step * BN >= block_all_lo && (uint32_t)(step + 1) * BN <= (uint32_t)block_all_hi;
+  };
+  // Before the decoding. Tokens that no row sees may hold anything: their scales and middles count as 0. So
+  // do those of a seen one that are not finite, as they must not reach the rows that do not see it (0 times NaN
+  // is NaN); those that do get a NaN at the end.
+  auto clean = [&](int step) QMM_INLINE {
+    if (seen_by_whole_block(step)) return;
+    uint32_t bad = 0;
 #pragma unroll
-      for (int i = 0; i < VU; ++i) {
-        const int u = dt + i * HALF, quad = u % QUADS, blk = u / QUADS;
-        if (UNITS % HALF && u >= UNITS) continue;
-        // Tokens that no row sees may hold anything: their scales and middles count as 0. So do those of a seen one
-        // that are not finite, as they must not reach the rows that do not see it (0 times NaN is NaN); those that
-        // do get a NaN at the end.
-        const int j0 = step * BN + 8 * blk;
-        const u32x4 words = raw4(3 * i);
-        u32x4 sv = raw4(3 * i + 1), mv = raw4(3 * i + 2);
-        uint32_t bad = 0;
+    for (int i = 0; i < VU; ++i) {
+      const int j0 = step * BN + 8 * blk_of(i) + 4 * (unit_of(i) & 1);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int j = j0 + 2 * x;
-          const uint32_t in = (j >= block_lo && j < block_hi ? 0xFFFFu : 0u) | (j + 1 >= block_lo && j + 1 < block_hi ? 0xFFFF0000u : 0u);
-          const uint32_t nf = (not_finite_halves(sv[x]) | not_finite_halves(mv[x])) & in;
-          bad |= nf;
-          sv[x] &= in & ~nf;
-          mv[x] &= in & ~nf;
-        }
-        if (bad) s_bad = 1;
-        f16x2 ss[4], c24[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          ss[x] = as_f16x2(sv[x]);
-          c24[x] = times_24(ss[x]);
-        }
-        uint8_t* to = buffer + K_BYTES;
-        auto channel = [&](auto r) {
-          constexpr int R = decltype(r)::value;
-          const int c = 4 * quad + R;
-          *reinterpret_cast<u32x4*>(to + c * (2 * BN) + ((blk ^ channel_turn(c)) * 16)) =
-              u32x4{decode<R>(words[0], ss[0], c24[0], masks), decode<R>(words[1], ss[1], c24[1], masks),
-                    decode<R>(words[2], ss[2], c24[2], masks), decode<R>(words[3], ss[3], c24[3], masks)};
-        };
-        channel(std::integral_constant<int, 0>{});
-        channel(std::integral_constant<int, 1>{});
-        channel(std::integral_constant<int, 2>{});
-        channel(std::integral_constant<int, 3>{});
-        if (quad * 4 % GS == 0) *reinterpret_cast<u32x4*>(buffer + 2 * K_BYTES + MID_BYTES + quad * 4 / GS * (2 * BN) + blk * 16) = mv;
+      for (int x = 0; x < 2; ++x) {
+        const int j = j0 + 2 * x;
+        const uint32_t in = (j >= block_lo && j < block_hi ? 0xFFFFu : 0u) | (j + 1 >= block_lo && j + 1 < block_hi ? 0xFFFF0000u : 0u);
+        const uint32_t nf = (not_finite_halves(vs[i][x]) | not_finite_halves(vm[i][x])) & in;
+        bad |= nf;
+        vs[i][x] &= in & ~nf;
+        vm[i][x] &= in & ~nf;
       }
-    } else if (BN * 4 == HALF || dt < BN * 4) {
+    }
+    if (bad) s_bad = 1;
+  };
+  // The middles (apart from the slices, which are to be without branches).
+  auto put_middles = [&](uint8_t* buffer) QMM_INLINE {
+    if (word0 == 0) {
+      u32x4 middles = {0, 0, 0, 0};
+      if constexpr (G == 1) {
+        middles[0] = kp[0] >> 16;
+      } else {
 #pragma unroll
-      for (int i = 0; i < KW; ++i) {
-        const int g = i * 32 / GS;
-        const f16 sg = as_f16x2(raw[KW + g / 2])[g % 2];
-        const f16x2 ss = {sg, sg}, c24 = times_24(ss);
-        *reinterpret_cast<u32x4*>(buffer + key * (2 * D) + (((4 * i + kquarter) ^ key_turn(key)) * 16)) =
-            u32x4{decode<0>(raw[i], ss, c24, masks), decode<1>(raw[i], ss, c24, masks), decode<2>(raw[i], ss, c24, masks),
-                  decode<3>(raw[i], ss, c24, masks)};
+        for (int x = 0; x < G / 2; ++x) middles[x] = kp[G / 2 + x];
       }
-      if (kquarter == 0) {
-        u32x4 middles = {0, 0, 0, 0};
-        if constexpr (G == 1) {
-          middles[0] = raw[KW] >> 16;
-        } else {
+      *reinterpret_cast<u32x4*>(buffer + 2 * K_BYTES + key * 16) = middles;
+    }
 #pragma unroll
-          for (int x = 0; x < G / 2; ++x) middles[x] = raw[KW + G / 2 + x];
-        }
-        *reinterpret_cast<u32x4*>(buffer + 2 * K_BYTES + key * 16) = middles;
+    for (int i = 0; i < VU; ++i)
+      if (quad_of(i) * 4 % GS == 0 && !no_values)
+        *reinterpret_cast<u32x2*>(buffer + 2 * K_BYTES + MID_BYTES + quad_of(i) * 4 / GS * (2 * BN) + blk_of(i) * 16 + (unit_of(i) & 1) * 8) =
+            u32x2{vm[i][0], vm[i][1]};
+  };
+  // The decoding in slices: the key's words, then four channels of each unit.
+  constexpr int SLICES = KW + 4 * VU;
+  auto decode_slice = [&](uint8_t* buffer, auto slice) QMM_INLINE {
+    constexpr int I = decltype(slice)::value;
+    if constexpr (I < KW) {
+      const int word = word0 + I, quarter = word / (D / 32), i = word % (D / 32), g = i * 32 / GS;
+      uint32_t pair = kp[0];
+      if constexpr (G > 2) {
+#pragma unroll
+        for (int x = 1; x < G / 2; ++x) pair = g / 2 == x ? kp[x] : pair;
       }
+      const f16 sg = G == 1 ? as_f16x2(pair)[0] : g % 2 ? as_f16x2(pair)[1] : as_f16x2(pair)[0];
+      const f16x2 s2 = {sg, sg}, c2 = times_24(s2);
+      *reinterpret_cast<u32x4*>(buffer + key_place(key, 4 * i + quarter)) =
+          u32x4{decode<0>(kw[I], s2, c2, masks), decode<1>(kw[I], s2, c2, masks), decode<2>(kw[I], s2, c2, masks), decode<3>(kw[I], s2, c2, masks)};
+    } else {
+      constexpr int U = (I - KW) / 4, R = (I - KW) % 4;
+      const int half = unit_of(U) & 1, quad = quad_of(U), blk = blk_of(U);
+      u32x2 v;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) v[x] = decode<R>(vw[U][x], as_f16x2(vs[U][x]), times_24(as_f16x2(vs[U][x])), masks);
+      if (UNITS >= THREADS || !no_values) *reinterpret_cast<u32x2*>(buffer + K_BYTES + value_place(4 * quad + R, blk) + half * 8) = v;
     }
   };
 
@@ -232,32 +252,43 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
   auto seen_by_none = [&](int key0) { return (uint32_t)key0 + BN <= (uint32_t)lo || key0 >= hi; };
   auto seen_by_all = [&](int key0) { return key0 >= all_lo && (uint32_t)key0 + BN <= (uint32_t)all_hi; };
   const int my_key = (n & 19) | (n & 4) << 1 | (n & 8) >> 1;  // of the 32 of row n: bits 2 and 3 change places
-  uint32_t k_at[STEPS], v_at[MT];
+  uint32_t k_at[STEPS];
 #pragma unroll
-  for (int s = 0; s < STEPS; ++s) k_at[s] = my_key * (2 * D) + (((2 * s + kg) ^ key_turn(my_key)) * 16);
+  for (int s = 0; s < STEPS; ++s) k_at[s] = key_place(my_key, 2 * s + kg);
+  const int v_at = value_place(n, 0);  // (block blk: an exclusive or with 16 blk; 32 channels on: the same place, 64 BN further)
+
+  // Rows of the values' middles: the groups', one of ones, one of zeros.
+  const int my_middles = (n < G ? n : n == 8 ? G : G + 1) * (2 * BN);
+  if (tid < 2 * BN) {
+    const int row = tid >= BN;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) v_at[m] = (32 * m + n) * (2 * BN);
-  const int my_turn = channel_turn(n);  // (the same for channels 32 apart)
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<uint16_t*>(lds + i * BUFFER + 2 * K_BYTES + MID_BYTES + (G + row) * (2 * BN) + tid % BN * 2) = row ? 0 : (uint16_t)kOnes;
+  }
 
   f32x16 o[MT] = {}, rest = {};  // rest: rows g < 8 the sums of p m_g, row 8 the sum of p
   float mx = -INFINITY;
+  // (of the steps asked for ahead those past the last are decoded too, to a buffer that is not read)
+  auto decode_step = [&](int step) QMM_INLINE {
+    clean(step);
+    put_middles(lds + (step & 1) * BUFFER);
+    each<SLICES>([&](auto i) QMM_INLINE { decode_slice(lds + (step & 1) * BUFFER, i); });
+    load();
+    find(step + 2);
+  };
   if (t0 < t1) {
     find(t0);
     load();
     find(t0 + 1);
     decode_step(t0);
-    load();
-    find(t0 + 2);
   }
   for (int step = t0; step < t1; ++step) {
     __syncthreads();  // the step's keys and values are there; those of the step before are done with
-    if (step + 1 < t1) {
-      decode_step(step + 1);
-      load();
-      find(step + 3);
-    }
     const int key0 = step * BN;
-    if (seen_by_none(key0)) continue;
+    // The next step's decoding goes between the matrix operations.
+    clean(step + 1);
+    uint8_t* next = lds + (~step & 1) * BUFFER;
+    put_middles(next);
     const uint8_t* ks = lds + (step & 1) * BUFFER;
     const uint8_t* vs8 = ks + K_BYTES;
     const uint8_t* mids = ks + 2 * K_BYTES;
@@ -266,7 +297,7 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
     constexpr int kAhead = 3;
     f32x16 st[SUB] = {};
     u32x4 kf[kAhead + 1][SUB];
-    auto read_keys = [&](int s) {
+    auto read_keys = [&](int s) QMM_INLINE {
 #pragma unroll
       for (int u = 0; u < SUB; ++u) kf[s % (kAhead + 1)][u] = *reinterpret_cast<const u32x4*>(ks + k_at[s] + u * 32 * D * 2);
     };
@@ -277,13 +308,19 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
     for (int s = 0; s < kAhead; ++s) read_keys(s);
 #pragma unroll
     for (int u = 0; u < SUB; ++u) st[u] = mfma32<false>(km[u], qsum, st[u]);
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
+    each<STEPS>([&](auto step_of) QMM_INLINE {
+      constexpr int s = decltype(step_of)::value;
       if (s + kAhead < STEPS) read_keys(s + kAhead);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int u = 0; u < SUB; ++u) st[u] = mfma32<false>(kf[s % (kAhead + 1)][u], q[s], st[u]);
-    }
+      constexpr int from = s * SLICES / STEPS, to = (s + 1) * SLICES / STEPS;
+      each<to - from>([&](auto i) QMM_INLINE { decode_slice(next, std::integral_constant<int, from + decltype(i)::value>{}); });
+    });
+    load();
+    find(step + 3);
+    // (asked here: a way of its own round the products makes the compiler spill hundreds of registers)
+    if (seen_by_none(key0)) continue;
     const bool whole = seen_by_all(key0);
     auto key_of = [&](int u, int i) { return key0 + 32 * u + 16 * (i >> 3) + 8 * kg + (i & 7); };
     // The largest score of the row; where a score is more than a multiply-add or a small cap of its
@@ -321,6 +358,7 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
       }
     }
     if (!whole) {
+      asm volatile("");  // (keeps the masks of whole steps from being computed along)
       seen = 0;
 #pragma unroll
       for (int u = 0; u < SUB; ++u)
@@ -381,6 +419,7 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
         for (int i = 0; i < 16; ++i) st[u][i] = fmaf(st[u][i], rule.scale, -off);
     }
     if (!whole) {
+      asm volatile("");
 #pragma unroll
       for (int u = 0; u < SUB; ++u)
 #pragma unroll
@@ -390,15 +429,13 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
     // exponentials and reads go between the matrix operations.
     constexpr int GROUPS = BN / 16;
     u32x4 vf[2][MT + 1], w[2];
-    auto read_values = [&](int g) {
+    auto read_values = [&](int g) QMM_INLINE {
       const int piece = 2 * g + kg;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) vf[g & 1][m] = *reinterpret_cast<const u32x4*>(vs8 + v_at[m] + ((piece ^ my_turn) * 16));
-      const u32x4 x = *reinterpret_cast<const u32x4*>(vmids + min(n, G - 1) * (2 * BN) + piece * 16);
-#pragma unroll
-      for (int y = 0; y < 4; ++y) vf[g & 1][MT][y] = n < G ? x[y] : n == 8 ? kOnes : 0u;
+      for (int m = 0; m < MT; ++m) vf[g & 1][m] = *reinterpret_cast<const u32x4*>(vs8 + (v_at ^ piece * 16) + m * (64 * BN));
+      vf[g & 1][MT] = *reinterpret_cast<const u32x4*>(vmids + my_middles + piece * 16);
     };
-    auto weigh = [&](int g) {
+    auto weigh = [&](int g) QMM_INLINE {
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int i = 8 * (g & 1) + 2 * x;
