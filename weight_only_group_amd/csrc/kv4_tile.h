@@ -22,8 +22,9 @@ namespace {
 // (lambdas that hold registers by reference: left as calls they would put them to memory)
 #define QMM_INLINE __attribute__((always_inline))
 
-// How a score follows from its product: a factor; a small cap; a large cap or a distance bias too.
-enum ScoreKind { kPlainScore, kCappedScore, kAnyScore };
+// How a score follows from its product: a factor; a small cap; a factor and a distance bias; any cap and a
+// bias. (Apart, as branches between them in a step make the compiler spill hundreds of registers.)
+enum ScoreKind { kPlainScore, kCappedScore, kBiasedScore, kAnyScore };
 
 // f of 0, 1, ... N - 1 as compile-time constants.
 template <int N, typename F>
@@ -58,9 +59,12 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
   constexpr int THREADS = 64 * WAVES, KW = BN * D / 8 / THREADS;  // words of keys a thread decodes
   constexpr int QUADS = D / 4, UNITS = 2 * BLOCKS * QUADS;       // of values: four tokens of four channels
   constexpr int VU = (UNITS + THREADS - 1) / THREADS;            // of a thread
-  constexpr int K_BYTES = BN * D * 2, MID_BYTES = BN * 16, VM_BYTES = (G + 2) * BN * 2, BUFFER = 2 * K_BYTES + MID_BYTES + VM_BYTES;
-  constexpr int LDO = 36, OUT_BYTES = ROWS * LDO * 4;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * BUFFER > OUT_BYTES ? 2 * BUFFER : OUT_BYTES];
+  // Two buffers of keys, each with its keys' middles; three of values, each with rows of middles: the groups', one of ones,
+  // one of zeros.
+  constexpr int TILE = BN * D * 2, K_BUFFER = TILE + BN * 16, VM_ROW = BN * 2, V_BUFFER = TILE + (G + 2) * VM_ROW;
+  constexpr int LDO = 36, OUT_BYTES = ROWS * LDO * 4, KV_BYTES = 2 * K_BUFFER + 3 * V_BUFFER;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[KV_BYTES > OUT_BYTES ? KV_BYTES : OUT_BYTES];
+  uint8_t* const v_lds = lds + 2 * K_BUFFER;
   __shared__ int range[4][WAVES], s_bad;
   const AttnKernelArgs& p = t.r;
   const AttentionArgs& a = p.a;
@@ -77,6 +81,7 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
   const int r0 = rt * ROWS + wave * 32;
   const Row row = row_of(p, r0 + n, span, hk);
   ScoreRule rule = score_rule(a, row.head);
+  if (KIND == kAnyScore) rule.scale = kLog2e * a.scale;  // (a small cap's has another factor)
 
   // Keys that any row of the wave sees, and those that all see; the block's from the waves'.
   int lo = row.lo < row.hi ? row.lo : INT32_MAX, hi = row.lo < row.hi ? row.hi : 0;
@@ -206,7 +211,7 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
     if (bad) s_bad = 1;
   };
   // The middles (apart from the slices, which are to be without branches).
-  auto put_middles = [&](uint8_t* buffer) QMM_INLINE {
+  auto put_middles = [&](uint8_t* k_to, uint8_t* v_to) QMM_INLINE {
     if (word0 == 0) {
       u32x4 middles = {0, 0, 0, 0};
       if constexpr (G == 1) {
@@ -215,17 +220,16 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
 #pragma unroll
         for (int x = 0; x < G / 2; ++x) middles[x] = kp[G / 2 + x];
       }
-      *reinterpret_cast<u32x4*>(buffer + 2 * K_BYTES + key * 16) = middles;
+      *reinterpret_cast<u32x4*>(k_to + TILE + key * 16) = middles;
     }
 #pragma unroll
     for (int i = 0; i < VU; ++i)
       if (quad_of(i) * 4 % GS == 0 && !no_values)
-        *reinterpret_cast<u32x2*>(buffer + 2 * K_BYTES + MID_BYTES + quad_of(i) * 4 / GS * (2 * BN) + blk_of(i) * 16 + (unit_of(i) & 1) * 8) =
-            u32x2{vm[i][0], vm[i][1]};
+        *reinterpret_cast<u32x2*>(v_to + TILE + quad_of(i) * 4 / GS * VM_ROW + blk_of(i) * 16 + (unit_of(i) & 1) * 8) = u32x2{vm[i][0], vm[i][1]};
   };
   // The decoding in slices: the key's words, then four channels of each unit.
   constexpr int SLICES = KW + 4 * VU;
-  auto decode_slice = [&](uint8_t* buffer, auto slice) QMM_INLINE {
+  auto decode_slice = [&](uint8_t* k_to, uint8_t* v_to, auto slice) QMM_INLINE {
     constexpr int I = decltype(slice)::value;
     if constexpr (I < KW) {
       const int word = word0 + I, quarter = word / (D / 32), i = word % (D / 32), g = i * 32 / GS;
@@ -236,7 +240,7 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
       }
       const f16 sg = G == 1 ? as_f16x2(pair)[0] : g % 2 ? as_f16x2(pair)[1] : as_f16x2(pair)[0];
       const f16x2 s2 = {sg, sg}, c2 = times_24(s2);
-      *reinterpret_cast<u32x4*>(buffer + key_place(key, 4 * i + quarter)) =
+      *reinterpret_cast<u32x4*>(k_to + key_place(key, 4 * i + quarter)) =
           u32x4{decode<0>(kw[I], s2, c2, masks), decode<1>(kw[I], s2, c2, masks), decode<2>(kw[I], s2, c2, masks), decode<3>(kw[I], s2, c2, masks)};
     } else {
       constexpr int U = (I - KW) / 4, R = (I - KW) % 4;
@@ -244,12 +248,11 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
       u32x2 v;
 #pragma unroll
       for (int x = 0; x < 2; ++x) v[x] = decode<R>(vw[U][x], as_f16x2(vs[U][x]), times_24(as_f16x2(vs[U][x])), masks);
-      if (UNITS >= THREADS || !no_values) *reinterpret_cast<u32x2*>(buffer + K_BYTES + value_place(4 * quad + R, blk) + half * 8) = v;
+      if (UNITS >= THREADS || !no_values) *reinterpret_cast<u32x2*>(v_to + value_place(4 * quad + R, blk) + half * 8) = v;
     }
   };
 
   // ---- products -------------------------------------------------------------------------
-  auto seen_by_none = [&](int key0) { return (uint32_t)key0 + BN <= (uint32_t)lo || key0 >= hi; };
   auto seen_by_all = [&](int key0) { return key0 >= all_lo && (uint32_t)key0 + BN <= (uint32_t)all_hi; };
   const int my_key = (n & 19) | (n & 4) << 1 | (n & 8) >> 1;  // of the 32 of row n: bits 2 and 3 change places
   uint32_t k_at[STEPS];
@@ -257,105 +260,115 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
   for (int s = 0; s < STEPS; ++s) k_at[s] = key_place(my_key, 2 * s + kg);
   const int v_at = value_place(n, 0);  // (block blk: an exclusive or with 16 blk; 32 channels on: the same place, 64 BN further)
 
-  // Rows of the values' middles: the groups', one of ones, one of zeros.
-  const int my_middles = (n < G ? n : n == 8 ? G : G + 1) * (2 * BN);
-  if (tid < 2 * BN) {
-    const int row = tid >= BN;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<uint16_t*>(lds + i * BUFFER + 2 * K_BYTES + MID_BYTES + (G + row) * (2 * BN) + tid % BN * 2) = row ? 0 : (uint16_t)kOnes;
+  const int my_middles = TILE + (n < G ? n : n == 8 ? G : G + 1) * VM_ROW;
+  for (int i = tid; i < 3 * V_BUFFER / 16; i += THREADS) {  // the rows of ones and zeros; values of 0 in all, for the weights of 0 ahead of the first step
+    const int at = i * 16 % V_BUFFER - TILE - G * VM_ROW;
+    const uint32_t x = at >= 0 && at < VM_ROW ? kOnes : 0u;
+    reinterpret_cast<u32x4*>(v_lds)[i] = u32x4{x, x, x, x};
   }
+  __syncthreads();
 
   f32x16 o[MT] = {}, rest = {};  // rest: rows g < 8 the sums of p m_g, row 8 the sum of p
   float mx = -INFINITY;
-  // (of the steps asked for ahead those past the last are decoded too, to a buffer that is not read)
-  auto decode_step = [&](int step) QMM_INLINE {
-    clean(step);
-    put_middles(lds + (step & 1) * BUFFER);
-    each<SLICES>([&](auto i) QMM_INLINE { decode_slice(lds + (step & 1) * BUFFER, i); });
-    load();
-    find(step + 2);
+  u32x4 w[BN / 16] = {};  // the weights of the step before, sixteen keys a piece
+  constexpr int GROUPS = BN / 16;
+  // The step before's weights times its values; between them `between(i)`, i < GROUPS.
+  auto add_values = [&](const uint8_t* from, auto between) QMM_INLINE {
+    u32x4 vf[2][MT + 1];
+    auto read_values = [&](int g) QMM_INLINE {
+      const int piece = 2 * g + kg;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) vf[g & 1][m] = *reinterpret_cast<const u32x4*>(from + (v_at ^ piece * 16) + m * (64 * BN));
+      vf[g & 1][MT] = *reinterpret_cast<const u32x4*>(from + my_middles + piece * 16);
+    };
+    read_values(0);
+    each<GROUPS>([&](auto group) QMM_INLINE {
+      constexpr int g = decltype(group)::value;
+      if constexpr (g + 1 < GROUPS) read_values(g + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) o[m] = mfma32<false>(vf[g & 1][m], w[g], o[m]);
+      rest = mfma32<false>(vf[g & 1][MT], w[g], rest);
+      between(group);
+    });
   };
+  // Everything that a wave has put to LDS is there, for all. (A fence would wait for the loads asked for ahead too.)
+  auto meet = [&]() QMM_INLINE {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  // Two waves share a SIMD: while one takes its matrix operations (the step before's values, the
+  // step's keys), the other takes its softmax. The second half of the waves is a phase behind.
+  const bool behind = WAVES == 8 && wave >= 4;
   if (t0 < t1) {
     find(t0);
     load();
     find(t0 + 1);
-    decode_step(t0);
+    clean(t0);
+    put_middles(lds + (t0 & 1) * K_BUFFER, v_lds + V_BUFFER);
+    each<SLICES>([&](auto i) QMM_INLINE { decode_slice(lds + (t0 & 1) * K_BUFFER, v_lds + V_BUFFER, i); });
+    load();
+    find(t0 + 2);
+    meet();
+    if (behind) meet();
   }
+  int v_last = 0, v_next = 2;  // buffers of the values of the step before and of the one after (the step's own is the third)
   for (int step = t0; step < t1; ++step) {
-    __syncthreads();  // the step's keys and values are there; those of the step before are done with
     const int key0 = step * BN;
-    // The next step's decoding goes between the matrix operations.
+    const uint8_t* ks = lds + (step & 1) * K_BUFFER;
+    // The next step's decoding goes between the matrix operations. (of the steps asked for ahead those past the last are
+    // decoded too, to buffers that are not read)
+    uint8_t* const k_to = lds + (~step & 1) * K_BUFFER;
+    uint8_t* const v_to = v_lds + v_next * V_BUFFER;
     clean(step + 1);
-    uint8_t* next = lds + (~step & 1) * BUFFER;
-    put_middles(next);
-    const uint8_t* ks = lds + (step & 1) * BUFFER;
-    const uint8_t* vs8 = ks + K_BYTES;
-    const uint8_t* mids = ks + 2 * K_BYTES;
-    const uint8_t* vmids = mids + MID_BYTES;
+    put_middles(k_to, v_to);
+    auto slices = [&](auto i, auto all) QMM_INLINE {  // those of place i of all
+      constexpr int from = decltype(i)::value * SLICES / decltype(all)::value, to = (decltype(i)::value + 1) * SLICES / decltype(all)::value;
+      each<to - from>([&](auto x) QMM_INLINE { decode_slice(k_to, v_to, std::integral_constant<int, from + decltype(x)::value>{}); });
+    };
+    constexpr int PLACES = GROUPS + STEPS;
+    add_values(v_lds + v_last * V_BUFFER, [&](auto i) QMM_INLINE { slices(i, std::integral_constant<int, PLACES>{}); });
     // Products of keys and queries, the keys' pieces read kAhead steps before.
     constexpr int kAhead = 3;
     f32x16 st[SUB] = {};
-    u32x4 kf[kAhead + 1][SUB];
+    u32x4 kf[kAhead + 1][SUB], km[SUB];
     auto read_keys = [&](int s) QMM_INLINE {
 #pragma unroll
       for (int u = 0; u < SUB; ++u) kf[s % (kAhead + 1)][u] = *reinterpret_cast<const u32x4*>(ks + k_at[s] + u * 32 * D * 2);
     };
-    u32x4 km[SUB];
 #pragma unroll
-    for (int u = 0; u < SUB; ++u) km[u] = *reinterpret_cast<const u32x4*>(mids + (32 * u + my_key) * 16);
+    for (int u = 0; u < SUB; ++u) km[u] = *reinterpret_cast<const u32x4*>(ks + TILE + (32 * u + my_key) * 16);
 #pragma unroll
     for (int s = 0; s < kAhead; ++s) read_keys(s);
 #pragma unroll
     for (int u = 0; u < SUB; ++u) st[u] = mfma32<false>(km[u], qsum, st[u]);
     each<STEPS>([&](auto step_of) QMM_INLINE {
       constexpr int s = decltype(step_of)::value;
-      if (s + kAhead < STEPS) read_keys(s + kAhead);
+      if constexpr (s + kAhead < STEPS) read_keys(s + kAhead);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int u = 0; u < SUB; ++u) st[u] = mfma32<false>(kf[s % (kAhead + 1)][u], q[s], st[u]);
-      constexpr int from = s * SLICES / STEPS, to = (s + 1) * SLICES / STEPS;
-      each<to - from>([&](auto i) QMM_INLINE { decode_slice(next, std::integral_constant<int, from + decltype(i)::value>{}); });
+      slices(std::integral_constant<int, GROUPS + s>{}, std::integral_constant<int, PLACES>{});
     });
     load();
     find(step + 3);
-    // (asked here: a way of its own round the products makes the compiler spill hundreds of registers)
-    if (seen_by_none(key0)) continue;
+    meet();
+    // The softmax (with weights of 0 where the wave's rows see none of the step's keys).
     const bool whole = seen_by_all(key0);
     auto key_of = [&](int u, int i) { return key0 + 32 * u + 16 * (i >> 3) + 8 * kg + (i & 7); };
     // The largest score of the row; where a score is more than a multiply-add or a small cap of its
     // product the scores are taken first, else only that of the largest product.
     float best = -INFINITY;
     uint32_t seen = ~0u;  // bit 16 u + i: the row sees key_of(u, i)
-    if (KIND == kAnyScore) {
-      const bool slopes = a.slopes != nullptr;
-      const Cap cap = cap_kind(a.softcap);
-      if (cap == kSmallCap) {
+    if (KIND >= kBiasedScore) {
 #pragma unroll
-        for (int u = 0; u < SUB; ++u)
+      for (int u = 0; u < SUB; ++u)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            st[u][i] = rule.template score<kSmallCap, false>(st[u][i], 0, 0);
-            if (i % 8 == 7) __builtin_amdgcn_sched_barrier(0);
-          }
-      } else if (cap == kAnyCap) {
-#pragma unroll
-        for (int u = 0; u < SUB; ++u)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            st[u][i] = rule.template score<kAnyCap, false>(st[u][i], 0, 0);
-            if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // (or the registers do not suffice)
-          }
-      } else {
-#pragma unroll
-        for (int u = 0; u < SUB; ++u) st[u] *= rule.scale;
-      }
-      if (slopes) {
-#pragma unroll
-        for (int u = 0; u < SUB; ++u)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) st[u][i] -= rule.slope * fabsf((float)(row.pos - key_of(u, i)));
-      }
+        for (int i = 0; i < 16; ++i) {
+          st[u][i] = rule.template score<KIND == kAnyScore ? kAnyCap : kNoCap, true>(st[u][i], row.pos, key_of(u, i));
+          if (KIND == kAnyScore && i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // (or the registers do not suffice)
+        }
     }
     if (!whole) {
       asm volatile("");  // (keeps the masks of whole steps from being computed along)
@@ -388,7 +401,7 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
     const float off = mx == -INFINITY ? 0.f : mx - kLift;
     // Exponents: the scores less the maximum, in one multiply-add of the product (or, with a cap, of
     // the reciprocal in the tanh).
-    if (KIND == kAnyScore) {
+    if (KIND >= kBiasedScore) {
 #pragma unroll
       for (int u = 0; u < SUB; ++u) st[u] -= off;
     } else if (KIND == kCappedScore) {
@@ -425,45 +438,20 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
 #pragma unroll
         for (int i = 0; i < 16; ++i) st[u][i] = seen >> (16 * u + i) & 1 ? st[u][i] : -INFINITY;
     }
-    // Weights and their products with the values, sixteen keys at a time: the next ones'
-    // exponentials and reads go between the matrix operations.
-    constexpr int GROUPS = BN / 16;
-    u32x4 vf[2][MT + 1], w[2];
-    auto read_values = [&](int g) QMM_INLINE {
-      const int piece = 2 * g + kg;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) vf[g & 1][m] = *reinterpret_cast<const u32x4*>(vs8 + (v_at ^ piece * 16) + m * (64 * BN));
-      vf[g & 1][MT] = *reinterpret_cast<const u32x4*>(vmids + my_middles + piece * 16);
-    };
-    auto weigh = [&](int g) QMM_INLINE {
+    for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int i = 8 * (g & 1) + 2 * x;
-        w[g & 1][x] = pack_pair<false>(__builtin_amdgcn_exp2f(st[g >> 1][i]), __builtin_amdgcn_exp2f(st[g >> 1][i + 1]));
+        w[g][x] = pack_pair<false>(__builtin_amdgcn_exp2f(st[g >> 1][i]), __builtin_amdgcn_exp2f(st[g >> 1][i + 1]));
       }
-    };
-    read_values(0);
-    weigh(0);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int g = 0; g < GROUPS; ++g) {
-      if (g + 1 < GROUPS) {
-        read_values(g + 1);
-        weigh(g + 1);
-      }
-#pragma unroll
-      for (int m = 0; m < MT; ++m) o[m] = mfma32<false>(vf[g & 1][m], w[g & 1], o[m]);
-      rest = mfma32<false>(vf[g & 1][MT], w[g & 1], rest);
-      if (g + 1 < GROUPS) {
-        __builtin_amdgcn_sched_group_barrier(0x100, MT + 1, 0);  // LDS reads
-#pragma unroll
-        for (int m = 0; m < MT + 1; ++m) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);               // a matrix operation
-          __builtin_amdgcn_sched_group_barrier(0x402, (16 + MT) / (MT + 1), 0);  // vector operations
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    v_last = v_last == 2 ? 0 : v_last + 1;
+    v_next = v_next == 2 ? 0 : v_next + 1;
+    meet();
+  }
+  if (t0 < t1) {
+    if (WAVES == 8 && !behind) meet();
+    add_values(v_lds + v_last * V_BUFFER, [](auto) {});
   }
 
   // Results leave by LDS, 32 dimensions at a time, each wave for its own rows.
@@ -523,7 +511,8 @@ hipError_t launch_tiles_of(const Kv4TileArgs& t, hipStream_t stream) {
   const dim3 grid((unsigned)tile_blocks(a.B, a.Hkv, rtiles));
   const auto run = [&](auto kernel) { kernel<<<grid, 64 * kKv4TileWaves<D>, 0, stream>>>(p); };
   const Cap cap = cap_kind(a.softcap);
-  if (a.slopes || cap == kAnyCap) run(kv4_tile_kernel<D, G, kAnyScore>);
+  if (cap == kAnyCap || (a.slopes && cap == kSmallCap)) run(kv4_tile_kernel<D, G, kAnyScore>);
+  else if (a.slopes) run(kv4_tile_kernel<D, G, kBiasedScore>);
   else if (cap == kSmallCap) run(kv4_tile_kernel<D, G, kCappedScore>);
   else run(kv4_tile_kernel<D, G, kPlainScore>);
   return hipGetLastError();
