@@ -61,10 +61,10 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
   constexpr int VU = (UNITS + THREADS - 1) / THREADS;            // of a thread
   // Two buffers of keys, each with its keys' middles; three of values, each with rows of middles: the groups', one of ones,
   // one of zeros.
-  constexpr int TILE = BN * D * 2, K_BUFFER = TILE + BN * 16, VM_ROW = BN * 2, V_BUFFER = TILE + (G + 2) * VM_ROW;
+  constexpr int TILE = BN * D * 2, K_BUFFER = TILE + BN * 16, VM_ROW = BN * 2, V_BUFFER = TILE + ((G + 2) * VM_ROW + 511) / 512 * 512;
   constexpr int LDO = 36, OUT_BYTES = ROWS * LDO * 4, KV_BYTES = 2 * K_BUFFER + 3 * V_BUFFER;
   __shared__ __attribute__((aligned(16))) uint8_t lds[KV_BYTES > OUT_BYTES ? KV_BYTES : OUT_BYTES];
-  uint8_t* const v_lds = lds + 2 * K_BUFFER;
+  constexpr int V_LDS = 2 * K_BUFFER;  // place of the first of them
   __shared__ int range[4][WAVES], s_bad;
   const AttnKernelArgs& p = t.r;
   const AttentionArgs& a = p.a;
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
     if (bad) s_bad = 1;
   };
   // The middles (apart from the slices, which are to be without branches).
-  auto put_middles = [&](uint8_t* k_to, uint8_t* v_to) QMM_INLINE {
+  auto put_middles = [&](int k_to, int v_to) QMM_INLINE {
     if (word0 == 0) {
       u32x4 middles = {0, 0, 0, 0};
       if constexpr (G == 1) {
@@ -220,19 +220,23 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
 #pragma unroll
         for (int x = 0; x < G / 2; ++x) middles[x] = kp[G / 2 + x];
       }
-      *reinterpret_cast<u32x4*>(k_to + TILE + key * 16) = middles;
+      *reinterpret_cast<u32x4*>(lds + k_to + TILE + key * 16) = middles;
     }
 #pragma unroll
     for (int i = 0; i < VU; ++i)
       if (quad_of(i) * 4 % GS == 0 && !no_values)
-        *reinterpret_cast<u32x2*>(v_to + TILE + quad_of(i) * 4 / GS * VM_ROW + blk_of(i) * 16 + (unit_of(i) & 1) * 8) = u32x2{vm[i][0], vm[i][1]};
+        *reinterpret_cast<u32x2*>(lds + v_to + TILE + quad_of(i) * 4 / GS * VM_ROW + blk_of(i) * 16 + (unit_of(i) & 1) * 8) = u32x2{vm[i][0], vm[i][1]};
   };
   // The decoding in slices: the key's words, then four channels of each unit.
   constexpr int SLICES = KW + 4 * VU;
-  auto decode_slice = [&](uint8_t* k_to, uint8_t* v_to, auto slice) QMM_INLINE {
+  const int key_at = key_place(key, 4 * (word0 % (D / 32)) + word0 / (D / 32));
+  int unit_at[VU];
+#pragma unroll
+  for (int i = 0; i < VU; ++i) unit_at[i] = value_place(4 * quad_of(i), blk_of(i)) + (unit_of(i) & 1) * 8;
+  auto decode_slice = [&](int k_to, int v_to, auto slice) QMM_INLINE {
     constexpr int I = decltype(slice)::value;
     if constexpr (I < KW) {
-      const int word = word0 + I, quarter = word / (D / 32), i = word % (D / 32), g = i * 32 / GS;
+      const int g = (word0 + I) % (D / 32) * 32 / GS;
       uint32_t pair = kp[0];
       if constexpr (G > 2) {
 #pragma unroll
@@ -240,57 +244,70 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
       }
       const f16 sg = G == 1 ? as_f16x2(pair)[0] : g % 2 ? as_f16x2(pair)[1] : as_f16x2(pair)[0];
       const f16x2 s2 = {sg, sg}, c2 = times_24(s2);
-      *reinterpret_cast<u32x4*>(k_to + key_place(key, 4 * i + quarter)) =
+      // (the places of a thread's pieces differ in bits that the buffers' places leave 0)
+      *reinterpret_cast<u32x4*>(lds + ((k_to + key_at) ^ I * 64)) =
           u32x4{decode<0>(kw[I], s2, c2, masks), decode<1>(kw[I], s2, c2, masks), decode<2>(kw[I], s2, c2, masks), decode<3>(kw[I], s2, c2, masks)};
     } else {
       constexpr int U = (I - KW) / 4, R = (I - KW) % 4;
-      const int half = unit_of(U) & 1, quad = quad_of(U), blk = blk_of(U);
       u32x2 v;
 #pragma unroll
       for (int x = 0; x < 2; ++x) v[x] = decode<R>(vw[U][x], as_f16x2(vs[U][x]), times_24(as_f16x2(vs[U][x])), masks);
-      if (UNITS >= THREADS || !no_values) *reinterpret_cast<u32x2*>(v_to + value_place(4 * quad + R, blk) + half * 8) = v;
+      constexpr int there = BN == 32 ? R * 64 : (R & 1) * 128 | (R >> 1) * (256 | 16);
+      if (UNITS >= THREADS || !no_values) *reinterpret_cast<u32x2*>(lds + ((v_to + unit_at[U]) ^ there)) = v;
     }
   };
 
   // ---- products -------------------------------------------------------------------------
   auto seen_by_all = [&](int key0) { return key0 >= all_lo && (uint32_t)key0 + BN <= (uint32_t)all_hi; };
   const int my_key = (n & 19) | (n & 4) << 1 | (n & 8) >> 1;  // of the 32 of row n: bits 2 and 3 change places
-  uint32_t k_at[STEPS];
-#pragma unroll
-  for (int s = 0; s < STEPS; ++s) k_at[s] = key_place(my_key, 2 * s + kg);
-  const int v_at = value_place(n, 0);  // (block blk: an exclusive or with 16 blk; 32 channels on: the same place, 64 BN further)
+  const int k_at = key_place(my_key, kg);  // (two pieces on: an exclusive or with 32)
+  const int v_at = value_place(n, kg);  // (two blocks on: an exclusive or with 32; 32 channels on: the same place, 64 BN further)
 
-  const int my_middles = TILE + (n < G ? n : n == 8 ? G : G + 1) * VM_ROW;
+  const int my_middles = TILE + (n < G ? n : n == 8 ? G : G + 1) * VM_ROW + kg * 16;
   for (int i = tid; i < 3 * V_BUFFER / 16; i += THREADS) {  // the rows of ones and zeros; values of 0 in all, for the weights of 0 ahead of the first step
     const int at = i * 16 % V_BUFFER - TILE - G * VM_ROW;
     const uint32_t x = at >= 0 && at < VM_ROW ? kOnes : 0u;
-    reinterpret_cast<u32x4*>(v_lds)[i] = u32x4{x, x, x, x};
+    reinterpret_cast<u32x4*>(lds + V_LDS)[i] = u32x4{x, x, x, x};
   }
   __syncthreads();
 
   f32x16 o[MT] = {}, rest = {};  // rest: rows g < 8 the sums of p m_g, row 8 the sum of p
   float mx = -INFINITY;
   u32x4 w[BN / 16] = {};  // the weights of the step before, sixteen keys a piece
-  constexpr int GROUPS = BN / 16;
-  // The step before's weights times its values; between them `between(i)`, i < GROUPS.
-  auto add_values = [&](const uint8_t* from, auto between) QMM_INLINE {
-    u32x4 vf[2][MT + 1];
-    auto read_values = [&](int g) QMM_INLINE {
-      const int piece = 2 * g + kg;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) vf[g & 1][m] = *reinterpret_cast<const u32x4*>(from + (v_at ^ piece * 16) + m * (64 * BN));
-      vf[g & 1][MT] = *reinterpret_cast<const u32x4*>(from + my_middles + piece * 16);
-    };
-    read_values(0);
-    each<GROUPS>([&](auto group) QMM_INLINE {
-      constexpr int g = decltype(group)::value;
-      if constexpr (g + 1 < GROUPS) read_values(g + 1);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) o[m] = mfma32<false>(vf[g & 1][m], w[g], o[m]);
-      rest = mfma32<false>(vf[g & 1][MT], w[g], rest);
-      between(group);
-    });
+  // A step's matrix operations: the step before's weights times its values, sixteen keys (MT products and one for the
+  // middles) after another; then the step's keys, their middles first, times the queries. Their left operands come from LDS
+  // AHEAD operations before. (A prompt of 8192, 32 heads of 128 over 8: with 3 859 us, with 5 762 us, with 7 784 and with 9
+  // 779: there is no room for their registers.)
+  constexpr int GROUPS = BN / 16, VALUE_OPS = GROUPS * (MT + 1), OPS = VALUE_OPS + SUB * (STEPS + 1), AHEAD = 5;
+  f32x16 st[SUB];
+  u32x4 operand[AHEAD + 1];
+  auto read = [&](int vb, int kb, auto op) QMM_INLINE {
+    constexpr int I = decltype(op)::value;
+    int from;
+    if constexpr (I < VALUE_OPS) {
+      constexpr int g = I / (MT + 1), m = I % (MT + 1);
+      from = m < MT ? ((vb + v_at) ^ g * 32) + m * (64 * BN) : vb + my_middles + g * 32;
+    } else if constexpr (I < VALUE_OPS + SUB) {
+      from = kb + TILE + (32 * (I - VALUE_OPS) + my_key) * 16;
+    } else {
+      constexpr int s = (I - VALUE_OPS - SUB) / SUB, u = (I - VALUE_OPS - SUB) % SUB;
+      from = ((kb + k_at) ^ s * 32) + u * (64 * D);
+    }
+    operand[I % (AHEAD + 1)] = *reinterpret_cast<const u32x4*>(lds + from);
+  };
+  auto multiply = [&](auto op) QMM_INLINE {
+    constexpr int I = decltype(op)::value;
+    const u32x4 x = operand[I % (AHEAD + 1)];
+    if constexpr (I < VALUE_OPS) {
+      constexpr int g = I / (MT + 1), m = I % (MT + 1);
+      if constexpr (m < MT) o[m] = mfma32<false>(x, w[g], o[m]);
+      else rest = mfma32<false>(x, w[g], rest);
+    } else if constexpr (I < VALUE_OPS + SUB) {
+      st[I - VALUE_OPS] = mfma32<false>(x, qsum, f32x16{});
+    } else {
+      constexpr int s = (I - VALUE_OPS - SUB) / SUB, u = (I - VALUE_OPS - SUB) % SUB;
+      st[u] = mfma32<false>(x, q[s], st[u]);
+    }
   };
   // Everything that a wave has put to LDS is there, for all. (A fence would wait for the loads asked for ahead too.)
   auto meet = [&]() QMM_INLINE {
@@ -306,8 +323,8 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
     load();
     find(t0 + 1);
     clean(t0);
-    put_middles(lds + (t0 & 1) * K_BUFFER, v_lds + V_BUFFER);
-    each<SLICES>([&](auto i) QMM_INLINE { decode_slice(lds + (t0 & 1) * K_BUFFER, v_lds + V_BUFFER, i); });
+    put_middles((t0 & 1) * K_BUFFER, V_LDS + V_BUFFER);
+    each<SLICES>([&](auto i) QMM_INLINE { decode_slice((t0 & 1) * K_BUFFER, V_LDS + V_BUFFER, i); });
     load();
     find(t0 + 2);
     meet();
@@ -316,40 +333,23 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
   int v_last = 0, v_next = 2;  // buffers of the values of the step before and of the one after (the step's own is the third)
   for (int step = t0; step < t1; ++step) {
     const int key0 = step * BN;
-    const uint8_t* ks = lds + (step & 1) * K_BUFFER;
+    const int ks = (step & 1) * K_BUFFER, vb = V_LDS + v_last * V_BUFFER;
     // The next step's decoding goes between the matrix operations. (of the steps asked for ahead those past the last are
     // decoded too, to buffers that are not read)
-    uint8_t* const k_to = lds + (~step & 1) * K_BUFFER;
-    uint8_t* const v_to = v_lds + v_next * V_BUFFER;
+    const int k_to = (~step & 1) * K_BUFFER, v_to = V_LDS + v_next * V_BUFFER;
+    each<AHEAD>([&](auto op) QMM_INLINE { read(vb, ks, op); });
     clean(step + 1);
     put_middles(k_to, v_to);
     auto slices = [&](auto i, auto all) QMM_INLINE {  // those of place i of all
       constexpr int from = decltype(i)::value * SLICES / decltype(all)::value, to = (decltype(i)::value + 1) * SLICES / decltype(all)::value;
       each<to - from>([&](auto x) QMM_INLINE { decode_slice(k_to, v_to, std::integral_constant<int, from + decltype(x)::value>{}); });
     };
-    constexpr int PLACES = GROUPS + STEPS;
-    add_values(v_lds + v_last * V_BUFFER, [&](auto i) QMM_INLINE { slices(i, std::integral_constant<int, PLACES>{}); });
-    // Products of keys and queries, the keys' pieces read kAhead steps before.
-    constexpr int kAhead = 3;
-    f32x16 st[SUB] = {};
-    u32x4 kf[kAhead + 1][SUB], km[SUB];
-    auto read_keys = [&](int s) QMM_INLINE {
-#pragma unroll
-      for (int u = 0; u < SUB; ++u) kf[s % (kAhead + 1)][u] = *reinterpret_cast<const u32x4*>(ks + k_at[s] + u * 32 * D * 2);
-    };
-#pragma unroll
-    for (int u = 0; u < SUB; ++u) km[u] = *reinterpret_cast<const u32x4*>(ks + TILE + (32 * u + my_key) * 16);
-#pragma unroll
-    for (int s = 0; s < kAhead; ++s) read_keys(s);
-#pragma unroll
-    for (int u = 0; u < SUB; ++u) st[u] = mfma32<false>(km[u], qsum, st[u]);
-    each<STEPS>([&](auto step_of) QMM_INLINE {
-      constexpr int s = decltype(step_of)::value;
-      if constexpr (s + kAhead < STEPS) read_keys(s + kAhead);
+    each<OPS>([&](auto op) QMM_INLINE {
+      constexpr int I = decltype(op)::value;
+      if constexpr (I + AHEAD < OPS) read(vb, ks, std::integral_constant<int, I + AHEAD>{});
       __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int u = 0; u < SUB; ++u) st[u] = mfma32<false>(kf[s % (kAhead + 1)][u], q[s], st[u]);
-      slices(std::integral_constant<int, GROUPS + s>{}, std::integral_constant<int, PLACES>{});
+      multiply(op);
+      slices(op, std::integral_constant<int, OPS>{});
     });
     load();
     find(step + 3);
@@ -451,7 +451,13 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
   }
   if (t0 < t1) {
     if (WAVES == 8 && !behind) meet();
-    add_values(v_lds + v_last * V_BUFFER, [](auto) {});
+    const int vb = V_LDS + v_last * V_BUFFER;
+    each<AHEAD>([&](auto op) QMM_INLINE { read(vb, 0, op); });
+    each<VALUE_OPS>([&](auto op) QMM_INLINE {
+      constexpr int I = decltype(op)::value;
+      if constexpr (I + AHEAD < VALUE_OPS) read(vb, 0, std::integral_constant<int, I + AHEAD>{});
+      multiply(op);
+    });
   }
 
   // Results leave by LDS, 32 dimensions at a time, each wave for its own rows.
