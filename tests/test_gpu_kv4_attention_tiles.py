@@ -16,7 +16,7 @@ KINDS = [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128), (256, 32), (256, 
 
 
 def in_blocks(w, B, T, Hq, Hkv, D, max_q, max_kv):  # noqa: F811
-    """Such a call needs no workspace: its keys are not split."""
+    """Such a call needs no workspace, whatever its masks: its keys are not split."""
     return w.library().qmm_kv4_attention_workspace_bytes(B, T, Hq, Hkv, D, max_q, max_kv) == 0
 
 
@@ -29,7 +29,7 @@ def tiles(w, kv_lens, q_lens, Hq, Hkv, D, *args, **kw):  # noqa: F811
 @pytest.mark.parametrize("D,group", KINDS)
 def test_prompts(w, D, group, dtype):  # noqa: F811
     """Ragged sequences, some of a token, rows that end inside a block."""
-    tiles(w, [139, 1, 66, 133], [139, 1, 65, 70], 32, 16, D, 24, group, dtype)
+    tiles(w, [139, 1, 66, 133], [139, 1, 65, 70], 128, 64, D, 24, group, dtype)
 
 
 @pytest.mark.parametrize("D,group", [(64, 32), (128, 64), (256, 32)])
@@ -37,8 +37,8 @@ def test_prompts(w, D, group, dtype):  # noqa: F811
 def test_cap_and_distance(w, D, group, softcap, slopes):  # noqa: F811
     kw = {"softcap": softcap}
     if slopes:
-        kw["slopes"] = 2.0 ** -np.arange(1, 65) ** 0.5
-    tiles(w, [101, 40], [101, 35], 64, 32, D, 16, group, "fp16", q_scale=4.0, **kw)
+        kw["slopes"] = 2.0 ** -np.arange(1, 257) ** 0.5
+    tiles(w, [101, 40], [101, 35], 256, 128, D, 16, group, "fp16", q_scale=4.0, **kw)
 
 
 @pytest.mark.parametrize("D,group", [(64, 64), (128, 32), (256, 64)])
@@ -56,17 +56,26 @@ def test_masks(w, kind, D, group):  # noqa: F811
         end = np.maximum(end, 50)
     else:
         first, end = r.integers(-50, 220, len(pos)), r.integers(-50, 220, len(pos))
-    out = tiles(w, kv_lens, q_lens, 32, 32, D, 24, group, "bf16", first=first, end=end)
+    out = tiles(w, kv_lens, q_lens, 160, 80, D, 24, group, "bf16", first=first, end=end)
     kv = np.repeat(kv_lens, q_lens)
     empty = np.maximum(first, 0) >= np.minimum(end, kv)
     assert not f64(out)[empty].any()
 
 
+@pytest.mark.parametrize("kind", ["window", "prefix"])
+def test_a_key_head_for_each(w, kind):  # noqa: F811
+    """Blocks of as many tokens as rows."""
+    pos = np.concatenate([np.arange(150), np.arange(10, 210)])
+    masks = {"first": pos - 30} if kind == "window" else {"end": np.maximum(pos + 1, 100)}
+    tiles(w, [150, 210], [150, 200], 96, 96, 128, 24, 64, "fp16", **masks)
+
+
 @pytest.mark.parametrize("D,group", [(64, 32), (128, 128), (256, 32)])
 def test_negative_scale_and_views(w, D, group):  # noqa: F811
-    k, v, table = paged4([100, 70], 32, D, 8, group, 1)
-    q = randn((170, 35 * D), "bf16", 2)[:, D:33 * D].unflatten(1, (32, D))
+    k, v, table = paged4([100, 70], 100, D, 8, group, 1)
+    q = randn((170, 203 * D), "bf16", 2)[:, D:201 * D].unflatten(1, (200, D))
     starts = np.array([0, 100, 170])
+    assert in_blocks(w, 2, 170, 200, 100, D, 100, 100)
     for scale in (-0.1, 0.05):
         out = w.qmm_kv4_attention(q, device(k), device(v), i32(table), i32(np.array([100, 70])), i32(starts), 100, 100, group, scale=scale)
         want, bound = co.attention(f64(q), co.parts(k, D, group, True), co.parts(v, D, group, False), table, [100, 70], starts, scale,
@@ -77,19 +86,19 @@ def test_negative_scale_and_views(w, D, group):  # noqa: F811
 @pytest.mark.parametrize("fill", [float("nan"), float("inf"), 60000.0])
 @pytest.mark.parametrize("D,group", KINDS)
 def test_places_past_the_end_have_no_part(w, D, group, fill):  # noqa: F811
-    tiles(w, [30, 77], [30, 70], 64, 32, D, 16, group, "fp16", fill=fill)
+    tiles(w, [30, 77], [30, 70], 352, 88, D, 16, group, "fp16", fill=fill)
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("D,group", [(64, 32), (128, 64), (256, 128)])
 def test_a_bad_group_reaches_only_queries_that_see_it(w, D, group, bad):  # noqa: F811
     kv = T = 100
-    Hkv, page = 32, 16
+    Hkv, page = 168, 16
     k, v, table = paged4([kv], Hkv, D, page, group, 1)
-    q = randn((T, 64, D), "bf16", 2)
+    q = randn((T, 336, D), "bf16", 2)
     starts = np.array([0, T])
     args = (i32(table), i32(np.array([kv])), i32(starts), T, kv, group)
-    assert in_blocks(w, 1, T, 64, Hkv, D, T, kv)
+    assert in_blocks(w, 1, T, 336, Hkv, D, T, kv)
     clean = w.qmm_kv4_attention(q, device(k), device(v), *args)
     half = np.frombuffer(np.float16(bad).tobytes(), np.uint8)
     for cache, head, key, which, keys in ((k, 0, 97, 0, True), (v, 1, 96, 1, False), (v, 30, 98, 0, False), (v, 2, 60, 0, False)):
@@ -98,7 +107,7 @@ def test_a_bad_group_reaches_only_queries_that_see_it(w, D, group, bad):  # noqa
         block[at:at + 2] = half
     got = w.qmm_kv4_attention(q, device(k), device(v), *args)
     assert torch.equal(got[:60], clean[:60])
-    same = [h for h in range(64) if h // 2 not in (0, 1, 2, 30)]
+    same = [h for h in range(336) if h // 2 not in (0, 1, 2, 30)]
     assert torch.equal(got[:, same], clean[:, same])
     some = [0, 1, 2, 3, 4, 5, 60, 61]  # the query heads of those key heads
     part = lambda c, keys: [x[:, [0, 1, 2, 30]] for x in co.parts(c, D, group, keys)]  # noqa: E731
@@ -108,8 +117,9 @@ def test_a_bad_group_reaches_only_queries_that_see_it(w, D, group, bad):  # noqa
 
 
 def test_a_bad_query_gives_nan_and_only_there(w):  # noqa: F811
-    k, v, table = paged4([100], 32, 128, 16, 64, 1)
-    q = randn((100, 64, 128), "bf16", 2)
+    k, v, table = paged4([100], 168, 128, 16, 64, 1)
+    q = randn((100, 336, 128), "bf16", 2)
+    assert in_blocks(w, 1, 100, 336, 168, 128, 100, 100)
     args = (device(k), device(v), i32(table), i32(np.array([100])), i32(np.array([0, 100])), 100, 100, 64)
     clean = w.qmm_kv4_attention(q, *args)
     q[7, 3, 77] = float("nan")
@@ -123,7 +133,7 @@ def test_a_bad_query_gives_nan_and_only_there(w):  # noqa: F811
 @pytest.mark.parametrize("q_scale,scale", [(300.0, 1.0), (1e-4, 1.0), (1.0, 500.0), (1.0, 1e-3)])
 def test_sizes(w, q_scale, scale):  # noqa: F811
     for dtype in ("fp16", "bf16"):
-        tiles(w, [90], [90], 64, 32, 128, 16, 64, dtype, q_scale=q_scale, scale=scale)
+        tiles(w, [90], [90], 384, 192, 128, 16, 64, dtype, q_scale=q_scale, scale=scale)
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
@@ -131,10 +141,10 @@ def test_padded_batches(w, D):  # noqa: F811
     """Tokens of no sequence get 0, and the others what they get without the padding."""
     say(f"kv4 attention in blocks, padded, D={D}")
     starts, kv_lens, max_q, T = [7, 137, 137, 237, 300], [130, 4, 150, 90], 110, 400
-    k, v, table = paged4(kv_lens, 16, D, 16, 32, 1)
-    q = randn((T, 32, D), "bf16", 2)
+    k, v, table = paged4(kv_lens, 60, D, 16, 32, 1)
+    q = randn((T, 120, D), "bf16", 2)
     rest = (device(k), device(v), i32(table), i32(np.array(kv_lens)))
-    assert in_blocks(w, 4, T, 32, 16, D, max_q, 150)
+    assert in_blocks(w, 4, T, 120, 60, D, max_q, 150)
     out = torch.ones_like(q)
     w.qmm_kv4_attention(q, *rest, i32(np.array(starts)), max_q, max(kv_lens), 32, out=out)
     of_none = np.ones(T, bool)
@@ -163,8 +173,9 @@ def test_blocks_agree_with_tiles(w):  # noqa: F811
 
 
 def test_in_a_graph(w):  # noqa: F811
-    k, v, table = paged4([139, 66], 16, 64, 16, 32, 1)
-    q = randn((205, 32, 64), "fp16", 2)
+    k, v, table = paged4([139, 66], 80, 64, 16, 32, 1)
+    q = randn((205, 160, 64), "fp16", 2)
+    assert in_blocks(w, 2, 205, 160, 80, 64, 139, 139)
     kv = i32(np.array([139, 66]))
     args = (device(k), device(v), i32(table), kv, i32(np.array([0, 139, 205])), 139, 139, 32)
     w.qmm_kv4_attention(q, *args)

@@ -23,7 +23,7 @@ struct Kv4GatherArgs {
 };
 hipError_t launch_kv4_gather(const Kv4GatherArgs& a, bool bf16, hipStream_t stream);
 
-long long kv4_attention_blocks(int B, int Hq, int Hkv, int D, int max_q, int max_kv);
+long long kv4_attention_blocks(const AttentionArgs& a);  // of the grid
 size_t kv4_attention_workspace(int B, int T, int Hq, int Hkv, int D, int max_q, int max_kv);
 hipError_t launch_kv4_attention(const AttentionArgs& a, int group_size, bool bf16, hipStream_t stream);
 

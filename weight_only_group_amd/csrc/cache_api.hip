@@ -112,7 +112,7 @@ qmm_status qmm_kv4_attention(const uint16_t* q, int64_t q_stride, int T, int Hq,
   st = check_attention_shape(a);
   if (st != QMM_OK) return st;
   if (T == 0 || B == 0 || max_q == 0) return ok();
-  st = check_attention_arrays(a, qmm::kv4_attention_blocks(B, Hq, Hkv, D, max_q, max_kv));
+  st = check_attention_arrays(a, qmm::kv4_attention_blocks(a));
   if (st == QMM_OK)
     st = check_workspace(workspace, workspace_bytes, qmm::kv4_attention_workspace(B, T, Hq, Hkv, D, max_q, max_kv));
   if (st != QMM_OK) return st;

@@ -659,36 +659,42 @@ hipError_t launch_split(const AttentionArgs& a, bool bf16, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Blocks of many rows where there are enough of them.
-template <int D>
-bool use_tiles_of(int B, int group, int Hkv, int max_q, DeviceTopo topo) {
-  const long long rows = (long long)max_q * group;
-  return rows > 64 && (long long)B * Hkv * ((rows + kKv4TileRows<D> - 1) / kKv4TileRows<D>) * 4 >= topo.cus;
+// Blocks of many rows, whose keys are not split, where their waves (32 rows each) fill the CUs' SIMDs and the sequences
+// have half a block of rows on average. Measured, time of the parts over that of the blocks, 24 to 32 heads over 8 to 32,
+// dimensions of 128: half as many waves 0.6 to 0.8; as many 1.1 to 1.3; many 1.5 to 1.9; sequences of a quarter of a
+// block 0.7 whatever their number. (Of 256 dimensions as many 1.2 to 1.7, of 64 1.0 to 1.3.)
+// A block of one query head to a key head spans the most positions, so that its rows see the fewest keys in common: with
+// masks or distances it is 0.7 to 1.0 there, where the cases below name it, and else 1.0 to 1.3.
+bool use_tiles(int B, int T, int Hq, int Hkv, int D, int max_q, bool masked, bool biased, DeviceTopo topo) {
+  const long long tokens = std::min<long long>(T, (long long)B * max_q), rows = tokens * (Hq / Hkv);
+  if (rows < 128ll * B || (rows + 31) / 32 * Hkv < 4ll * topo.cus) return false;
+  return Hq != Hkv || !(D == 64 ? masked : D == 256 && biased);
 }
-bool use_tiles(int B, int Hq, int Hkv, int D, int max_q, DeviceTopo topo) {
-  return D == 64 ? use_tiles_of<64>(B, Hq / Hkv, Hkv, max_q, topo)
-         : D == 128 ? use_tiles_of<128>(B, Hq / Hkv, Hkv, max_q, topo) : use_tiles_of<256>(B, Hq / Hkv, Hkv, max_q, topo);
+
+bool tiles_take(const AttentionArgs& a) {
+  return use_tiles(a.B, a.T, a.Hq, a.Hkv, a.D, a.max_q, a.first || a.end, a.slopes, device_topology());
 }
 
 }  // namespace
 
 size_t kv4_attention_workspace(int B, int T, int Hq, int Hkv, int D, int max_q, int max_kv) {
-  if (use_tiles(B, Hq, Hkv, D, max_q, device_topology())) return 0;
+  if (use_tiles(B, T, Hq, Hkv, D, max_q, true, true, device_topology())) return 0;
   const Kv4Plan p = kv4_plan(B, Hq, Hkv, D, max_q, max_kv, device_topology());
   return p.parts ? kWorkspaceHeader + p.blocks * kRows * (D + 2) * sizeof(float) : 0;
 }
 
-long long kv4_attention_blocks(int B, int Hq, int Hkv, int D, int max_q, int max_kv) {
-  if (use_tiles(B, Hq, Hkv, D, max_q, device_topology())) {
+long long kv4_attention_blocks(const AttentionArgs& a) {
+  const int B = a.B, Hq = a.Hq, Hkv = a.Hkv, D = a.D, max_q = a.max_q;
+  if (tiles_take(a)) {
     // (twice as many where a block has eight waves: the limit on blocks is one on threads)
     const int rows = D == 256 ? kKv4TileRows<256> : kKv4TileRows<128>;
     return tile_blocks(B, Hkv, row_tiles(max_q, Hq / Hkv, rows)) * (D == 256 ? 1 : 2);
   }
-  return kv4_plan(B, Hq, Hkv, D, max_q, max_kv, device_topology()).blocks;
+  return kv4_plan(B, Hq, Hkv, D, max_q, a.max_kv, device_topology()).blocks;
 }
 
 hipError_t launch_kv4_attention(const AttentionArgs& a, int group_size, bool bf16, hipStream_t stream) {
-  if (use_tiles(a.B, a.Hq, a.Hkv, a.D, a.max_q, device_topology())) {
+  if (tiles_take(a)) {
     const Kv4TileArgs t = {a, bf16};
     return a.D == 64 ? launch_kv4_tiles<64>(t, group_size, stream)
            : a.D == 128 ? launch_kv4_tiles<128>(t, group_size, stream) : launch_kv4_tiles<256>(t, group_size, stream);
