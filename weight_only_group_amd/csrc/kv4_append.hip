@@ -57,16 +57,22 @@ struct AppendKernelArgs {
   FixedDiv by_page;
   int groups;
   int group_lanes, group_shift;  // lanes per group; log2 of it
+  unsigned xcds;
 };
 
 // Eight values of one head per thread. A thread of a rotated half loads its partner's
-// eight values too: a group's values then lie in neighbouring lanes.
+// eight values too: a group's values then lie in neighbouring lanes. Bound by memory: 16381 tokens (24 heads of 64 over 4,
+// 124 MB in all) take 29.6 us, 4.2 TB/s; the queries alone 19.8 us, 5.1 TB/s, and the rest is the scattered writes of the
+// codes, two or four bytes each. (Neighbouring tokens on different XCDs: 30.8 us. Threads of two and four heads, which load
+// a token's angles and slot once: 31.0 and 34.8 us, and 7 tokens 5.4 and 7.8 us for 4.1.)
 template <bool BF, bool ADJ>
 __global__ void __launch_bounds__(256) kv4_append_kernel(AppendKernelArgs p) {
   const AppendArgs& a = p.a;
   const int chunks = a.D / 8;
   const int heads = a.Hq + 2 * a.Hkv;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  // Neighbouring tokens on one XCD (blocks go round them), whose L2 then holds a block of the cache whole.
+  const unsigned block_i = blockIdx.x % p.xcds * (gridDim.x / p.xcds) + blockIdx.x / p.xcds;
+  const long long i = (long long)block_i * 256 + threadIdx.x;
   const int c = (int)(i % chunks);
   const long long th = i / chunks;
   const int h = (int)(th % heads);
@@ -167,64 +173,86 @@ struct GatherKernelArgs {
   int group_shift;  // log2 of a group's threads
 };
 
-// Eight values of one head per thread, as for the append.
-template <bool BF>
+// Eight values of a token per thread, of HEADS heads: blockIdx.y tells which, of the keys, then the values. Bound by memory,
+// the results' writes above all: 50021 tokens (8 heads of 128, 259 MB in all) take 52 us, 5.0 TB/s, as fast as a large
+// copy; with one head per thread 80 us, with the results kept in the L2s 66. Where one head per thread does not fill the
+// CUs' waves it is faster (7 tokens 3.4 against 3.9 us).
+template <bool BF, int HEADS>
 __global__ void __launch_bounds__(256) kv4_gather_kernel(GatherKernelArgs p) {
   const Kv4GatherArgs& a = p.a;
   const int chunks = a.D / 8;
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   const int c = (int)(i % chunks);
-  const long long th = i / chunks;
-  const int h = (int)(th % (2 * a.Hkv));
-  const long long t = th / (2 * a.Hkv);
+  const long long t = i / chunks;
   if (t >= a.T) return;
-  const bool is_v = h >= a.Hkv;
-  const int hk = is_v ? h - a.Hkv : h;
-  uint16_t* dst = (is_v ? a.v : a.k) + (t * a.Hkv + hk) * a.D + 8 * c;
+  const int parts = (a.Hkv + HEADS - 1) / HEADS;
+  const bool is_v = (int)blockIdx.y >= parts;
+  const int h0 = ((int)blockIdx.y - (is_v ? parts : 0)) * HEADS, here = min(HEADS, a.Hkv - h0);
+  uint16_t* dst = (is_v ? a.v : a.k) + (t * a.Hkv + h0) * a.D + 8 * c;
   const int64_t slot = a.slots[t];
   if (slot < 0 || slot >= (long long)a.pages * a.page_size) {
-    *reinterpret_cast<u32x4*>(dst) = u32x4{0, 0, 0, 0};
+    for (int h = 0; h < here; ++h) *reinterpret_cast<u32x4*>(dst + h * a.D) = u32x4{0, 0, 0, 0};
     return;
   }
   const int page = p.by_page((int)slot);
   int at = (int)slot - page * a.page_size;
-  const int groups = a.D / a.group_size;
-  const long long row = ((long long)page * a.Hkv + hk) * a.page_size + at;
-  const uint8_t* block = (is_v ? a.v_cache : a.k_cache) + row / kBlockTokens * kv4_block_bytes(a.D, groups);
+  const int groups = a.D / a.group_size, block_bytes = kv4_block_bytes(a.D, groups);
+  const long long row = ((long long)page * a.Hkv + h0) * a.page_size + at;
+  const uint8_t* block = (is_v ? a.v_cache : a.k_cache) + row / kBlockTokens * block_bytes;
+  const size_t to_next = (size_t)a.page_size / kBlockTokens * block_bytes;  // the next head's
   at %= kBlockTokens;
   const int g = c >> p.group_shift;
-  const f16* rest = reinterpret_cast<const f16*>(block + 4 * a.D);
-  uint32_t w;
-  float s, m;
-  if (!is_v) {
-    w = reinterpret_cast<const uint32_t*>(block)[at * chunks + (a.D / 32) * (c & 3) + c / 4];
-    s = (float)rest[at * 2 * groups + g];
-    m = (float)rest[at * 2 * groups + groups + g];
-  } else {
-    const uint16_t* codes = reinterpret_cast<const uint16_t*>(block);
-    w = codes[(2 * c) * kBlockTokens + at] | (uint32_t)codes[(2 * c + 1) * kBlockTokens + at] << 16;
-    s = (float)rest[g * 2 * kBlockTokens + at];
-    m = (float)rest[(g * 2 + 1) * kBlockTokens + at];
-  }
-  if (!(fabsf(s) < INFINITY) || !(fabsf(m) < INFINITY)) s = m = NAN;
-  u32x4 out;
+  uint32_t w[HEADS];
+  f16 s[HEADS], m[HEADS];
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    const int lo = is_v ? 8 * x : 4 * x, hi = is_v ? 8 * x + 4 : 16 + 4 * x;
-    const float u = m + s * (float)((int)(w >> lo & 15) - 8), v = m + s * (float)((int)(w >> hi & 15) - 8);
-    out[x] = float_to_bits<BF>(u) | (uint32_t)float_to_bits<BF>(v) << 16;
+  for (int h = 0; h < HEADS; ++h) {
+    const uint8_t* from = block + (h < here ? h : 0) * to_next;
+    const f16* rest = reinterpret_cast<const f16*>(from + 4 * a.D);
+    if (!is_v) {
+      w[h] = reinterpret_cast<const uint32_t*>(from)[at * chunks + (a.D / 32) * (c & 3) + c / 4];
+      s[h] = rest[at * 2 * groups + g];
+      m[h] = rest[at * 2 * groups + groups + g];
+    } else {
+      const uint16_t* codes = reinterpret_cast<const uint16_t*>(from);
+      w[h] = codes[(2 * c) * kBlockTokens + at] | (uint32_t)codes[(2 * c + 1) * kBlockTokens + at] << 16;
+      s[h] = rest[g * 2 * kBlockTokens + at];
+      m[h] = rest[(g * 2 + 1) * kBlockTokens + at];
+    }
   }
-  *reinterpret_cast<u32x4*>(dst) = out;
+#pragma unroll
+  for (int h = 0; h < HEADS; ++h) {
+    float sh = (float)s[h], mh = (float)m[h];
+    if (!(fabsf(sh) < INFINITY) || !(fabsf(mh) < INFINITY)) sh = mh = NAN;
+    u32x4 out;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int lo = is_v ? 8 * x : 4 * x, hi = is_v ? 8 * x + 4 : 16 + 4 * x;
+      const float u = mh + sh * (float)((int)(w[h] >> lo & 15) - 8), v = mh + sh * (float)((int)(w[h] >> hi & 15) - 8);
+      out[x] = float_to_bits<BF>(u) | (uint32_t)float_to_bits<BF>(v) << 16;
+    }
+    if (h >= here) continue;
+    u32x4* to = reinterpret_cast<u32x4*>(dst + h * a.D);
+    // (more than fits in the L2s, which then keep the cache's lines for the threads that come back to them)
+    if (HEADS > 1) __builtin_nontemporal_store(out, to);
+    else *to = out;
+  }
 }
 
 int log2_of(int n) { return __builtin_ctz((unsigned)n); }
+
+template <bool BF, int HEADS>
+void launch_gather_heads(const GatherKernelArgs& p, hipStream_t stream) {
+  const long long n = (long long)p.a.T * (p.a.D / 8);
+  kv4_gather_kernel<BF, HEADS><<<dim3((unsigned)((n + 255) / 256), 2 * ((p.a.Hkv + HEADS - 1) / HEADS)), 256, 0, stream>>>(p);
+}
 
 }  // namespace
 
 hipError_t launch_kv4_append(const AppendArgs& a, int group_size, bool bf16, bool adjacent, hipStream_t stream) {
   const long long n = (long long)a.T * (a.Hq + 2 * a.Hkv) * (a.D / 8);
-  const dim3 grid((unsigned)((n + 255) / 256));
-  const AppendKernelArgs p = {a, fixed_div(a.page_size), a.D / group_size, group_size / 8, log2_of(group_size / 8)};
+  const int xcds = device_topology().xcds;
+  const dim3 grid((unsigned)((n + 256 * xcds - 1) / (256 * xcds) * xcds));
+  const AppendKernelArgs p = {a, fixed_div(a.page_size), a.D / group_size, group_size / 8, log2_of(group_size / 8), (unsigned)xcds};
   if (bf16 && adjacent) kv4_append_kernel<true, true><<<grid, 256, 0, stream>>>(p);
   else if (bf16) kv4_append_kernel<true, false><<<grid, 256, 0, stream>>>(p);
   else if (adjacent) kv4_append_kernel<false, true><<<grid, 256, 0, stream>>>(p);
@@ -233,11 +261,10 @@ hipError_t launch_kv4_append(const AppendArgs& a, int group_size, bool bf16, boo
 }
 
 hipError_t launch_kv4_gather(const Kv4GatherArgs& a, bool bf16, hipStream_t stream) {
-  const long long n = (long long)a.T * 2 * a.Hkv * (a.D / 8);
-  const dim3 grid((unsigned)((n + 255) / 256));
   const GatherKernelArgs p = {a, fixed_div(a.page_size), log2_of(a.group_size / 8)};
-  if (bf16) kv4_gather_kernel<true><<<grid, 256, 0, stream>>>(p);
-  else kv4_gather_kernel<false><<<grid, 256, 0, stream>>>(p);
+  const bool many = (long long)a.T * 2 * a.Hkv * (a.D / 8) > 32ll * 64 * device_topology().cus;
+  if (many) bf16 ? launch_gather_heads<true, 2>(p, stream) : launch_gather_heads<false, 2>(p, stream);
+  else bf16 ? launch_gather_heads<true, 1>(p, stream) : launch_gather_heads<false, 1>(p, stream);
   return hipGetLastError();
 }
 
