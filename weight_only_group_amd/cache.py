@@ -62,12 +62,12 @@ def kv4_page_bytes(page_size: int, D: int, group_size: int) -> int:
 def _kv4_cache(k_cache, v_cache, D, group_size, dev):
     """Pages, heads and page size of a 4-bit cache, checked."""
     block = kv4_page_bytes(8, D, group_size)
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 3 or k_cache.shape[2] % block or not k_cache.shape[2]:
+    shape = k_cache.shape if isinstance(k_cache, torch.Tensor) else ()
+    if len(shape) != 3 or shape[2] % block or not shape[2]:
         raise ValueError(f"k_cache must be a tensor (pages, Hkv, kv4_page_bytes(page_size, {D}, {group_size}))")
-    _array(k_cache, "k_cache", torch.uint8, k_cache.shape, dev)
-    _array(v_cache, "v_cache", torch.uint8, k_cache.shape, dev)
-    pages, Hkv, page = k_cache.shape
-    return pages, Hkv, page // block * 8
+    _array(k_cache, "k_cache", torch.uint8, shape, dev)
+    _array(v_cache, "v_cache", torch.uint8, shape, dev)
+    return shape[0], shape[1], shape[2] // block * 8
 
 
 def qmm_kv4_append(q, k, v, cos, sin, positions, slots, k_cache, v_cache, group_size: int, adjacent: bool = False, out=None):
@@ -150,6 +150,22 @@ def _pools(caches):
     """Pointers, bytes per page, count, pages and device of caches (each contiguous, pages first), checked."""
     if isinstance(caches, torch.Tensor) or not len(caches):
         raise ValueError("caches must be a sequence of tensors, one at least")
+    try:  # of many caches the checks take longer than the copies: the fewest calls for those that are right
+        first = caches[0]
+        pages, index = first.size(0), first.get_device()
+        bad = index < 0 or any([t.get_device() != index or t.dim() < 2 or t.size(0) != pages or not t.is_contiguous() for t in caches])
+        sizes = [] if bad else [t.nbytes // pages for t in caches]
+        bad = bad or 0 in sizes
+    except (AttributeError, IndexError, ZeroDivisionError, RuntimeError):
+        bad = True
+    if bad:
+        _refuse_pools(caches)
+    n = len(sizes)
+    return (ctypes.c_void_p * n)(*[t.data_ptr() for t in caches]), (ctypes.c_int64 * n)(*sizes), n, pages, first.device
+
+
+def _refuse_pools(caches):
+    """The error of caches that _pools finds wrong."""
     for i, t in enumerate(caches):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"caches[{i}] must be a torch.Tensor")
@@ -161,10 +177,7 @@ def _pools(caches):
             raise ValueError(f"caches[{i}] must have the first one's pages and more dimensions (got shape {tuple(t.shape)})")
         if not t.is_contiguous():
             raise ValueError(f"caches[{i}] must be contiguous")
-    n, pages = len(caches), caches[0].shape[0]
-    pointers = (ctypes.c_void_p * n)(*[t.data_ptr() for t in caches])
-    sizes = (ctypes.c_int64 * n)(*[t.numel() // pages * t.element_size() for t in caches])
-    return pointers, sizes, n, pages, caches[0].device
+    raise ValueError("caches must be tensors in memory of their own")
 
 
 def qmm_kv_copy_pages(caches, src, dst):
