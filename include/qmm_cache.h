@@ -95,7 +95,7 @@ qmm_status qmm_kv4_attention(const uint16_t* q, int64_t q_stride, int T, int Hq,
  * qmm_kv_copy_pages -- page dst[i] of every cache becomes page src[i], i < n: pages
  * of a forked sequence that is to write on, a prefix for another owner. src and dst (n,) int32. A pair with an
  * index outside [0, pages) is left out. A page may be copied many times; no
- * page may be in dst twice, nor in dst and (of another pair) in src. n * 2^16 < 2^47.
+ * page may be in dst twice, nor in dst and (of another pair) in src.
  */
 qmm_status qmm_kv_copy_pages(void* const* caches, const int64_t* page_bytes, int n_caches, int pages,
                              const int32_t* src, const int32_t* dst, int n, hipStream_t stream);

@@ -190,3 +190,19 @@ def test_in_a_graph(w):  # noqa: F811
         torch.cuda.synchronize()
         got = out.clone()
         assert torch.equal(got, w.qmm_kv4_attention(q, *args)), n
+
+
+def test_large_cache_offsets(w):  # noqa: F811
+    """Pages past 2^32 bytes."""
+    Hq, Hkv, D, page, group, n = 168, 8, 256, 128, 32, 200
+    size = w.kv4_page_bytes(page, D, group)
+    pages = (1 << 32) // (Hkv * size) + 5
+    k = torch.zeros((pages, Hkv, size), dtype=torch.uint8, device=DEV)
+    v = torch.zeros_like(k)
+    last = [device(c) for c in paged4([2 * page], Hkv, D, page, group, 1, spare=0)[:2]]
+    k[-2:], v[-2:] = last
+    q = randn((n, Hq, D), "fp16", 3)
+    assert in_blocks(w, 1, n, Hq, Hkv, D, n, n)
+    rest = (i32(np.array([n])), i32(np.array([0, n])), n, n, group)
+    out = w.qmm_kv4_attention(q, k, v, i32(np.array([[pages - 1, pages - 2]])), *rest)
+    assert torch.equal(out, w.qmm_kv4_attention(q, *last, i32(np.array([[1, 0]])), *rest)) and out.any()
