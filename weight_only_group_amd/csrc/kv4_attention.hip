@@ -80,6 +80,11 @@ __device__ __forceinline__ float max_of_rows(float v) {
 // take 10 us. With c chunks a part, sum ceil(chunks / c) is at most sum chunks / c + tiles, so c =
 // sum chunks / parts gives no more blocks than parts + tiles; smaller ones are tried first.
 // A sequence's chunks are those of its first and last query.
+// Beyond kMostTiles tiles there are enough for one part each; of sequences of 17 to 128 rows half of them (longer
+// ones' last tiles see the most keys: in parts two or three prompts of 2000 to 3000 rows take 0.3 to 0.5 of the time).
+// Of several tiles a block then takes two, so that its keys and values are decoded once for both: against parts, sequences
+// of 17 to 32 rows in 2049 to 4096 tiles 1.5 times as fast (one tile a block: 1.2), of 65 to 128 rows 1.15 (1.07);
+// against one tile a block, in more tiles 1.25 and 1.03 to 1.1. D 256 has no registers for it (0.6 to 1.1).
 constexpr int kMostSequences = 1024;  // of a split launch
 constexpr int kMostTiles = 4096;
 constexpr int kMostParts = 256;       // of a tile
@@ -92,6 +97,7 @@ struct Kv4Plan {
   int group, rtiles;
   int fit;    // blocks that run at a time
   int parts;  // parts beyond one a tile that there may be; 0: one a tile
+  bool wide;  // a block takes two tiles
   long long blocks;
 };
 Kv4Plan kv4_plan(int B, int Hq, int Hkv, int D, int max_q, int max_kv, DeviceTopo topo) {
@@ -101,8 +107,11 @@ Kv4Plan kv4_plan(int B, int Hq, int Hkv, int D, int max_q, int max_kv, DeviceTop
   const long long tiles = (long long)B * Hkv * p.rtiles;
   p.fit = resident_blocks(D, topo);
   p.parts = 0;
-  if (B <= kMostSequences && tiles <= kMostTiles && max_kv > kLeastChunks * kChunk) p.parts = (int)std::max(p.fit - tiles, p.fit / 2ll);
+  const long long rows = (long long)max_q * p.group;
+  if (B <= kMostSequences && tiles <= (rows > kRows && rows <= 8 * kRows ? kMostTiles / 2 : kMostTiles) && max_kv > kLeastChunks * kChunk) p.parts = (int)std::max(p.fit - tiles, p.fit / 2ll);
   const long long most = ((long long)max_kv + kLeastChunks * kChunk - 1) / (kLeastChunks * kChunk);
+  p.wide = rows > kRows && !p.parts && D <= 128;
+  if (p.wide) p.rtiles = row_tiles(max_q, p.group, 2 * kRows);
   p.blocks = p.parts ? std::min(tiles + p.parts, tiles * most) : tile_blocks(B, Hkv, p.rtiles);
   return p;
 }
@@ -293,7 +302,7 @@ __device__ __forceinline__ void join_parts(const Kv4KernelArgs& p, const Share& 
   }
 }
 
-// Block: one tile of 16 rows, one part of its keys, in chunks of 32 keys a wave, as for the
+// Block: a tile of 16 rows (or RT of them), one part of its keys, in chunks of 32 keys a wave, as for the
 // cache of 16-bit values. The products are K q^T and V^T p^T. Row i of a chunk's t-th
 // sixteen is key 8 (i / 4) + 4 t + i % 4, so that a lane's scores are those of one block of
 // eight tokens, whose values' words hold two tokens each: they need no exchange.
@@ -302,13 +311,15 @@ __device__ __forceinline__ void join_parts(const Kv4KernelArgs& p, const Share& 
 // asked for as the registers fall free. Few rows are bound by memory and by a block's start and end (the share of the work,
 // page, keys; the join of the parts: 10 us together): 48 decodes of 128 to 8192 keys (32 heads of 128 over 8, 92 MB) 28.8 us,
 // three on up to 131071 (157 MB) 39 us, 4.0 TB/s; one on 1500 keys 11 us, all of it latency. Tiles of sixteen rows are bound by
-// the vector ALUs, 77% busy over documents of 24 heads of 64 (49 us): codes are decoded again in each.
+// the vector ALUs, 77% busy over documents of 24 heads of 64 (49 us): codes are decoded again in each. Two tiles a block: 47.5 us.
+//
+// RT: tiles of a block, one behind another (a wave's operands serve both); with parts one.
 //
 // NARROW: no more than four rows (one token of up to four heads a key head). Twelve of
 // a product's sixteen columns are then free: the scores of the eight keys of a lane are spread
 // over them, two a lane, for the softmax.
-template <int D, int G, bool NARROW>
-__global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4KernelArgs k) {
+template <int D, int G, bool NARROW, int RT>
+__global__ void __launch_bounds__(256, D == 256 || (D == 128 && RT == 2) ? 2 : 3) kv4_split_kernel(Kv4KernelArgs k) {
   constexpr int STEPS = D / 32, U = D / 64, GS = D / G, BLOCK = kv4_block_bytes(D, G);
   constexpr int NS = GS == 32 ? U : G;  // sets of scales that a lane needs for its values
   constexpr int LD = D + 4;
@@ -323,7 +334,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4Ker
   const uint8_t* k_cache = reinterpret_cast<const uint8_t*>(a.k_cache);
   const uint8_t* v_cache = reinterpret_cast<const uint8_t*>(a.v_cache);
   Share share;
-  if (k.parts) {
+  if (RT == 1 && k.parts) {
     share = share_of(k);
     if (share.b < 0) return;
   } else {
@@ -334,17 +345,26 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4Ker
   }
   const int b = share.b, hk = share.hk, rt = share.rt;
   const Span span = share.span;
-  const int rtiles = max(row_tiles_of(span, p.group), 1);
+  const int rtiles = max((row_tiles_of(span, p.group) + RT - 1) / RT, 1);
   zero_rest<D>(p, span, b, hk, rt * share.parts + share.part, rtiles * share.parts);
-  const int rows_left = (span.q1 - span.q0) * p.group - rt * kRows;
+  const int rows_left = (span.q1 - span.q0) * p.group - rt * RT * kRows;
   if (rows_left <= 0) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 15, kg = lane >> 4;
-  const Row row = row_of(p, rt * kRows + (NARROW ? n & 3 : n), span, hk);
-  ScoreRule rule = score_rule(a, row.head);
+  Row row[RT];
+  ScoreRule rule[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    row[r] = row_of(p, (rt * RT + r) * kRows + (NARROW ? n & 3 : n), span, hk);
+    rule[r] = score_rule(a, row[r].head);
+  }
 
   // The keys that any row sees, and those that all see (rows past the last count as seeing all).
-  int lo = row.lo < row.hi ? row.lo : INT32_MAX, hi = row.lo < row.hi ? row.hi : 0;
-  int all_lo = row.token < 0 ? 0 : row.lo, all_hi = row.token < 0 ? INT32_MAX : row.hi;
+  int lo = INT32_MAX, hi = 0, all_lo = 0, all_hi = INT32_MAX;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    if (row[r].lo < row[r].hi) lo = min(lo, row[r].lo), hi = max(hi, row[r].hi);
+    if (row[r].token >= 0) all_lo = max(all_lo, row[r].lo), all_hi = min(all_hi, row[r].hi);
+  }
   lo = __builtin_amdgcn_readfirstlane(least_of_row(lo));
   hi = __builtin_amdgcn_readfirstlane(largest_of_row(hi));
   all_lo = __builtin_amdgcn_readfirstlane(largest_of_row(all_lo));
@@ -354,11 +374,13 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4Ker
   const int c0 = c_first + (int)((long long)chunks * share.part / share.parts), c1 = c_first + (int)((long long)chunks * (share.part + 1) / share.parts);
 
   // The row's query, asked for ahead of the keys that its use waits for too.
-  u32x4 raw[STEPS];
+  u32x4 q[RT][STEPS];
 #pragma unroll
-  for (int s = 0; s < STEPS; ++s)
-    raw[s] = row.token < 0 ? u32x4{0, 0, 0, 0}
-                           : *reinterpret_cast<const u32x4*>(a.q + row.token * a.q_stride + (long long)row.head * D + s * 32 + kg * 8);
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+      q[r][s] = row[r].token < 0 ? u32x4{0, 0, 0, 0}
+                                 : *reinterpret_cast<const u32x4*>(a.q + row[r].token * a.q_stride + (long long)row[r].head * D + s * 32 + kg * 8);
 
   // Number of the block of eight tokens that holds tokens 8 (lane & 3) on of a chunk; past
   // the seen keys' ends the nearest.
@@ -403,35 +425,36 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4Ker
   }
 
   // The row's query in fp16, and its groups' sums in three parts (lane group 0: the first, ...).
-  u32x4 q[STEPS], qsum = {0, 0, 0, 0};
-  {
+  u32x4 qsum[RT];
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) q[s] = raw[s];
-    const float back = scale_query<4>(q, bf16_data);
-    rule.scale = fminf(fmaxf(rule.scale * back, -3e38f), 3e38f);
-    rule.inverse = fminf(fmaxf(rule.inverse * back, -3e38f), 3e38f);
+  for (int r = 0; r < RT; ++r) {
+    const float back = scale_query<4>(q[r], bf16_data);
+    rule[r].scale = fminf(fmaxf(rule[r].scale * back, -3e38f), 3e38f);
+    rule[r].inverse = fminf(fmaxf(rule[r].inverse * back, -3e38f), 3e38f);
     f16 part_of[8] = {};
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       f32x4 sums = {};  // in every lane of a column
 #pragma unroll
-      for (int s = g * GS / 32; s < (g + 1) * GS / 32; ++s) sums = mfma16<false>(u32x4{kOnes, kOnes, kOnes, kOnes}, q[s], sums);
+      for (int s = g * GS / 32; s < (g + 1) * GS / 32; ++s) sums = mfma16<false>(u32x4{kOnes, kOnes, kOnes, kOnes}, q[r][s], sums);
       const float s = sums[0];
       const f16 first = (f16)s, second = (f16)(s - (float)first), third = (f16)(s - (float)first - (float)second);
       part_of[g] = kg == 0 ? first : kg == 1 ? second : kg == 2 ? third : (f16)0.f;
     }
 #pragma unroll
-    for (int x = 0; x < 4; ++x) qsum[x] = as_u32(f16x2{part_of[2 * x], part_of[2 * x + 1]});
+    for (int x = 0; x < 4; ++x) qsum[r][x] = as_u32(f16x2{part_of[2 * x], part_of[2 * x + 1]});
   }
 
   const DecodeMasks masks;
-  f32x4 acc[U][4] = {}, rest = {};  // rest: rows g the sums of p m_g, row 15 the sum of p
-  float mx = -INFINITY;
+  f32x4 acc[RT][U][4] = {}, rest[RT] = {};  // rest: rows g the sums of p m_g, row 15 the sum of p
+  float mx[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) mx[r] = -INFINITY;
   bool any_bad = false;
   // One chunk; with MORE the next one's loads go out as the registers fall free.
   auto step = [&](int c, auto more) {
     constexpr bool MORE = decltype(more)::value;
-    f32x4 st[2] = {};
+    f32x4 st[RT][2] = {};
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       // Halves [s of all groups][m of all groups].
@@ -442,7 +465,8 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4Ker
 #pragma unroll
         for (int x = 0; x < G / 2; ++x) middles[x] = kp[t][G / 2 + x];
       }
-      st[t] = mfma16<false>(middles, qsum, st[t]);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) st[r][t] = mfma16<false>(middles, qsum[r], st[r][t]);
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
         const int g = s * 32 / GS;
@@ -450,8 +474,9 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4Ker
         const f16 sg = as_f16x2(pair)[g % 2];
         const f16x2 ss = {sg, sg}, c24 = times_24(ss);
         const uint32_t w = kw[t][s];
-        st[t] = mfma16<false>(u32x4{decode<0>(w, ss, c24, masks), decode<1>(w, ss, c24, masks), decode<2>(w, ss, c24, masks),
-                                     decode<3>(w, ss, c24, masks)}, q[s], st[t]);
+        const u32x4 keys = {decode<0>(w, ss, c24, masks), decode<1>(w, ss, c24, masks), decode<2>(w, ss, c24, masks), decode<3>(w, ss, c24, masks)};
+#pragma unroll
+        for (int r = 0; r < RT; ++r) st[r][t] = mfma16<false>(keys, q[r][s], st[r][t]);
       }
     }
     if constexpr (MORE) {
@@ -467,58 +492,61 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4Ker
     constexpr int NX = NARROW ? 2 : 8;
     const int j0 = c * kChunk + 8 * kg + (NARROW ? 2 * (n >> 2) : 0);
     const bool whole = seen_by_all(c);
-    float s[NX], best = -INFINITY;
-    if constexpr (NARROW) {
-      s[0] = spread(st[0][0], st[0][2], st[1][0], st[1][2]);
-      s[1] = spread(st[0][1], st[0][3], st[1][1], st[1][3]);
-    } else {
+    u32x4 w[RT];
 #pragma unroll
-      for (int x = 0; x < NX; ++x) s[x] = st[x >> 2][x & 3];
-    }
-    if (k.cap == kNoCap) {
+    for (int r = 0; r < RT; ++r) {
+      float s[NX], best = -INFINITY;
+      if constexpr (NARROW) {
+        s[0] = spread(st[r][0][0], st[r][0][2], st[r][1][0], st[r][1][2]);
+        s[1] = spread(st[r][0][1], st[r][0][3], st[r][1][1], st[r][1][3]);
+      } else {
 #pragma unroll
-      for (int x = 0; x < NX; ++x) s[x] = rule.template score<kNoCap, false>(s[x], 0, 0);
-    } else if (k.cap == kSmallCap) {
+        for (int x = 0; x < NX; ++x) s[x] = st[r][x >> 2][x & 3];
+      }
+      if (k.cap == kNoCap) {
 #pragma unroll
-      for (int x = 0; x < NX; ++x) s[x] = rule.template score<kSmallCap, false>(s[x], 0, 0);
-    } else {
+        for (int x = 0; x < NX; ++x) s[x] = rule[r].template score<kNoCap, false>(s[x], 0, 0);
+      } else if (k.cap == kSmallCap) {
 #pragma unroll
-      for (int x = 0; x < NX; ++x) s[x] = rule.template score<kAnyCap, false>(s[x], 0, 0);
-    }
-    if (a.slopes) {
+        for (int x = 0; x < NX; ++x) s[x] = rule[r].template score<kSmallCap, false>(s[x], 0, 0);
+      } else {
 #pragma unroll
-      for (int x = 0; x < NX; ++x) s[x] -= rule.slope * fabsf((float)(row.pos - (j0 + x)));
-    }
-    if (!whole) {
+        for (int x = 0; x < NX; ++x) s[x] = rule[r].template score<kAnyCap, false>(s[x], 0, 0);
+      }
+      if (a.slopes) {
 #pragma unroll
-      for (int x = 0; x < NX; ++x) s[x] = j0 + x >= row.lo && j0 + x < row.hi ? s[x] : -INFINITY;
-    }
+        for (int x = 0; x < NX; ++x) s[x] -= rule[r].slope * fabsf((float)(row[r].pos - (j0 + x)));
+      }
+      if (!whole) {
 #pragma unroll
-    for (int x = 0; x < NX; ++x) best = fmaxf(best, s[x]);
-    if (NARROW) {
-      best = fmaxf(best, rotated<4>(best));
-      best = fmaxf(best, rotated<8>(best));
-    }
-    best = max_of_rows(best);
-    if (__any(best > mx + kSlack)) {
-      const float m = best > mx + kSlack ? best : mx;
-      const float f = mx == m ? 1.f : __builtin_amdgcn_exp2f(mx - m);
-      rest *= f;
+        for (int x = 0; x < NX; ++x) s[x] = j0 + x >= row[r].lo && j0 + x < row[r].hi ? s[x] : -INFINITY;
+      }
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int x = 0; x < NX; ++x) best = fmaxf(best, s[x]);
+      if (NARROW) {
+        best = fmaxf(best, rotated<4>(best));
+        best = fmaxf(best, rotated<8>(best));
+      }
+      best = max_of_rows(best);
+      if (__any(best > mx[r] + kSlack)) {
+        const float m = best > mx[r] + kSlack ? best : mx[r];
+        const float f = mx[r] == m ? 1.f : __builtin_amdgcn_exp2f(mx[r] - m);
+        rest[r] *= f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[u][i] *= f;
-      mx = m;
-    }
-    const float off = mx == -INFINITY ? 0.f : mx - kLift;
-    u32x4 w;
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int x = 0; x < NX / 2; ++x)
-      w[x] = pack_pair<false>(__builtin_amdgcn_exp2f(s[2 * x] - off), __builtin_amdgcn_exp2f(s[2 * x + 1] - off));
-    if constexpr (NARROW) {  // (what columns past the fourth get is in no result)
-      w[1] = shifted<4>(w[0]);
-      w[2] = shifted<8>(w[0]);
-      w[3] = shifted<12>(w[0]);
+          for (int i = 0; i < 4; ++i) acc[r][u][i] *= f;
+        mx[r] = m;
+      }
+      const float off = mx[r] == -INFINITY ? 0.f : mx[r] - kLift;
+#pragma unroll
+      for (int x = 0; x < NX / 2; ++x)
+        w[r][x] = pack_pair<false>(__builtin_amdgcn_exp2f(s[2 * x] - off), __builtin_amdgcn_exp2f(s[2 * x + 1] - off));
+      if constexpr (NARROW) {  // (what columns past the fourth get is in no result)
+        w[r][1] = shifted<4>(w[r][0]);
+        w[r][2] = shifted<8>(w[r][0]);
+        w[r][3] = shifted<12>(w[r][0]);
+      }
     }
     if (!whole) {
       // Places that no row sees may hold anything: their scales and middles count as 0. So do those
@@ -544,7 +572,8 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4Ker
       u32x4 m = vm;
 #pragma unroll
       for (int x = 0; x < 4; ++x) m[x] = n < G ? m[x] : n == 15 ? kOnes : 0u;
-      rest = mfma16<false>(m, w, rest);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) rest[r] = mfma16<false>(m, w[r], rest[r]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -560,7 +589,8 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4Ker
         u32x4 vt;
 #pragma unroll
         for (int x = 0; x < 4; ++x) vt[x] = decode<R>(vw[u][x], ss[x], c24[x], masks);
-        acc[u][R] = mfma16<false>(vt, w, acc[u][R]);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[r][u][R] = mfma16<false>(vt, w[r], acc[r][u][R]);
       };
       product(std::integral_constant<int, 0>{});
       product(std::integral_constant<int, 1>{});
@@ -578,76 +608,80 @@ __global__ void __launch_bounds__(256, D == 256 ? 2 : 3) kv4_split_kernel(Kv4Ker
     step(c, std::false_type{});
   }
 
-  // The waves' sums meet in LDS. Register r of acc[u][i] is channel 64 u + 16 kg + 4 r + i.
-  const float sum = __shfl(rest[3], 48 + n);
+  // The waves' sums meet in LDS, sixteen rows at a time. Register r of acc[t][u][i] is channel 64 u + 16 kg + 4 r + i.
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    float middle;
-    if constexpr (GS == 32) {  // of group 2 u + kg / 2
-      const float m0 = __shfl(rest[2 * u & 3], (2 * u >> 2) * 16 + n), m1 = __shfl(rest[(2 * u + 1) & 3], ((2 * u + 1) >> 2) * 16 + n);
-      middle = kg >> 1 ? m1 : m0;
-    } else {
-      constexpr int PER = GS / 64;
-      middle = __shfl(rest[u / PER & 3], (u / PER >> 2) * 16 + n);
+  for (int t = 0; t < RT; ++t) {
+    if (t > 0) __syncthreads();
+    const float sum = __shfl(rest[t][3], 48 + n);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float middle;
+      if constexpr (GS == 32) {  // of group 2 u + kg / 2
+        const float m0 = __shfl(rest[t][2 * u & 3], (2 * u >> 2) * 16 + n), m1 = __shfl(rest[t][(2 * u + 1) & 3], ((2 * u + 1) >> 2) * 16 + n);
+        middle = kg >> 1 ? m1 : m0;
+      } else {
+        constexpr int PER = GS / 64;
+        middle = __shfl(rest[t][u / PER & 3], (u / PER >> 2) * 16 + n);
+      }
+      if (NARROW && n >= 4) continue;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<f32x4*>(&so[wave][n][u * 64 + kg * 16 + r * 4]) =
+            f32x4{acc[t][u][0][r], acc[t][u][1][r], acc[t][u][2][r], acc[t][u][3][r]} + middle;
     }
-    if (NARROW && n >= 4) continue;
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      *reinterpret_cast<f32x4*>(&so[wave][n][u * 64 + kg * 16 + r * 4]) =
-          f32x4{acc[u][0][r], acc[u][1][r], acc[u][2][r], acc[u][3][r]} + middle;
-  }
-  if (kg == 0) sml[wave][n][0] = mx, sml[wave][n][1] = sum;
-  if (tid < kRows) ends[tid] = {row.token < 0 ? -1 : ((long long)row.token * a.Hq + row.head) * D, row.lo < row.hi};
-  if (any_bad) {
-    // Rare: the groups left out above, to the rows that see them.
-    for (int c = c0 + wave; c < c1; c += kWaves) {
-      if (seen_by_all(c)) continue;
-      const uint32_t here = token_block(c);
-      for (int key = 0; key < kChunk; ++key) {
-        const int j = c * kChunk + key;
-        const uint16_t* params = reinterpret_cast<const uint16_t*>(v_cache + (size_t)__shfl(here, key >> 3) * BLOCK + 4 * D) + (key & 7);
-        if (j < row.lo || j >= row.hi) continue;
-        for (int g = kg; g < G; g += 4)
-          if (not_finite<false>(params[g * 16]) || not_finite<false>(params[g * 16 + 8]))
-            for (int d = 0; d < GS; ++d) so[wave][n][g * GS + d] = NAN;
+    if (kg == 0) sml[wave][n][0] = mx[t], sml[wave][n][1] = sum;
+    if (tid < kRows) ends[tid] = {row[t].token < 0 ? -1 : ((long long)row[t].token * a.Hq + row[t].head) * D, row[t].lo < row[t].hi};
+    if (any_bad) {
+      // Rare: the groups left out above, to the rows that see them.
+      for (int c = c0 + wave; c < c1; c += kWaves) {
+        if (seen_by_all(c)) continue;
+        const uint32_t here = token_block(c);
+        for (int key = 0; key < kChunk; ++key) {
+          const int j = c * kChunk + key;
+          const uint16_t* params = reinterpret_cast<const uint16_t*>(v_cache + (size_t)__shfl(here, key >> 3) * BLOCK + 4 * D) + (key & 7);
+          if (j < row[t].lo || j >= row[t].hi) continue;
+          for (int g = kg; g < G; g += 4)
+            if (not_finite<false>(params[g * 16]) || not_finite<false>(params[g * 16 + 8]))
+              for (int d = 0; d < GS; ++d) so[wave][n][g * GS + d] = NAN;
+        }
       }
     }
-  }
-  __syncthreads();
-  // Thread: row tid / 16, D / 16 neighbouring dimensions.
-  const auto pack = [=](float x, float y) { return bf16_data ? pack_pair<true>(x, y) : pack_pair<false>(x, y); };
-  constexpr int E = D / 16;
-  const int r = tid >> 4, d0 = (tid & 15) * E, rows = min(rows_left, kRows);
-  float m = -INFINITY, l = 0, o[E] = {};
-  if (r < rows) {
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) m = fmaxf(m, sml[w][r][0]);
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float f = sml[w][r][0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(sml[w][r][0] - m);
-      l += sml[w][r][1] * f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] += so[w][r][d0 + e] * f;
-    }
-  }
-  if (share.parts > 1) {
+    __syncthreads();
+    // Thread: row tid / 16, D / 16 neighbouring dimensions.
+    const auto pack = [=](float x, float y) { return bf16_data ? pack_pair<true>(x, y) : pack_pair<false>(x, y); };
+    constexpr int E = D / 16;
+    const int r = tid >> 4, d0 = (tid & 15) * E, rows = min(rows_left - t * kRows, kRows);
+    float m = -INFINITY, l = 0, o[E] = {};
     if (r < rows) {
-      // A thread's pairs lie 256 pairs apart: the threads of a store write whole lines.
-      float* to = p.part + (size_t)blockIdx.x * kRows * D + 2 * tid;
 #pragma unroll
-      for (int e = 0; e < E; e += 2) handoff_store(to + e * 256, o[e], o[e + 1]);
-      if ((tid & 15) == 0) handoff_store(p.part_ml + ((size_t)blockIdx.x * kRows + r) * 2, m, l);
+      for (int w = 0; w < kWaves; ++w) m = fmaxf(m, sml[w][r][0]);
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = sml[w][r][0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(sml[w][r][0] - m);
+        l += sml[w][r][1] * f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += so[w][r][d0 + e] * f;
+      }
     }
-    const size_t tile = ((size_t)b * a.Hkv + hk) * p.rtiles + rt;
-    if (handoff_last(&p.counters[tile], (uint32_t)share.parts, &s_last)) join_parts<D>(k, share, ends, rows, shared, pack);
-    return;
-  }
-  if (r >= rows) return;
-  const float inv = ends[r].some ? 1 / l : 0.f;
-  uint16_t* dst = a.out + ends[r].at + d0;
+    if (RT == 1 && share.parts > 1) {
+      if (r < rows) {
+        // A thread's pairs lie 256 pairs apart: the threads of a store write whole lines.
+        float* to = p.part + (size_t)blockIdx.x * kRows * D + 2 * tid;
 #pragma unroll
-  for (int e = 0; e < E; e += 4)
-    *reinterpret_cast<u32x2*>(dst + e) = u32x2{pack(o[e] * inv, o[e + 1] * inv), pack(o[e + 2] * inv, o[e + 3] * inv)};
+        for (int e = 0; e < E; e += 2) handoff_store(to + e * 256, o[e], o[e + 1]);
+        if ((tid & 15) == 0) handoff_store(p.part_ml + ((size_t)blockIdx.x * kRows + r) * 2, m, l);
+      }
+      const size_t tile = ((size_t)b * a.Hkv + hk) * p.rtiles + rt;
+      if (handoff_last(&p.counters[tile], (uint32_t)share.parts, &s_last)) join_parts<D>(k, share, ends, rows, shared, pack);
+      return;
+    }
+    if (r >= rows) continue;
+    const float inv = ends[r].some ? 1 / l : 0.f;
+    uint16_t* dst = a.out + ends[r].at + d0;
+#pragma unroll
+    for (int e = 0; e < E; e += 4)
+      *reinterpret_cast<u32x2*>(dst + e) = u32x2{pack(o[e] * inv, o[e + 1] * inv), pack(o[e + 2] * inv, o[e + 3] * inv)};
+  }
 }
 
 template <int D, int G>
@@ -660,8 +694,9 @@ hipError_t launch_split(const AttentionArgs& a, bool bf16, hipStream_t stream) {
     p.r.part_ml = p.r.part + plan.blocks * kRows * D;
   }
   const dim3 grid((unsigned)plan.blocks);
-  if ((long long)a.max_q * plan.group <= 4) kv4_split_kernel<D, G, true><<<grid, 64 * kWaves, 0, stream>>>(p);
-  else kv4_split_kernel<D, G, false><<<grid, 64 * kWaves, 0, stream>>>(p);
+  if ((long long)a.max_q * plan.group <= 4) kv4_split_kernel<D, G, true, 1><<<grid, 64 * kWaves, 0, stream>>>(p);
+  else if (!plan.wide) kv4_split_kernel<D, G, false, 1><<<grid, 64 * kWaves, 0, stream>>>(p);
+  else if constexpr (D <= 128) kv4_split_kernel<D, G, false, 2><<<grid, 64 * kWaves, 0, stream>>>(p);
   return hipGetLastError();
 }
 
