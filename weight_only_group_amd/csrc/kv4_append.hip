@@ -56,6 +56,8 @@ struct AppendKernelArgs {
   AppendArgs a;
   FixedDiv by_page;
   int groups;
+  FixedDiv by_heads;
+  int chunk_shift;               // log2 of a head's threads
   int group_lanes, group_shift;  // lanes per group; log2 of it
   unsigned xcds;
 };
@@ -68,16 +70,13 @@ struct AppendKernelArgs {
 template <bool BF, bool ADJ>
 __global__ void __launch_bounds__(256) kv4_append_kernel(AppendKernelArgs p) {
   const AppendArgs& a = p.a;
-  const int chunks = a.D / 8;
-  const int heads = a.Hq + 2 * a.Hkv;
+  const int chunks = 1 << p.chunk_shift;
   // Neighbouring tokens on one XCD (blocks go round them), whose L2 then holds a block of the cache whole.
   const unsigned block_i = blockIdx.x % p.xcds * (gridDim.x / p.xcds) + blockIdx.x / p.xcds;
-  const long long i = (long long)block_i * 256 + threadIdx.x;
-  const int c = (int)(i % chunks);
-  const long long th = i / chunks;
-  const int h = (int)(th % heads);
-  const long long t = th / heads;
-  if (t >= a.T) return;
+  const int i = (int)(block_i * 256 + threadIdx.x);  // (below 2^31: three times T Hq D / 8 at most)
+  const int c = i & (chunks - 1), th = i >> p.chunk_shift, token = p.by_heads(th), h = th - token * (a.Hq + 2 * a.Hkv);
+  if (token >= a.T) return;
+  const long long t = token;
 
   const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
   const uint16_t* src;
@@ -170,7 +169,7 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(AppendKernelArgs p) {
 struct GatherKernelArgs {
   Kv4GatherArgs a;
   FixedDiv by_page;
-  int group_shift;  // log2 of a group's threads
+  int chunk_shift, group_shift;  // log2 of a head's threads and of a group's
 };
 
 // Eight values of a token per thread, of HEADS heads: blockIdx.y tells which, of the keys, then the values. Bound by memory,
@@ -180,10 +179,10 @@ struct GatherKernelArgs {
 template <bool BF, int HEADS>
 __global__ void __launch_bounds__(256) kv4_gather_kernel(GatherKernelArgs p) {
   const Kv4GatherArgs& a = p.a;
-  const int chunks = a.D / 8;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  const int c = (int)(i % chunks);
-  const long long t = i / chunks;
+  const int chunks = 1 << p.chunk_shift;
+  const unsigned i = blockIdx.x * 256 + threadIdx.x;
+  const int c = i & (chunks - 1);
+  const long long t = i >> p.chunk_shift;
   if (t >= a.T) return;
   const int parts = (a.Hkv + HEADS - 1) / HEADS;
   const bool is_v = (int)blockIdx.y >= parts;
@@ -252,7 +251,7 @@ hipError_t launch_kv4_append(const AppendArgs& a, int group_size, bool bf16, boo
   const long long n = (long long)a.T * (a.Hq + 2 * a.Hkv) * (a.D / 8);
   const int xcds = device_topology().xcds;
   const dim3 grid((unsigned)((n + 256 * xcds - 1) / (256 * xcds) * xcds));
-  const AppendKernelArgs p = {a, fixed_div(a.page_size), a.D / group_size, group_size / 8, log2_of(group_size / 8), (unsigned)xcds};
+  const AppendKernelArgs p = {a, fixed_div(a.page_size), a.D / group_size, fixed_div(a.Hq + 2 * a.Hkv), log2_of(a.D / 8), group_size / 8, log2_of(group_size / 8), (unsigned)xcds};
   if (bf16 && adjacent) kv4_append_kernel<true, true><<<grid, 256, 0, stream>>>(p);
   else if (bf16) kv4_append_kernel<true, false><<<grid, 256, 0, stream>>>(p);
   else if (adjacent) kv4_append_kernel<false, true><<<grid, 256, 0, stream>>>(p);
@@ -261,7 +260,7 @@ hipError_t launch_kv4_append(const AppendArgs& a, int group_size, bool bf16, boo
 }
 
 hipError_t launch_kv4_gather(const Kv4GatherArgs& a, bool bf16, hipStream_t stream) {
-  const GatherKernelArgs p = {a, fixed_div(a.page_size), log2_of(a.group_size / 8)};
+  const GatherKernelArgs p = {a, fixed_div(a.page_size), log2_of(a.D / 8), log2_of(a.group_size / 8)};
   const bool many = (long long)a.T * 2 * a.Hkv * (a.D / 8) > 32ll * 64 * device_topology().cus;
   if (many) bf16 ? launch_gather_heads<true, 2>(p, stream) : launch_gather_heads<false, 2>(p, stream);
   else bf16 ? launch_gather_heads<true, 1>(p, stream) : launch_gather_heads<false, 1>(p, stream);
