@@ -169,3 +169,33 @@ def test_copies_past_32_bits(w):  # noqa: F811
     for old, data in ((pages - 2, x[0]), (8, x[1]), (3, x[0])):
         assert torch.equal(cache[int(moved_to[old])], data) and int(moved_to[old]) < 3
     assert torch.equal(new[0], moved_to[torch.tensor([pages - 2, 8, 3], device=DEV)])
+
+
+@pytest.mark.parametrize("kind", ["halves", "normal", "turned"])
+def test_codes_of_many_values(w, kind):  # noqa: F811
+    """Scales of every mantissa that 8 bits have, and values half way between codes and next to that: the codes are the
+    definition's, bit for bit."""
+    D, group, page, T, Hkv = 128, 64, 64, 1016, 4
+    r = np.random.default_rng(5)
+    if kind == "halves":
+        step = 2.0 ** r.integers(-9, 3, (T, Hkv, 1)) * (1 + np.arange(T)[:, None, None] % 127)
+        x = np.minimum(step * r.integers(0, 31, (T, Hkv, D)) / 2 * (1 + r.integers(-1, 2, (T, Hkv, D)) * 2.0**-11), 15 * step)
+        x[..., ::64], x[..., 1::64] = 0, 15 * step
+        x *= r.choice([-1.0, 1.0], (T, Hkv, 1))
+    else:
+        x = r.standard_normal((T, Hkv, D)) * 10.0 ** r.integers(-5, 4, (T, Hkv, 1)) + r.standard_normal((T, Hkv, 1))
+    k = torch.from_numpy(x.astype(np.float16)).to(DEV)
+    q = randn((T, Hkv, D), "fp16", 1)
+    angle = r.uniform(0, 6.28, (T, D // 2))
+    turn = [torch.from_numpy(f(angle).astype(np.float32)).to(DEV) for f in (np.cos, np.sin)] if kind == "turned" else [None, None]
+    caches = [torch.zeros((T // page + 1, Hkv, w.kv4_page_bytes(page, D, group)), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    w.qmm_kv4_append(q, k, k, *turn, i32(np.arange(T)) if kind == "turned" else None, torch.arange(T, device=DEV), *caches, group)
+    for cache, keys in zip(caches, (True, False)):
+        want = f64(k)
+        if keys and kind == "turned":
+            (a, b), (c, s) = np.split(want, 2, -1), (f64(t)[:, None] for t in turn)
+            want = np.concatenate([a * c - b * s, b * c + a * s], -1)
+        s, m, c = co.quantise(want, group)
+        got = [t.transpose(0, 2, 1, 3).reshape(-1, Hkv, D)[:T] for t in co.parts(cache.cpu().numpy(), D, group, keys)]
+        s, m = (np.repeat(t.astype(np.float64), group, -1) for t in (s, m))
+        assert np.array_equal(got[0], s * (c - 8)) and np.array_equal(got[1], m), keys

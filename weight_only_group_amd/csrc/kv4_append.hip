@@ -39,10 +39,16 @@ __device__ __forceinline__ Quantised quantise(float (&x)[8], int lanes) {
   const float s = (float)r.s;
   r.m = (f16)(lo + 8 * s);
   const float m = (float)r.m;
+  // rint(d / s) without the division's own steps: `near` is within two units of the quotient's last place, so
+  // that (s has 8 bits) d - near s is exact, and `quotient` is d / s to 2^-21 of a unit, rounded. Where d / s is no half-integer itself
+  // it differs from one by d's unit over s, more than half a unit of its own by a part in 2^8 (s < 2 - 2^-7 times its
+  // power of two): both are rounded to the same integer.
+  const float inverse = __builtin_amdgcn_rcpf(s);
   r.codes = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float c = s > 0 ? fminf(fmaxf(rintf((x[e] - m) / s), -8.f), 7.f) : 0.f;
+    const float d = x[e] - m, near = d * inverse, quotient = fmaf(fmaf(-near, s, d), inverse, near);
+    const float c = s > 0 ? fminf(fmaxf(rintf(quotient), -8.f), 7.f) : 0.f;
     r.codes |= (uint32_t)((int)c + 8) << (4 * e);
   }
   if (nan) {
@@ -63,10 +69,11 @@ struct AppendKernelArgs {
 };
 
 // Eight values of one head per thread. A thread of a rotated half loads its partner's
-// eight values too: a group's values then lie in neighbouring lanes. Bound by memory: 16381 tokens (24 heads of 64 over 4,
-// 124 MB in all) take 29.6 us, 4.2 TB/s; the queries alone 19.8 us, 5.1 TB/s, and the rest is the scattered writes of the
-// codes, two or four bytes each. (Neighbouring tokens on different XCDs: 30.8 us. Threads of two and four heads, which load
-// a token's angles and slot once: 31.0 and 34.8 us, and 7 tokens 5.4 and 7.8 us for 4.1.)
+// eight values too: a group's values then lie in neighbouring lanes. 16381 tokens (24 heads of 64 over 4,
+// 118 MB in all) take 26.7 us, 4.4 TB/s. The queries alone reach 5.1 TB/s; keys and values wait for the vector ALUs too
+// (rotation in fp64, codes), with plain divisions 28.2 us, with indices in 64 bits 31.2 us. (Neighbouring tokens on different XCDs: 30.8
+// us for 29.6. Threads of two and four heads, which load a token's angles and slot once: 31.0 and 34.8 us for 30.8, and 7
+// tokens 5.4 and 7.8 us for 4.1.)
 template <bool BF, bool ADJ>
 __global__ void __launch_bounds__(256) kv4_append_kernel(AppendKernelArgs p) {
   const AppendArgs& a = p.a;
