@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
     else return (c >> 1) * 256 + (((c ^ c >> 4) & 1) * 8 + (blk ^ (c >> 1 & 7))) * 16;
   };
   auto seen_by_whole_block = [&](int step) {
-    return step * BN >= block_all_lo && (uint32_t)(step + 1) * BN <= (uint32_t)block_all_hi;
+    return (uint32_t)step * BN >= (uint32_t)block_all_lo && (uint32_t)(step + 1) * BN <= (uint32_t)block_all_hi;
   };
   // Before the decoding. Tokens that no row sees may hold anything: their scales and middles count as 0. So
   // do those of a seen one that are not finite, as they must not reach the rows that do not see it (0 times NaN
@@ -206,11 +206,11 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
     uint32_t bad = 0;
 #pragma unroll
     for (int i = 0; i < VU; ++i) {
-      const int j0 = step * BN + 8 * blk_of(i) + 4 * (unit_of(i) & 1);
+      const uint32_t j0 = (uint32_t)step * BN + 8 * blk_of(i) + 4 * (unit_of(i) & 1);  // (a step asked for ahead may begin at 2^31)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int j = j0 + 2 * x;
-        const uint32_t in = (j >= block_lo && j < block_hi ? 0xFFFFu : 0u) | (j + 1 >= block_lo && j + 1 < block_hi ? 0xFFFF0000u : 0u);
+        const uint32_t j = j0 + 2 * x, lo = block_lo, hi = block_hi;
+        const uint32_t in = (j >= lo && j < hi ? 0xFFFFu : 0u) | (j + 1 >= lo && j + 1 < hi ? 0xFFFF0000u : 0u);
         const uint32_t nf = (not_finite_halves(vs[i][x]) | not_finite_halves(vm[i][x])) & in;
         bad |= nf;
         vs[i][x] &= in & ~nf;
