@@ -56,7 +56,8 @@ def launches(path):
             group = taken[j::n]
             kernel = group[0][0]["Kernel_Name"]
             assert all(g[0]["Kernel_Name"] == kernel for g in group), case["name"]
-            yield case["name"], re.sub(r"void |qmm::|\(anonymous namespace\)::|\(qmm::.*Args\)|\(\w+Args\)", "", kernel), group
+            short = kernel.replace("void ", "").replace("(anonymous namespace)::", "").replace("qmm::", "")
+            yield case["name"], re.sub(r"\(\w+Args\)$", "", short), group
     if left:
         sys.exit(f"{path}: {len(left)} launches more than the cases make")
 
@@ -67,7 +68,7 @@ def times(path):
     for name, kernel, group in launches(path):
         t = sorted((int(g[0]["End_Timestamp"]) - int(g[0]["Start_Timestamp"])) / 1e3 for g in group)
         r = group[0][0]
-        print(f"{name:20s} {kernel:42s} grid {r['Grid_Size_X']}x{r['Grid_Size_Y']} vgpr {r['VGPR_Count']} lds {r['LDS_Block_Size']} "
+        print(f"{name:20s} {kernel:44s} grid {r['Grid_Size_X']}x{r['Grid_Size_Y']} vgpr {r['VGPR_Count']} lds {r['LDS_Block_Size']} "
               f"scratch {r['Scratch_Size']} n={len(t)} min {t[0]:.2f} med {statistics.median(t):.2f} max {t[-1]:.2f}")
 
 
