@@ -21,6 +21,8 @@ def run(w, kv_lens, q_lens, Hq, Hkv, D, page, group, dtype, seed=1, fill=None, v
         q = randn((T, (Hq + 3) * D), dtype, seed + 1, q_scale)[:, D:(Hq + 1) * D].unflatten(1, (Hq, D))
     else:
         q = randn((T, Hq, D), dtype, seed + 1, q_scale)
+    if max_kv and max_kv > table.shape[1] * page:
+        table = np.pad(table, ((0, 0), (0, -(-max_kv // page) - table.shape[1])))
     starts = np.concatenate([[0], np.cumsum(q_lens)])
     dev = {n: (torch.from_numpy(a).float().to(DEV) if n == "slopes" else i32(a)) if isinstance(a, np.ndarray) else a
            for n, a in kw.items()}

@@ -206,3 +206,22 @@ def test_large_cache_offsets(w):  # noqa: F811
     rest = (i32(np.array([n])), i32(np.array([0, n])), n, n, group)
     out = w.qmm_kv4_attention(q, k, v, i32(np.array([[pages - 1, pages - 2]])), *rest)
     assert torch.equal(out, w.qmm_kv4_attention(q, *last, i32(np.array([[1, 0]])), *rest)) and out.any()
+
+
+@pytest.mark.parametrize("D,group", KINDS)
+def test_infinite_middles_that_all_see(w, D, group):  # noqa: F811
+    """Such a group stands for NaN, in blocks and where each sequence has few rows."""
+    Hq, Hkv, n, page = 336, 168, 200, 8
+    k, v, table = paged4([n], Hkv, D, page, group, 1)
+    for cache, head, keys, sign in ((k, 0, True, 1), (k, 1, True, -1), (v, 2, False, 1), (v, 3, False, -1)):
+        at = co.scale_places(5, 0, D, group, keys)[1]
+        cache[table[0, 0], head].reshape(1, -1)[0, at:at + 2] = np.frombuffer(np.float16(sign * np.inf).tobytes(), np.uint8)
+    some = np.r_[0:8, 20]
+    part = lambda c, keys: [x[:, [0, 1, 2, 3, 10]] for x in co.parts(c, D, group, keys)]  # noqa: E731
+    for T in (100, 3):
+        assert in_blocks(w, 1, T, Hq, Hkv, D, T, n) or T == 3
+        q = randn((T, Hq, D), "fp16", 2)
+        got = w.qmm_kv4_attention(q, device(k), device(v), i32(table), i32(np.array([n])), i32(np.array([0, T])), T, n, group)
+        assert torch.isfinite(got[:, 8:]).all()
+        want, bound = co.attention(f64(q)[:, np.r_[0:8, 20, 21]], part(k, True), part(v, False), table, [n], [0, T], D**-0.5, group)
+        check(got[:, some], want[:, :9], bound[:, :9], f"T={T}")

@@ -25,6 +25,13 @@ namespace {
 // kept times 2^kLift, so that they pass neither end of fp16.
 constexpr float kLift = 7.f, kSlack = 8.f;
 
+// Two middles, infinite ones as NaN (what such a group stands for): an infinity alone would give infinite
+// sums, and a weight of 0 to the key whose score is minus infinity.
+__device__ __forceinline__ uint32_t infinite_as_nan(uint32_t m) {
+  const f16x2 v = as_f16x2(m), zero = {(f16)0.f, (f16)0.f};
+  return as_u32(__builtin_elementwise_fma(v, zero, v));
+}
+
 // The AND's and the OR's constant, in registers: as literals they would take an instruction each.
 struct DecodeMasks {
   uint32_t code, sixteen;

@@ -80,13 +80,16 @@ __device__ __forceinline__ float max_of_rows(float v) {
 // take 10 us. With c chunks a part, sum ceil(chunks / c) is at most sum chunks / c + tiles, so c =
 // sum chunks / parts gives no more blocks than parts + tiles; smaller ones are tried first.
 // A sequence's chunks are those of its first and last query.
-// Beyond kMostTiles tiles there are enough for one part each; of sequences of 17 to 128 rows half of them (longer
-// ones' last tiles see the most keys: in parts two or three prompts of 2000 to 3000 rows take 0.3 to 0.5 of the time).
-// Of several tiles a block then takes two, so that its keys and values are decoded once for both: against parts, sequences
-// of 17 to 32 rows in 2049 to 4096 tiles 1.5 times as fast (one tile a block: 1.2), of 65 to 128 rows 1.15 (1.07);
-// against one tile a block, in more tiles 1.25 and 1.03 to 1.1. D 256 has no registers for it (0.6 to 1.1).
+// One part each where that is faster: a share, its hand-over and the join cost 5 us and more a block, against the time of
+// the longest tile alone. Measured, the time in parts over that without, single tokens: up to 16 tiles of D 64, 128 and 256 on 400 keys
+// 1.35, 1.3 and 1.15, on 1000 1.3, 1.1 and 0.9, on 3000 0.8, 0.7 and 0.55; 256 to 4096 tiles on less than four keys
+// a tile 1.1 to 6, and where one sequence among short ones has eight keys a tile 0.5 to 0.9. Sequences of more than 128
+// rows are split up to kMostTiles tiles: their last ones see the most keys (two or three prompts of 2000 to 3000 rows
+// take 0.3 to 0.5 of the time in parts).
+// Of several tiles of a sequence a block then takes two, so that its keys and values are decoded once for both: against one
+// tile a block 1.2 to 1.25 times as fast with 17 to 32 rows, 1.03 to 1.1 with 65 to 128. D 256 has no registers for it (0.6).
 constexpr int kMostSequences = 1024;  // of a split launch
-constexpr int kMostTiles = 4096;
+constexpr int kMostTiles = 4096, kPartsFrom = 192 * 1024;  // keys, with D: 1536, 1024, 614
 constexpr int kMostParts = 256;       // of a tile
 constexpr int kLeastChunks = kWaves;  // of a part
 
@@ -108,7 +111,9 @@ Kv4Plan kv4_plan(int B, int Hq, int Hkv, int D, int max_q, int max_kv, DeviceTop
   p.fit = resident_blocks(D, topo);
   p.parts = 0;
   const long long rows = (long long)max_q * p.group;
-  if (B <= kMostSequences && tiles <= (rows > kRows && rows <= 8 * kRows ? kMostTiles / 2 : kMostTiles) && max_kv > kLeastChunks * kChunk) p.parts = (int)std::max(p.fit - tiles, p.fit / 2ll);
+  const bool worth_it = max_kv > kPartsFrom / (D + 64) && (rows > 8 * kRows || max_kv > 4 * tiles);
+  if (B <= kMostSequences && tiles <= kMostTiles && worth_it)
+    p.parts = (int)std::max(p.fit - tiles, p.fit / 2ll);
   const long long most = ((long long)max_kv + kLeastChunks * kChunk - 1) / (kLeastChunks * kChunk);
   p.wide = rows > kRows && !p.parts && D <= 128;
   if (p.wide) p.rtiles = row_tiles(max_q, p.group, 2 * kRows);
@@ -460,10 +465,10 @@ __global__ void __launch_bounds__(256, D == 256 || (D == 128 && RT == 2) ? 2 : 3
       // Halves [s of all groups][m of all groups].
       u32x4 middles = {0, 0, 0, 0};
       if constexpr (G == 1) {
-        middles[0] = kp[t][0] >> 16;
+        middles[0] = infinite_as_nan(kp[t][0] >> 16);
       } else {
 #pragma unroll
-        for (int x = 0; x < G / 2; ++x) middles[x] = kp[t][G / 2 + x];
+        for (int x = 0; x < G / 2; ++x) middles[x] = infinite_as_nan(kp[t][G / 2 + x]);
       }
 #pragma unroll
       for (int r = 0; r < RT; ++r) st[r][t] = mfma16<false>(middles, qsum[r], st[r][t]);
@@ -623,6 +628,7 @@ __global__ void __launch_bounds__(256, D == 256 || (D == 128 && RT == 2) ? 2 : 3
         constexpr int PER = GS / 64;
         middle = __shfl(rest[t][u / PER & 3], (u / PER >> 2) * 16 + n);
       }
+      if (fabsf(middle) == INFINITY) middle = NAN;  // (from a group of infinite middle)
       if (NARROW && n >= 4) continue;
 #pragma unroll
       for (int r = 0; r < 4; ++r)

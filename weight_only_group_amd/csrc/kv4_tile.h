@@ -224,17 +224,17 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
     if (word0 == 0) {
       u32x4 middles = {0, 0, 0, 0};
       if constexpr (G == 1) {
-        middles[0] = kp[0] >> 16;
+        middles[0] = infinite_as_nan(kp[0] >> 16);
       } else {
 #pragma unroll
-        for (int x = 0; x < G / 2; ++x) middles[x] = kp[G / 2 + x];
+        for (int x = 0; x < G / 2; ++x) middles[x] = infinite_as_nan(kp[G / 2 + x]);
       }
       *reinterpret_cast<u32x4*>(lds + k_to + TILE + key * 16) = middles;
     }
 #pragma unroll
     for (int i = 0; i < VU; ++i)
       if (quad_of(i) * 4 % GS == 0 && !no_values)
-        *reinterpret_cast<u32x2*>(lds + v_to + TILE + quad_of(i) * 4 / GS * VM_ROW + blk_of(i) * 16 + (unit_of(i) & 1) * 8) = u32x2{vm[i][0], vm[i][1]};
+        *reinterpret_cast<u32x2*>(lds + v_to + TILE + quad_of(i) * 4 / GS * VM_ROW + blk_of(i) * 16 + (unit_of(i) & 1) * 8) = u32x2{infinite_as_nan(vm[i][0]), infinite_as_nan(vm[i][1])};
   };
   // The decoding in slices: the key's words, then four channels of each unit.
   constexpr int SLICES = KW + 4 * VU;
