@@ -84,8 +84,8 @@ __device__ __forceinline__ float max_of_rows(float v) {
 // the longest tile alone. Measured, the time in parts over that without, single tokens: up to 16 tiles of D 64, 128 and 256 on 400 keys
 // 1.35, 1.3 and 1.15, on 1000 1.3, 1.1 and 0.9, on 3000 0.8, 0.7 and 0.55; 256 to 4096 tiles on less than four keys
 // a tile 1.1 to 6, and where one sequence among short ones has eight keys a tile 0.5 to 0.9. Sequences of more than 128
-// rows are split up to kMostTiles tiles: their last ones see the most keys (two or three prompts of 2000 to 3000 rows
-// take 0.3 to 0.5 of the time in parts).
+// rows are split up to kMostTiles tiles and from half as many keys on: their last ones see the most keys (two or three
+// prompts of 2000 to 3000 rows take 0.3 to 0.5 of the time in parts, of 1000 0.6 to 0.7; of 300 3 times as long).
 // Of several tiles of a sequence a block then takes two, so that its keys and values are decoded once for both: against one
 // tile a block 1.2 to 1.25 times as fast with 17 to 32 rows, 1.03 to 1.1 with 65 to 128. D 256 has no registers for it (0.6).
 constexpr int kMostSequences = 1024;  // of a split launch
@@ -111,7 +111,8 @@ Kv4Plan kv4_plan(int B, int Hq, int Hkv, int D, int max_q, int max_kv, DeviceTop
   p.fit = resident_blocks(D, topo);
   p.parts = 0;
   const long long rows = (long long)max_q * p.group;
-  const bool worth_it = max_kv > kPartsFrom / (D + 64) && (rows > 8 * kRows || max_kv > 4 * tiles);
+  const bool prompts = rows > 8 * kRows;
+  const bool worth_it = max_kv > kPartsFrom / (D + 64) / (prompts ? 2 : 1) && (prompts || max_kv > 4 * tiles);
   if (B <= kMostSequences && tiles <= kMostTiles && worth_it)
     p.parts = (int)std::max(p.fit - tiles, p.fit / 2ll);
   const long long most = ((long long)max_kv + kLeastChunks * kChunk - 1) / (kLeastChunks * kChunk);
