@@ -15,8 +15,9 @@
  * a middle m, both fp16 (s with at most 8 significant bits, so that s times a
  * code's distance from 8 is exact in fp16), and code c of it stands for
  *   m + s (c - 8)
- * A group whose s or m is not finite stands for NaN. The format is the same
- * for fp16 and bf16 queries. A head's tokens of a page lie in blocks of eight
+ * A group whose s or m is not finite, or whose s is beyond +-QMM_KV4_LARGEST_SCALE
+ * (24 s is then no fp16 number; qmm_kv4_append gives 2192 at most), stands for NaN. The
+ * format is the same for fp16 and bf16 queries. A head's tokens of a page lie in blocks of eight
  * tokens, one behind another, each of 4 D + 32 D / group_size bytes:
  *   keys:   codes (8 tokens, D / 8 words), then fp16 (8 tokens, [s, m], groups);
  *           word (D / 32) g + i of a token (little-endian, 0 <= g < 4) has channels
@@ -36,7 +37,8 @@
 extern "C" {
 #endif
 
-#define QMM_KV4_LARGEST 16384 /* keys and values are cut to +-16384 */
+#define QMM_KV4_LARGEST 16384      /* keys and values are cut to +-16384 */
+#define QMM_KV4_LARGEST_SCALE 2728 /* of a group that stands for numbers */
 
 /* Bytes of one head of a page: page_size (D / 2 + 4 D / group_size); 0 for arguments that no call takes. */
 size_t qmm_kv4_page_bytes(int page_size, int D, int group_size);

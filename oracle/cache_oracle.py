@@ -7,7 +7,7 @@ import numpy as np
 from .layer_oracle import F32, ROUNDOFF, TINY, rotate
 from .qmm_oracle import bf16_to_f64, f64_to_bf16
 
-LARGEST = 16384.0
+LARGEST, LARGEST_SCALE = 16384.0, 2728.0
 BLOCK = 8  # tokens of a head that lie interleaved
 
 
@@ -68,7 +68,8 @@ def put(cache, page, head, at, s, m, c, group, keys):
 
 
 def parts(cache, D, group, keys):
-    """(pages, Hkv, page_size, D) float64: s (c - 8) and m of every channel; NaN in both where either is not finite."""
+    """(pages, Hkv, page_size, D) float64: s (c - 8) and m of every channel; NaN in both where either
+    is not finite or the scale is too large."""
     pages, heads, size = cache.shape
     blocks = cache.reshape(pages, heads, -1, block_bytes(D, group))
     step, middle = (np.zeros((pages, heads, blocks.shape[2], BLOCK, D)) for _ in range(2))
@@ -76,7 +77,7 @@ def parts(cache, D, group, keys):
         for g in range(D // group):
             s, m = (np.ascontiguousarray(blocks[..., p:p + 2]).view(np.float16)[..., 0].astype(np.float64)
                     for p in scale_places(t, g, D, group, keys))
-            bad = ~(np.isfinite(s) & np.isfinite(m))
+            bad = ~((np.abs(s) <= LARGEST_SCALE) & np.isfinite(m))
             s, m = np.where(bad, np.nan, s), np.where(bad, np.nan, m)
             for d in range(g * group, (g + 1) * group):
                 byte, half = (key_place if keys else value_place)(t, d, D)

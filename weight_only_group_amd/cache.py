@@ -24,6 +24,7 @@ from .layer import QMM_ADJACENT, QMM_BF16, _array, _heads, _launch, _p, _result
 
 GROUPS = (32, 64, 128)
 LARGEST = 16384  # keys and values are cut to this size
+LARGEST_SCALE = 2728  # a group whose scale is beyond it stands for NaN
 
 # Every symbol qmm_cache.h declares.
 EXPORTS = (

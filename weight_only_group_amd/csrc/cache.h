@@ -12,6 +12,9 @@ constexpr int kBlockTokens = 8;  // tokens of a head that lie interleaved
 __host__ __device__ constexpr int kv4_block_bytes(int D, int groups) { return 4 * D + 32 * groups; }
 
 constexpr int kKv4Largest = 16384;
+// A group of a larger scale (or of an infinite one) stands for NaN: 24 s, which the attention decodes with, is no fp16
+// number beyond it.
+constexpr int kKv4LargestScale = 2728;
 // In AppendArgs and AttentionArgs the caches' pointers stand for bytes.
 hipError_t launch_kv4_append(const AppendArgs& a, int group_size, bool bf16, bool adjacent, hipStream_t stream);
 

@@ -46,7 +46,7 @@ qmm_status check_pools(void* const* caches, const int64_t* page_bytes, int n_cac
 
 }  // namespace
 
-static_assert(QMM_KV4_LARGEST == qmm::kKv4Largest, "the limit of the kernels");
+static_assert(QMM_KV4_LARGEST == qmm::kKv4Largest && QMM_KV4_LARGEST_SCALE == qmm::kKv4LargestScale, "the limits of the kernels");
 
 extern "C" {
 

@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(GatherKernelArgs p) {
 #pragma unroll
   for (int h = 0; h < HEADS; ++h) {
     float sh = (float)s[h], mh = (float)m[h];
-    if (!(fabsf(sh) < INFINITY) || !(fabsf(mh) < INFINITY)) sh = mh = NAN;
+    if (!(fabsf(sh) <= kKv4LargestScale) || !(fabsf(mh) < INFINITY)) sh = mh = NAN;
     u32x4 out;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {

@@ -25,13 +25,6 @@ namespace {
 // kept times 2^kLift, so that they pass neither end of fp16.
 constexpr float kLift = 7.f, kSlack = 8.f;
 
-// Two middles, infinite ones as NaN (what such a group stands for): an infinity alone would give infinite
-// sums, and a weight of 0 to the key whose score is minus infinity.
-__device__ __forceinline__ uint32_t infinite_as_nan(uint32_t m) {
-  const f16x2 v = as_f16x2(m), zero = {(f16)0.f, (f16)0.f};
-  return as_u32(__builtin_elementwise_fma(v, zero, v));
-}
-
 // The AND's and the OR's constant, in registers: as literals they would take an instruction each.
 struct DecodeMasks {
   uint32_t code, sixteen;
@@ -47,11 +40,28 @@ __device__ __forceinline__ uint32_t decode(uint32_t w, f16x2 s, f16x2 c24, const
   const uint32_t at = R == 0 ? w << 6 : R == 1 ? w << 2 : R == 2 ? w >> 2 : w >> 6;
   return as_u32(__builtin_elementwise_fma(as_f16x2((at & k.code) | k.sixteen), s, c24));
 }
-__device__ __forceinline__ f16x2 times_24(f16x2 s) { return s * f16x2{(f16)-24.f, (f16)-24.f}; }  // exact: 10 bits
+// Exact (10 bits) up to kKv4LargestScale, and beyond it infinite, as every code of the group then is.
+__device__ __forceinline__ f16x2 times_24(f16x2 s) { return s * f16x2{(f16)-24.f, (f16)-24.f}; }
 
-// Whether a half of the pair is an infinity or a NaN, as a mask of those halves.
-__device__ __forceinline__ uint32_t not_finite_halves(uint32_t v) {
-  return (not_finite<false>(v) ? 0xFFFFu : 0u) | (not_finite<false>(v >> 16) ? 0xFFFF0000u : 0u);
+// Two groups' middles, NaN where the group stands for NaN (the middle is not finite or the scale s too large): an infinity
+// alone would give infinite sums, and a weight of 0 to the key whose score is minus infinity.
+__device__ __forceinline__ uint32_t middles_or_nan(uint32_t m, uint32_t s) {
+  const f16x2 v = as_f16x2(m), none = times_24(as_f16x2(s)) * f16x2{(f16)0.f, (f16)0.f};  // 0 or NaN
+  return as_u32(__builtin_elementwise_fma(v, none, v));
+}
+
+// Whether the low half is no middle, no scale of a group that stands for numbers.
+__device__ __forceinline__ bool bad_middle(uint32_t m) { return not_finite<false>(m); }
+__device__ __forceinline__ bool bad_scale(uint32_t s) {
+  constexpr uint32_t most = __builtin_bit_cast(uint16_t, (f16)kKv4LargestScale);
+  return (s & 0x7FFFu) > most;
+}
+// The same of both halves of a pair, as a mask of the bad ones.
+__device__ __forceinline__ uint32_t bad_middles(uint32_t m) {
+  return (bad_middle(m) ? 0xFFFFu : 0u) | (bad_middle(m >> 16) ? 0xFFFF0000u : 0u);
+}
+__device__ __forceinline__ uint32_t bad_scales(uint32_t s) {
+  return (bad_scale(s) ? 0xFFFFu : 0u) | (bad_scale(s >> 16) ? 0xFFFF0000u : 0u);
 }
 
 // BYTES (a multiple of 4, up to 32) from p as 32-bit words.

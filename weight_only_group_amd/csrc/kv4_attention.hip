@@ -466,10 +466,10 @@ __global__ void __launch_bounds__(256, D == 256 || (D == 128 && RT == 2) ? 2 : 3
       // Halves [s of all groups][m of all groups].
       u32x4 middles = {0, 0, 0, 0};
       if constexpr (G == 1) {
-        middles[0] = infinite_as_nan(kp[t][0] >> 16);
+        middles[0] = middles_or_nan(kp[t][0] >> 16, kp[t][0] & 0xFFFF);
       } else {
 #pragma unroll
-        for (int x = 0; x < G / 2; ++x) middles[x] = infinite_as_nan(kp[t][G / 2 + x]);
+        for (int x = 0; x < G / 2; ++x) middles[x] = middles_or_nan(kp[t][G / 2 + x], kp[t][x]);
       }
 #pragma unroll
       for (int r = 0; r < RT; ++r) st[r][t] = mfma16<false>(middles, qsum[r], st[r][t]);
@@ -556,22 +556,22 @@ __global__ void __launch_bounds__(256, D == 256 || (D == 128 && RT == 2) ? 2 : 3
     }
     if (!whole) {
       // Places that no row sees may hold anything: their scales and middles count as 0. So do those
-      // of a seen place that are not finite, as they must not reach the rows that do not see it (0
+      // of a seen place that stands for NaN, as they must not reach the rows that do not see it (0
       // times NaN is NaN); those that do get a NaN after the loop.
       uint32_t bad = 0;
-      auto clean = [&](u32x4& v) {
+      auto clean = [&](u32x4& v, auto bad_of) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int j = c * kChunk + 8 * kg + 2 * x;
           const uint32_t in = (j >= lo && j < hi ? 0xFFFFu : 0u) | (j + 1 >= lo && j + 1 < hi ? 0xFFFF0000u : 0u);
-          const uint32_t nf = not_finite_halves(v[x]) & in;
-          bad |= nf;
-          v[x] &= in & ~nf;
+          const uint32_t nan = bad_of(v[x]) & in;
+          bad |= nan;
+          v[x] &= in & ~nan;
         }
       };
 #pragma unroll
-      for (int i = 0; i < NS; ++i) clean(vs[i]);
-      clean(vm);
+      for (int i = 0; i < NS; ++i) clean(vs[i], bad_scales);
+      clean(vm, bad_middles);
       if (__any(bad != 0)) any_bad = true;
     }
     {
@@ -629,7 +629,8 @@ __global__ void __launch_bounds__(256, D == 256 || (D == 128 && RT == 2) ? 2 : 3
         constexpr int PER = GS / 64;
         middle = __shfl(rest[t][u / PER & 3], (u / PER >> 2) * 16 + n);
       }
-      if (fabsf(middle) == INFINITY) middle = NAN;  // (from a group of infinite middle)
+      // From a group that stands for NaN: its middle is infinite or, the scale being too large, every code.
+      if (fabsf(middle) == INFINITY || fabsf(acc[t][u][0][0]) == INFINITY) middle = NAN;
       if (NARROW && n >= 4) continue;
 #pragma unroll
       for (int r = 0; r < 4; ++r)
@@ -648,7 +649,7 @@ __global__ void __launch_bounds__(256, D == 256 || (D == 128 && RT == 2) ? 2 : 3
           const uint16_t* params = reinterpret_cast<const uint16_t*>(v_cache + (size_t)__shfl(here, key >> 3) * BLOCK + 4 * D) + (key & 7);
           if (j < row[t].lo || j >= row[t].hi) continue;
           for (int g = kg; g < G; g += 4)
-            if (not_finite<false>(params[g * 16]) || not_finite<false>(params[g * 16 + 8]))
+            if (bad_scale(params[g * 16]) || bad_middle(params[g * 16 + 8]))
               for (int d = 0; d < GS; ++d) so[wave][n][g * GS + d] = NAN;
         }
       }

@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
     return (uint32_t)step * BN >= (uint32_t)block_all_lo && (uint32_t)(step + 1) * BN <= (uint32_t)block_all_hi;
   };
   // Before the decoding. Tokens that no row sees may hold anything: their scales and middles count as 0. So
-  // do those of a seen one that are not finite, as they must not reach the rows that do not see it (0 times NaN
+  // do those of a seen one that stands for NaN, as they must not reach the rows that do not see it (0 times NaN
   // is NaN); those that do get a NaN at the end.
   auto clean = [&](int step) QMM_INLINE {
     if (seen_by_whole_block(step)) return;
@@ -211,10 +211,10 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
       for (int x = 0; x < 2; ++x) {
         const uint32_t j = j0 + 2 * x, lo = block_lo, hi = block_hi;
         const uint32_t in = (j >= lo && j < hi ? 0xFFFFu : 0u) | (j + 1 >= lo && j + 1 < hi ? 0xFFFF0000u : 0u);
-        const uint32_t nf = (not_finite_halves(vs[i][x]) | not_finite_halves(vm[i][x])) & in;
-        bad |= nf;
-        vs[i][x] &= in & ~nf;
-        vm[i][x] &= in & ~nf;
+        const uint32_t nan = (bad_scales(vs[i][x]) | bad_middles(vm[i][x])) & in;
+        bad |= nan;
+        vs[i][x] &= in & ~nan;
+        vm[i][x] &= in & ~nan;
       }
     }
     if (bad) s_bad = 1;
@@ -224,17 +224,17 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
     if (word0 == 0) {
       u32x4 middles = {0, 0, 0, 0};
       if constexpr (G == 1) {
-        middles[0] = infinite_as_nan(kp[0] >> 16);
+        middles[0] = middles_or_nan(kp[0] >> 16, kp[0] & 0xFFFF);
       } else {
 #pragma unroll
-        for (int x = 0; x < G / 2; ++x) middles[x] = infinite_as_nan(kp[G / 2 + x]);
+        for (int x = 0; x < G / 2; ++x) middles[x] = middles_or_nan(kp[G / 2 + x], kp[x]);
       }
       *reinterpret_cast<u32x4*>(lds + k_to + TILE + key * 16) = middles;
     }
 #pragma unroll
     for (int i = 0; i < VU; ++i)
       if (quad_of(i) * 4 % GS == 0 && !no_values)
-        *reinterpret_cast<u32x2*>(lds + v_to + TILE + quad_of(i) * 4 / GS * VM_ROW + blk_of(i) * 16 + (unit_of(i) & 1) * 8) = u32x2{infinite_as_nan(vm[i][0]), infinite_as_nan(vm[i][1])};
+        *reinterpret_cast<u32x2*>(lds + v_to + TILE + quad_of(i) * 4 / GS * VM_ROW + blk_of(i) * 16 + (unit_of(i) & 1) * 8) = u32x2{middles_or_nan(vm[i][0], vs[i][0]), middles_or_nan(vm[i][1], vs[i][1])};
   };
   // The decoding in slices: the key's words, then four channels of each unit.
   constexpr int SLICES = KW + 4 * VU;
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
       for (int j = 0; j < BN; ++j) {
         const uint16_t* params = reinterpret_cast<const uint16_t*>(v_cache + (size_t)__shfl(here, j >> 3) * BLOCK + 4 * D) + g * 16 + (j & 7);
         if (step * BN + j < row.lo || step * BN + j >= row.hi) continue;
-        if (not_finite<false>(params[0]) || not_finite<false>(params[8]))
+        if (bad_scale(params[0]) || bad_middle(params[8]))
           for (int d = kg; d < 32; d += 2) so[n * LDO + d] = NAN;
       }
     }
