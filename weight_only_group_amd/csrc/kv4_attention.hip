@@ -709,25 +709,27 @@ hipError_t launch_split(const AttentionArgs& a, bool bf16, hipStream_t stream) {
 }
 
 // Blocks of many rows, whose keys are not split, where their waves (32 rows each) fill the CUs' SIMDs and the sequences
-// have half a block of rows on average. Measured, time of the parts over that of the blocks, 24 to 32 heads over 8 to 32,
-// dimensions of 128: half as many waves 0.6 to 0.8; as many 1.1 to 1.3; many 1.5 to 1.9; sequences of a quarter of a
-// block 0.7 whatever their number. (Of 256 dimensions as many 1.2 to 1.7, of 64 1.0 to 1.3.)
-// A block of one query head to a key head spans the most positions, so that its rows see the fewest keys in common: with
-// masks or distances it is 0.7 to 1.0 there, where the cases below name it, and else 1.0 to 1.3.
-bool use_tiles(int B, int T, int Hq, int Hkv, int D, int max_q, bool masked, bool biased, DeviceTopo topo) {
+// have half a block of rows on average. Measured, time of the other kernel over that of the blocks, 24 to 32 heads over 8 to 32,
+// dimensions of 128: half as many waves 0.5 to 0.7; as many 0.85 to 1.3; many 1.5 to 1.8; sequences of a quarter of a
+// block 0.45 to 0.7 with one query head a key head.
+// There a block spans the most positions, so that its rows see the fewest keys in common: prompts of 500 to 8000 without masks, with
+// windows, documents and distances (756 shapes, the middle 80 of 100) 0.7 to 1.06 with D 64, 0.9 on average; 0.8 to 1.04 with D 256 and
+// distances, 0.92; but 0.9 to 1.3 with D 128 and 1.0 to 1.15 with D 256 otherwise. Prompts of few tiles, whose keys would be
+// in parts, 0.8 to 1.5 whatever D, 1.2 on average. (Several query heads a key head: 1.0 to 1.6, D 64 1.2 on average, D 128 1.5.)
+bool use_tiles(int B, int T, int Hq, int Hkv, int D, int max_q, int max_kv, bool biased, DeviceTopo topo) {
   const long long tokens = std::min<long long>(T, (long long)B * max_q), rows = tokens * (Hq / Hkv);
   if (rows < 128ll * B || (rows + 31) / 32 * Hkv < 4ll * topo.cus) return false;
-  return Hq != Hkv || !(D == 64 ? masked : D == 256 && biased);
+  return Hq != Hkv || !(D == 64 || (D == 256 && biased)) || kv4_plan(B, Hq, Hkv, D, max_q, max_kv, topo).parts > 0;
 }
 
 bool tiles_take(const AttentionArgs& a) {
-  return use_tiles(a.B, a.T, a.Hq, a.Hkv, a.D, a.max_q, a.first || a.end, a.slopes, device_topology());
+  return use_tiles(a.B, a.T, a.Hq, a.Hkv, a.D, a.max_q, a.max_kv, a.slopes, device_topology());
 }
 
 }  // namespace
 
 size_t kv4_attention_workspace(int B, int T, int Hq, int Hkv, int D, int max_q, int max_kv) {
-  if (use_tiles(B, T, Hq, Hkv, D, max_q, true, true, device_topology())) return 0;
+  if (use_tiles(B, T, Hq, Hkv, D, max_q, max_kv, true, device_topology())) return 0;
   const Kv4Plan p = kv4_plan(B, Hq, Hkv, D, max_q, max_kv, device_topology());
   return p.parts ? kWorkspaceHeader + p.blocks * kRows * (D + 2) * sizeof(float) : 0;
 }
