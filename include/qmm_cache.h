@@ -87,6 +87,22 @@ qmm_status qmm_kv4_attention(const uint16_t* q, int64_t q_stride, int T, int Hq,
                              uint16_t* out, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * qmm_kv4_attention_plan_info -- the launch qmm_kv4_attention makes for these sizes on the
+ * current device, with (biased) or without slopes, for tests and measurement. Host only:
+ * no work is enqueued. Writes min(n, 6) ints:
+ *   info[0] kernel: 0 = a tile of 16 rows a block, 1 = two tiles a block, 2 = tiles in
+ *           parts of their keys, which blocks share, 3 = blocks of many rows
+ *   info[1] rows of a block     info[2] blocks of the grid
+ *   info[3] kernel 2: blocks that run at a time, for which the parts are cut, else 0
+ *   info[4] kernel 2: blocks that the parts may come to beyond one a tile, else 0
+ *   info[5] compute units of the device
+ * Returns QMM_ERR_NULL for a NULL info with n > 0, QMM_ERR_SHAPE for sizes that
+ * qmm_kv4_attention would reject or for which it launches nothing, else QMM_OK.
+ */
+qmm_status qmm_kv4_attention_plan_info(int B, int T, int Hq, int Hkv, int D, int max_q, int max_kv, int biased, int32_t* info,
+                                       int n);
+
+/*
  * The care of pages, for caches of any kind: n_caches arrays (one layer's k_cache,
  * another's v_cache, ...), each of `pages` pages, cache i of page_bytes[i] bytes a
  * page (all heads). `caches` and `page_bytes` are host arrays of n_caches, read

@@ -21,7 +21,7 @@ The operators of a decoder layer between the products (include/qmm_layer.h) are
 in ``layer`` and exported here: ``qmm_moe_route``, ``qmm_moe``, ``qmm_kv_append``,
 ``qmm_attention``, ``qmm_logprobs``. A key/value cache in 4 bits and the care of a cache's
 pages (include/qmm_cache.h) are in ``cache``: ``qmm_kv4_append``, ``qmm_kv4_gather``,
-``qmm_kv4_attention``, ``qmm_kv_copy_pages``, ``qmm_kv_compact``, ``kv4_page_bytes``.
+``qmm_kv4_attention``, ``qmm_kv_copy_pages``, ``qmm_kv_compact``, ``kv4_page_bytes``, ``kv4_attention_plan_info``.
 
 Bit widths 1, 2, 3, 4 and 8. The floating-point data (x, zeros, scales, bias,
 the result) are all float16 or all bfloat16; bfloat16 calls the ``_bf16``
@@ -477,5 +477,5 @@ def quantized_matmul(x, qweight, qzeros, scales, bits: int, group_size: int, qwe
 from . import layer  # noqa: E402  (it uses the helpers above)
 from .layer import qmm_attention, qmm_kv_append, qmm_logprobs, qmm_moe, qmm_moe_route  # noqa: E402,F401
 from . import cache  # noqa: E402
-from .cache import (kv4_page_bytes, qmm_kv4_append, qmm_kv4_attention, qmm_kv4_gather, qmm_kv_compact,  # noqa: E402,F401
-                    qmm_kv_copy_pages)
+from .cache import (kv4_attention_plan_info, kv4_page_bytes, qmm_kv4_append, qmm_kv4_attention, qmm_kv4_gather,  # noqa: E402,F401
+                    qmm_kv_compact, qmm_kv_copy_pages)

@@ -5,6 +5,7 @@
 * ``qmm_kv4_append(q, k, v, cos, sin, positions, slots, k_cache, v_cache, group_size, adjacent=False)`` -> rotated q
 * ``qmm_kv4_gather(k_cache, v_cache, slots, D, group_size, dtype)`` -> ``(k, v)`` in 16 bits
 * ``qmm_kv4_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q, max_kv, group_size, ...)`` -> out
+* ``kv4_attention_plan_info(B, T, Hq, Hkv, D, max_q, max_kv, biased=False)`` -> the kernel and grid of such a call
 * ``qmm_kv_copy_pages(caches, src, dst)``, ``qmm_kv_compact(caches, page_table, kv_lens, page_size)``: for
   caches of either kind, those of all layers at once
 
@@ -29,7 +30,7 @@ LARGEST_SCALE = 2728  # a group whose scale is beyond it stands for NaN
 # Every symbol qmm_cache.h declares.
 EXPORTS = (
     "qmm_kv4_page_bytes", "qmm_kv4_append", "qmm_kv4_gather", "qmm_kv4_attention_workspace_bytes", "qmm_kv4_attention",
-    "qmm_kv_copy_pages", "qmm_kv_compact_workspace_bytes", "qmm_kv_compact",
+    "qmm_kv4_attention_plan_info", "qmm_kv_copy_pages", "qmm_kv_compact_workspace_bytes", "qmm_kv_compact",
 )
 
 
@@ -41,6 +42,7 @@ def declare(lib):
             ("qmm_kv4_gather", I, [P, P, I, I, I, I, I, P, I, U, P, P, P]),
             ("qmm_kv4_attention_workspace_bytes", SZ, [I, I, I, I, I, I, I]),
             ("qmm_kv4_attention", I, [P, L, I, I, I, I, I, P, P, I, I, P, I, P, P, I, I, I, P, P, F, F, P, U, P, P, SZ, P]),
+            ("qmm_kv4_attention_plan_info", I, [I, I, I, I, I, I, I, I, P, I]),
             ("qmm_kv_copy_pages", I, [P, P, I, I, P, P, I, P]),
             ("qmm_kv_compact_workspace_bytes", SZ, [I]),
             ("qmm_kv_compact", I, [P, P, I, I, P, I, P, I, I, P, P, P, P, SZ, P])):
@@ -145,6 +147,19 @@ def qmm_kv4_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q:
             _p(kv_lens), _p(q_starts), B, max_q, max_kv, _p(first), _p(end), 1.0 / math.sqrt(D) if scale is None else scale,
             softcap, _p(slopes), QMM_BF16 if dt == torch.bfloat16 else 0, _p(out))
     return _launch("qmm_kv4_attention", dev, args, out, workspace, (B, T, Hq, Hkv, D, max_q, max_kv))
+
+
+KV4_KERNELS = ("tile", "pair", "parts", "blocks")
+KV4_PLAN_FIELDS = ("kernel", "rows", "blocks", "resident", "parts", "cus")
+
+
+def kv4_attention_plan_info(B: int, T: int, Hq: int, Hkv: int, D: int, max_q: int, max_kv: int, biased: bool = False) -> dict:
+    """The launch qmm_kv4_attention makes for these sizes on the current device, with or without slopes (host only);
+    ``kernel`` is one of KV4_KERNELS."""
+    info = (ctypes.c_int32 * len(KV4_PLAN_FIELDS))()
+    _qmm._check(_qmm.library().qmm_kv4_attention_plan_info(B, T, Hq, Hkv, D, max_q, max_kv, biased, ctypes.addressof(info), len(info)),
+                "qmm_kv4_attention_plan_info")
+    return dict(zip(KV4_PLAN_FIELDS, (KV4_KERNELS[info[0]], *info[1:])))
 
 
 def _pools(caches):

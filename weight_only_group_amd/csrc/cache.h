@@ -26,7 +26,16 @@ struct Kv4GatherArgs {
 };
 hipError_t launch_kv4_gather(const Kv4GatherArgs& a, bool bf16, hipStream_t stream);
 
-long long kv4_attention_blocks(const AttentionArgs& a);  // of the grid
+// Which kernel takes a call, and its grid.
+enum Kv4Kernel { kKv4Tile, kKv4Pair, kKv4Parts, kKv4Blocks };
+struct Kv4Launch {
+  Kv4Kernel kernel;
+  int rows;                 // of a block
+  long long blocks;         // of the grid
+  int resident, parts;      // kKv4Parts: blocks that run at a time, blocks beyond one a tile
+  int threads;              // of a block
+};
+Kv4Launch kv4_attention_launch(int B, int T, int Hq, int Hkv, int D, int max_q, int max_kv, bool biased);
 size_t kv4_attention_workspace(int B, int T, int Hq, int Hkv, int D, int max_q, int max_kv);
 hipError_t launch_kv4_attention(const AttentionArgs& a, int group_size, bool bf16, hipStream_t stream);
 

@@ -31,6 +31,9 @@ qmm_status check_kv4(int page_size, int D, int group_size) {
   return QMM_OK;
 }
 
+// A launch's blocks, counted as of 256 threads each.
+long long blocks_of_256(const qmm::Kv4Launch& p) { return p.blocks * (p.threads / 256); }
+
 qmm_status check_pools(void* const* caches, const int64_t* page_bytes, int n_caches, int pages) {
   if (n_caches < 0 || n_caches > qmm::kMostCaches) return fail(QMM_ERR_SHAPE, "n_caches=%d must be in [0, %d]", n_caches, qmm::kMostCaches);
   if (pages < 1) return fail(QMM_ERR_SHAPE, "pages=%d must be >= 1", pages);
@@ -112,11 +115,25 @@ qmm_status qmm_kv4_attention(const uint16_t* q, int64_t q_stride, int T, int Hq,
   st = check_attention_shape(a);
   if (st != QMM_OK) return st;
   if (T == 0 || B == 0 || max_q == 0) return ok();
-  st = check_attention_arrays(a, qmm::kv4_attention_blocks(a));
+  st = check_attention_arrays(a, blocks_of_256(qmm::kv4_attention_launch(B, T, Hq, Hkv, D, max_q, max_kv, slopes != nullptr)));
   if (st == QMM_OK)
     st = check_workspace(workspace, workspace_bytes, qmm::kv4_attention_workspace(B, T, Hq, Hkv, D, max_q, max_kv));
   if (st != QMM_OK) return st;
   return from_hip(qmm::launch_kv4_attention(a, group_size, (flags & QMM_BF16) != 0, stream), "qmm_kv4_attention launch");
+}
+
+qmm_status qmm_kv4_attention_plan_info(int B, int T, int Hq, int Hkv, int D, int max_q, int max_kv, int biased, int32_t* info,
+                                       int n) {
+  if (!qmm::attention_size_ok(B, T, Hq, Hkv, D, max_q, max_kv))
+    return fail(QMM_ERR_SHAPE, "B=%d, T=%d, Hq=%d, Hkv=%d, D=%d, max_q=%d, max_kv=%d: no sizes of a launch", B, T, Hq, Hkv, D, max_q, max_kv);
+  if (n > 0 && !info) return fail(QMM_ERR_NULL, "info is NULL");
+  const qmm::Kv4Launch p = qmm::kv4_attention_launch(B, T, Hq, Hkv, D, max_q, max_kv, biased != 0);
+  const qmm_status st = qmm::check_attention_blocks(B, Hkv, max_q, blocks_of_256(p));
+  if (st != QMM_OK) return st;
+  const int32_t v[6] = {p.kernel, p.rows, (int32_t)p.blocks, p.resident, p.parts,
+                        qmm::device_topology().cus};
+  for (int i = 0; i < n && i < 6; ++i) info[i] = v[i];
+  return ok();
 }
 
 qmm_status qmm_kv_copy_pages(void* const* caches, const int64_t* page_bytes, int n_caches, int pages,

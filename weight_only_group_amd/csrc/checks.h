@@ -95,16 +95,21 @@ inline qmm_status check_attention_shape(const AttentionArgs& a) {
   return QMM_OK;
 }
 
+// A launch's threads (256 a block) are counted in 32 bits.
+inline qmm_status check_attention_blocks(int B, int Hkv, int max_q, long long blocks) {
+  if (blocks >= (1ll << 24))
+    return fail(QMM_ERR_SHAPE, "B=%d, Hkv=%d and max_q=%d: 2^24 blocks and more; pass the long sequences in a call of their own", B, Hkv, max_q);
+  return QMM_OK;
+}
+
 inline qmm_status check_attention_arrays(const AttentionArgs& a, long long blocks) {
   const qmm_status st = check_cache(a.k_cache, a.v_cache, a.pages, a.Hkv, a.page_size);
   if (st != QMM_OK) return st;
   if (a.table_stride < 1 || (long long)a.table_stride * a.page_size >= (1ll << 31) || a.max_kv > (long long)a.table_stride * a.page_size)
     return fail(QMM_ERR_SHAPE, "max_kv=%d must not exceed table_stride=%d * page_size=%d (below 2^31)", a.max_kv, a.table_stride,
                 a.page_size);
-  // A launch's threads (256 a block) are counted in 32 bits.
-  if (blocks >= (1ll << 24))
-    return fail(QMM_ERR_SHAPE, "B=%d, Hkv=%d and max_q=%d: 2^24 blocks and more; pass the long sequences in a call of their own", a.B,
-                a.Hkv, a.max_q);
+  const qmm_status grid = check_attention_blocks(a.B, a.Hkv, a.max_q, blocks);
+  if (grid != QMM_OK) return grid;
   if (!a.q || !a.page_table || !a.kv_lens || !a.q_starts || !a.out) return fail(QMM_ERR_NULL, "a required pointer is NULL");
   if (!aligned16(a.q) || !aligned16(a.out)) return fail(QMM_ERR_ALIGN, "q and out must be 16-byte aligned");
   if (!aligned(a.page_table, 4) || !aligned(a.kv_lens, 4) || !aligned(a.q_starts, 4) || !aligned(a.first, 4) || !aligned(a.end, 4) ||

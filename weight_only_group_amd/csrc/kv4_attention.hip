@@ -722,10 +722,6 @@ bool use_tiles(int B, int T, int Hq, int Hkv, int D, int max_q, int max_kv, bool
   return Hq != Hkv || !(D == 64 || (D == 256 && biased)) || kv4_plan(B, Hq, Hkv, D, max_q, max_kv, topo).parts > 0;
 }
 
-bool tiles_take(const AttentionArgs& a) {
-  return use_tiles(a.B, a.T, a.Hq, a.Hkv, a.D, a.max_q, a.max_kv, a.slopes, device_topology());
-}
-
 }  // namespace
 
 size_t kv4_attention_workspace(int B, int T, int Hq, int Hkv, int D, int max_q, int max_kv) {
@@ -734,18 +730,19 @@ size_t kv4_attention_workspace(int B, int T, int Hq, int Hkv, int D, int max_q, 
   return p.parts ? kWorkspaceHeader + p.blocks * kRows * (D + 2) * sizeof(float) : 0;
 }
 
-long long kv4_attention_blocks(const AttentionArgs& a) {
-  const int B = a.B, Hq = a.Hq, Hkv = a.Hkv, D = a.D, max_q = a.max_q;
-  if (tiles_take(a)) {
-    // (twice as many where a block has eight waves: the limit on blocks is one on threads)
-    const int rows = D == 256 ? kKv4TileRows<256> : kKv4TileRows<128>;
-    return tile_blocks(B, Hkv, row_tiles(max_q, Hq / Hkv, rows)) * (D == 256 ? 1 : 2);
+Kv4Launch kv4_attention_launch(int B, int T, int Hq, int Hkv, int D, int max_q, int max_kv, bool biased) {
+  const DeviceTopo topo = device_topology();
+  if (use_tiles(B, T, Hq, Hkv, D, max_q, max_kv, biased, topo)) {
+    const int rows = D == 256 ? kKv4TileRows<256> : kKv4TileRows<128>, waves = D == 256 ? kKv4TileWaves<256> : kKv4TileWaves<128>;
+    return {kKv4Blocks, rows, tile_blocks(B, Hkv, row_tiles(max_q, Hq / Hkv, rows)), 0, 0, 64 * waves};
   }
-  return kv4_plan(B, Hq, Hkv, D, max_q, a.max_kv, device_topology()).blocks;
+  const Kv4Plan p = kv4_plan(B, Hq, Hkv, D, max_q, max_kv, topo);
+  return {p.parts ? kKv4Parts : p.wide ? kKv4Pair : kKv4Tile, p.wide ? 2 * kRows : kRows, p.blocks, p.parts ? p.fit : 0, p.parts,
+          64 * kWaves};
 }
 
 hipError_t launch_kv4_attention(const AttentionArgs& a, int group_size, bool bf16, hipStream_t stream) {
-  if (tiles_take(a)) {
+  if (kv4_attention_launch(a.B, a.T, a.Hq, a.Hkv, a.D, a.max_q, a.max_kv, a.slopes).kernel == kKv4Blocks) {
     const Kv4TileArgs t = {a, bf16};
     return a.D == 64 ? launch_kv4_tiles<64>(t, group_size, stream)
            : a.D == 128 ? launch_kv4_tiles<128>(t, group_size, stream) : launch_kv4_tiles<256>(t, group_size, stream);
