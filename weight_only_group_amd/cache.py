@@ -21,7 +21,7 @@ import torch
 
 import weight_only_group_amd as _qmm
 
-from .layer import QMM_ADJACENT, QMM_BF16, _array, _heads, _launch, _p, _result
+from .layer import QMM_ADJACENT, QMM_BF16, _array, _heads, _launch, _p, _result, _sizes
 
 GROUPS = (32, 64, 128)
 LARGEST = 16384  # keys and values are cut to this size
@@ -55,6 +55,7 @@ def declare(lib):
 def kv4_page_bytes(page_size: int, D: int, group_size: int) -> int:
     """Bytes of one head of a page of a 4-bit cache, page_size (D / 2 + 4 D / group_size). ``page_size`` is a multiple
     of 8, D 64, 128 or 256, ``group_size`` (channels per scale) 32, 64 or 128 and at most D."""
+    _sizes(page_size=page_size, D=D, group_size=group_size)
     n = _qmm.library().qmm_kv4_page_bytes(page_size, D, group_size)
     if not n:
         raise ValueError(f"page_size={page_size} must be a positive multiple of 8, D={D} 64, 128 or 256, "
@@ -134,6 +135,8 @@ def qmm_kv4_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q:
     _array(page_table, "page_table", torch.int32, (B, table_stride), dev)
     _array(kv_lens, "kv_lens", torch.int32, (B,), dev)
     _array(q_starts, "q_starts", torch.int32, (B + 1,), dev)
+    if not (0 <= max_q < 2**31 and 0 <= max_kv < 2**31 > table_stride):
+        _sizes(max_q=max_q, max_kv=max_kv, table_stride=table_stride)
     if first is not None:
         _array(first, "first", torch.int32, (T,), dev)
     if end is not None:
@@ -156,6 +159,7 @@ KV4_PLAN_FIELDS = ("kernel", "rows", "blocks", "resident", "parts", "cus")
 def kv4_attention_plan_info(B: int, T: int, Hq: int, Hkv: int, D: int, max_q: int, max_kv: int, biased: bool = False) -> dict:
     """The launch qmm_kv4_attention makes for these sizes on the current device, with or without slopes (host only);
     ``kernel`` is one of KV4_KERNELS."""
+    _sizes(B=B, T=T, Hq=Hq, Hkv=Hkv, D=D, max_q=max_q, max_kv=max_kv)
     info = (ctypes.c_int32 * len(KV4_PLAN_FIELDS))()
     _qmm._check(_qmm.library().qmm_kv4_attention_plan_info(B, T, Hq, Hkv, D, max_q, max_kv, biased, ctypes.addressof(info), len(info)),
                 "qmm_kv4_attention_plan_info")
@@ -177,6 +181,7 @@ def _pools(caches):
     if bad:
         _refuse_pools(caches)
     n = len(sizes)
+    _sizes(pages=pages)
     return (ctypes.c_void_p * n)(*[t.data_ptr() for t in caches]), (ctypes.c_int64 * n)(*sizes), n, pages, first.device
 
 
@@ -207,6 +212,7 @@ def qmm_kv_copy_pages(caches, src, dst):
     n = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() == 1 else 0
     _array(src, "src", torch.int32, (n,), dev)
     _array(dst, "dst", torch.int32, (n,), dev)
+    _sizes(n=n)
     _launch("qmm_kv_copy_pages", dev, (pointers, sizes, n_caches, pages, _p(src), _p(dst), n))
 
 
@@ -214,6 +220,7 @@ def qmm_kv_compact(caches, page_table, kv_lens, page_size: int, workspace=None):
     """Packs the pages in use (page_table[b, i], i < ceil(kv_lens[b] / page_size)) of all ``caches`` into the lowest ones.
     Returns the page table with them renamed, ``moved_to`` (pages,) int32, the place of each page now (-1: it was free),
     and ``live`` (1,) int32, their number: the pages from there on are free. Pages in use below ``live`` stay."""
+    _sizes(page_size=page_size)
     pointers, sizes, n_caches, pages, dev = _pools(caches)
     B, table_stride = page_table.shape if isinstance(page_table, torch.Tensor) and page_table.dim() == 2 else (0, 0)
     _array(page_table, "page_table", torch.int32, (B, table_stride), dev)

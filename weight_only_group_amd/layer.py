@@ -113,6 +113,13 @@ def _launch(name, dev, args, out=(), workspace=None, shape=None):
     return out
 
 
+def _sizes(**sizes):
+    """Refuses sizes past 32 bits: they would reach the library cut to their low bits, as other sizes."""
+    for name, n in sizes.items():
+        if not -2**31 <= n < 2**31:
+            raise ValueError(f"{name}={n} must be below 2^31")
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
 
@@ -248,6 +255,8 @@ def qmm_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q: int
     _array(page_table, "page_table", torch.int32, (B, table_stride), dev)
     _array(kv_lens, "kv_lens", torch.int32, (B,), dev)
     _array(q_starts, "q_starts", torch.int32, (B + 1,), dev)
+    if not (0 <= max_q < 2**31 and 0 <= max_kv < 2**31 > table_stride):
+        _sizes(max_q=max_q, max_kv=max_kv, table_stride=table_stride)
     if first is not None:
         _array(first, "first", torch.int32, (T,), dev)
     if end is not None:
