@@ -8,7 +8,9 @@
 
 Counters take a pass each of: the SQ counters of layer_operators.py, FETCH_SIZE, WRITE_SIZE.
 ``run`` takes every case of perf/more_operators.py through the public entry points, PASSES times over two sets of
-buffers in turn; one launch of each of a case's kernels per pass, which is how the launches are told apart afterwards.
+buffers in turn after WARM passes that are left out (after a pause the clock takes some thirty launches of the long prompt
+to settle: 850 to 970 us at first, then 740); one launch of each of a case's kernels per pass, which is how the launches are
+told apart afterwards.
 """
 from __future__ import annotations
 
@@ -20,6 +22,7 @@ import sys
 
 from layer_operators import PASSES, SQ
 
+WARM = 40
 KERNELS = {"append": 2, "compact": 2}  # launches of a pass; 1 for the others
 
 
@@ -35,7 +38,7 @@ def run():
     op = operators()
     for case in op.listed():
         states = [op.prepare(case, seed) for seed in range(2)]
-        for i in range(PASSES):
+        for i in range(WARM + PASSES):
             op.run(states[i % 2])
         torch.cuda.synchronize()
         print(case["name"], flush=True)
@@ -51,7 +54,7 @@ def launches(path):
     left = [by_dispatch[i] for i in sorted(by_dispatch)]
     for case in operators().listed():
         n = KERNELS.get(case["op"], 1)
-        taken, left = left[:PASSES * n], left[PASSES * n:]
+        taken, left = left[WARM * n:(WARM + PASSES) * n], left[(WARM + PASSES) * n:]
         for j in range(n):
             group = taken[j::n]
             kernel = group[0][0]["Kernel_Name"]

@@ -81,13 +81,14 @@ __device__ __forceinline__ float max_of_rows(float v) {
 // sum chunks / parts gives no more blocks than parts + tiles; smaller ones are tried first.
 // A sequence's chunks are those of its first and last query.
 // One part each where that is faster: a share, its hand-over and the join cost 5 us and more a block, against the time of
-// the longest tile alone. Measured, the time in parts over that without, single tokens: up to 16 tiles of D 64, 128 and 256 on 400 keys
-// 1.35, 1.3 and 1.15, on 1000 1.3, 1.1 and 0.9, on 3000 0.8, 0.7 and 0.55; 256 to 4096 tiles on less than four keys
-// a tile 1.1 to 6, and where one sequence among short ones has eight keys a tile 0.5 to 0.9. Sequences of more than 128
-// rows are split up to kMostTiles tiles and from half as many keys on: their last ones see the most keys (two or three
-// prompts of 2000 to 3000 rows take 0.3 to 0.5 of the time in parts, of 1000 0.6 to 0.7; of 300 3 times as long).
-// Of several tiles of a sequence a block then takes two, so that its keys and values are decoded once for both: against one
-// tile a block 1.2 to 1.25 times as fast with 17 to 32 rows, 1.03 to 1.1 with 65 to 128. D 256 has no registers for it (0.6).
+// the longest tile alone. Measured, the time in parts over that without (profiles/cache_attention_choices.txt, means), single
+// tokens: up to 16 tiles of D 64, 128 and 256 on 400 keys 1.57, 1.37 and 1.19, on 1000 1.20, 1.09 and 0.84, on 3000 0.66, 0.61
+// and 0.48; 256 to 4096 tiles on less than four keys a tile 1.97 (one at 6.2), and where one sequence among short ones has eight keys a
+// tile and more 0.43. Sequences of more than 128 rows are split up to kMostTiles tiles and from half as many keys on: their
+// last ones see the most keys. A prompt of 3000 alone takes 0.57 of the time in parts, of 2000 0.71, of 1000 1.06; two
+// to four of them 0.98 to 1.25, and prompts of 150 to 500, which are not split, would take 2.2 to 1.7.
+// Of several tiles of a sequence a block then takes two, so that its keys and values are decoded once for both: 1.08 times as fast
+// as one tile a block with 17 to 32 rows, 1.16 with 33 to 64, 1.05 with 65 to 128. D 256 has no registers for it (0.6).
 constexpr int kMostSequences = 1024;  // of a split launch
 constexpr int kMostTiles = 4096, kPartsFrom = 192 * 1024;  // keys, with D: 1536, 1024, 614
 constexpr int kMostParts = 256;       // of a tile
@@ -315,8 +316,8 @@ __device__ __forceinline__ void join_parts(const Kv4KernelArgs& p, const Share& 
 //
 // No operand passes through LDS: a wave's 32 keys are read once, by the lanes that need them, and the next ones are
 // asked for as the registers fall free. Few rows are bound by memory and by a block's start and end (the share of the work,
-// page, keys; the join of the parts: 10 us together): 48 decodes of 128 to 8192 keys (32 heads of 128 over 8, 92 MB) 28.8 us,
-// three on up to 131071 (157 MB) 39 us, 4.0 TB/s; one on 1500 keys 11 us, all of it latency. Tiles of sixteen rows are bound by
+// page, keys; the join of the parts: 10 us together): 48 decodes of 128 to 8192 keys (32 heads of 128 over 8, 92 MB) 29 us,
+// three on up to 131071 (157 MB) 42 us, 3.7 TB/s; one on 1500 keys 11 us, all of it latency. Tiles of sixteen rows are bound by
 // the vector ALUs, 77% busy over documents of 24 heads of 64 (49 us): codes are decoded again in each. Two tiles a block: 47.5 us.
 //
 // RT: tiles of a block, one behind another (a wave's operands serve both); with parts one.

@@ -6,8 +6,8 @@
 // queries in the columns, so that a softmax is two lanes' affair) it decodes its part of the next step's keys and values between them;
 // the other wave of its SIMD, a phase behind, takes its softmax meanwhile. Keys lie in two buffers, values
 // in three, pieces of 16 bytes placed by an exclusive or against bank conflicts.
-// Bound by the vector ALUs: a prompt of 8192 with a cap (32 heads of 128 over 8) takes 762 us, 720 TFLOP/s, with the
-// vector ALUs busy 68% of the cycles (of a score two exponentials and a reciprocal, each as long as two other
+// Bound by the vector ALUs: a prompt of 8192 with a cap (32 heads of 128 over 8) takes 737 us, 746 TFLOP/s (the first
+// thirty after a pause up to 970: the clock settles), with the vector ALUs busy 67% of the cycles (of a score two exponentials and a reciprocal, each as long as two other
 // operations) and the matrix cores 40%. The 16-bit cache's kernel takes 690 to 750 us for it.
 #pragma once
 
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
   // A step's matrix operations: the step before's weights times its values, sixteen keys (MT products and one for the
   // middles) after another; then the step's keys, their middles first, times the queries. Their left operands come from LDS
   // AHEAD operations before. (A prompt of 8192, 32 heads of 128 over 8: with 3 859 us, with 5 762 us, with 7 784 and with 9
-  // 779: there is no room for their registers.)
+  // 779, all measured after a pause: there is no room for their registers.)
   constexpr int GROUPS = BN / 16, VALUE_OPS = GROUPS * (MT + 1), OPS = VALUE_OPS + SUB * (STEPS + 1), AHEAD = 5;
   f32x16 st[SUB];
   u32x4 operand[AHEAD + 1];
