@@ -8,11 +8,13 @@
 // A code becomes one by an AND, an OR and half a packed multiply-add: the half 16 + c
 // has it in the top of its mantissa, and s (16 + c) - 24 s is rounded once, so not at all.
 // The second sums are one matrix operation more for all channels together, with
-// the middles as further channels; Q goes in three fp16 parts (33 bits). A row of ones among
-// the value's middles gives the weights' sum.
+// the middles as further channels; Q, an fp32 sum, goes in fp16 parts: three (all of it) where a block has few rows, two (to 2^-22
+// of it) in blocks of many, whose lane groups are two. A row of ones among the value's middles gives the weights' sum.
 //
-// Queries are scaled by a power of two, so that a row's largest is in [1, 2) and fp16
-// holds them whatever their type. The weights p are fp16, times 2^7.
+// Queries are scaled by a power of two, so that a row's largest is in [1, 2): the matrix operations take fp16 operands, which
+// hold codes times scales exactly (bf16 would not). Values below 2^-14 of it (bf16: 2^-17), subnormal then, are rounded to steps of
+// 2^-24: a score is off by 2^-25 of the largest times the key's values there at most, about what one rounding of the largest
+// one's product costs in fp32. The weights p are fp16, times 2^7.
 #pragma once
 
 #include "attention_rows.h"

@@ -3,12 +3,12 @@
 //
 // A block has 256 rows (128 where D is 256), 32 a wave, and takes 64 keys a step (32). While a wave has its matrix
 // operations in hand (the step before's values, the step's keys; 32x32x16, keys and channels in the rows, the wave's
-// queries in the columns, so that a softmax is two lanes' affair) it decodes its part of the next step's keys and values between them;
-// the other wave of its SIMD, a phase behind, takes its softmax meanwhile. Keys lie in two buffers, values
-// in three, pieces of 16 bytes placed by an exclusive or against bank conflicts.
+// queries in the columns, so that a softmax is two lanes' affair) it decodes its part of the next step's keys and values
+// between them; the other wave of its SIMD, a phase behind, takes its softmax meanwhile.
 // Bound by the vector ALUs: a prompt of 8192 with a cap (32 heads of 128 over 8) takes 737 us, 746 TFLOP/s (the first
-// thirty after a pause up to 970: the clock settles), with the vector ALUs busy 67% of the cycles (of a score two exponentials and a reciprocal, each as long as two other
-// operations) and the matrix cores 40%. The 16-bit cache's kernel takes 690 to 750 us for it.
+// thirty after a pause up to 970: the clock settles), with the vector ALUs busy 67% of the cycles (of a score two
+// exponentials and a reciprocal, each as long as two other operations) and the matrix cores 39%. The 16-bit cache's kernel
+// takes 690 to 750 us for it.
 #pragma once
 
 #include <type_traits>
@@ -49,9 +49,16 @@ struct Kv4TileKernelArgs {
   bool bf16;
 };
 
-// Block: 32 rows a wave of one key head, all their keys in steps of BN that go through two
-// LDS buffers. The first half of the waves decodes the values of the next step, the second half
-// the keys, from words asked for a step before that; then all take the step's products.
+// Block: 32 rows a wave of one key head, all their keys in steps of BN. Step s has two phases, each ended by a barrier (meet):
+//   products   V^T p^T of step s - 1, then K q^T of s; between them each wave decodes its own part of the keys and values of
+//              step s + 1, from words asked for a step before, and asks for those of s + 2
+//   softmax    of step s: the weights p stay in registers for the next products
+// Of eight waves those of the second half are a phase behind (one barrier more ahead of the loop, one less behind it), so that
+// a SIMD has one wave in each phase; four waves, one a SIMD, go together.
+// Buffers in LDS: keys of s are read in the products of s, while s + 1 is written: two, by the parity of the step. Values of s
+// are written in the products of s - 1 and read in those of s + 1, so that three steps' are there at a time: s - 1 read, s
+// whole or (by the half behind) still being written, s + 1 written. A buffer is written anew two (three) steps later, one barrier at
+// least after the half behind has read it.
 // Bound: the vector ALUs (exponentials, with a cap reciprocals too, and the decoding, which is why a
 // block has as many rows as registers allow).
 //
@@ -121,7 +128,7 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
   block_all_hi = __builtin_amdgcn_readfirstlane(block_all_hi);
   const int t0 = block_lo < block_hi ? block_lo / BN : 0, t1 = block_lo < block_hi ? (block_hi - 1) / BN + 1 : 0;
 
-  // The row's query, and its groups' sums in two parts (one a lane group).
+  // The row's query, and its groups' sums in two parts (one a lane group): 2^-22 of a sum off, as four roundings of its product in fp32.
   u32x4 q[STEPS], qsum = {0, 0, 0, 0};
 #pragma unroll
   for (int s = 0; s < STEPS; ++s)
@@ -285,8 +292,8 @@ __global__ void __launch_bounds__(64 * kKv4TileWaves<D>, D == 256 ? 1 : 2) kv4_t
   u32x4 w[BN / 16] = {};  // the weights of the step before, sixteen keys a piece
   // A step's matrix operations: the step before's weights times its values, sixteen keys (MT products and one for the
   // middles) after another; then the step's keys, their middles first, times the queries. Their left operands come from LDS
-  // AHEAD operations before. (A prompt of 8192, 32 heads of 128 over 8: with 3 859 us, with 5 762 us, with 7 784 and with 9
-  // 779, all measured after a pause: there is no room for their registers.)
+  // AHEAD operations before. (A prompt of 8192, 32 heads of 128 over 8: with 3 859 us, side by side with 5 762, with 7 784 and with 9
+  // 779: there is no room for their registers.)
   constexpr int GROUPS = BN / 16, VALUE_OPS = GROUPS * (MT + 1), OPS = VALUE_OPS + SUB * (STEPS + 1), AHEAD = 5;
   f32x16 st[SUB];
   u32x4 operand[AHEAD + 1];
