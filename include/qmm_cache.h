@@ -73,13 +73,13 @@ qmm_status qmm_kv4_gather(const uint8_t* k_cache, const uint8_t* v_cache, int pa
 /*
  * qmm_kv4_attention -- qmm_attention to a 4-bit cache: the same formulas, masks,
  * arguments and requirements (and those above), with keys and values as the
- * cache's codes stand for, exactly (where a scale has more than 8 significant bits: s (c - 8)
- * rounded to fp16), and sums in fp32. Of a query head's channels those smaller than 2^-14 of
- * its largest one (bf16: 2^-17) are rounded to steps of 2^-24 of the power of two below that. The
- * weights exp(s) are rounded to fp16 (for
- * bf16 data too; weights below 2^-32 of a row's largest count as 0), the
- * same rounded weights make the denominator. A query with a value that is not finite gives
- * NaN where it sees a key.
+ * cache's codes stand for, exactly (a scale of more than 8 significant bits, which no call
+ * writes, may put s (c - 8) off by s / 64), and sums in fp32. Of a query head's
+ * channels those smaller than 2^-14 of its largest one (bf16: 2^-17) are rounded to
+ * steps of 2^-24 of the power of two below that. The weights exp(s) are rounded to
+ * fp16 (for bf16 data too; weights below 2^-32 of a row's largest count as 0), the same
+ * rounded weights make the denominator. A query with a value that is not finite
+ * gives NaN where it sees a key.
  */
 size_t qmm_kv4_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int max_q, int max_kv);
 qmm_status qmm_kv4_attention(const uint16_t* q, int64_t q_stride, int T, int Hq, int Hkv, int D, int group_size,

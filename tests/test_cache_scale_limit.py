@@ -43,3 +43,13 @@ def test_parts_are_nan_beyond_it():
             for p, want in ((step, s), (middle, 0.0)):
                 assert np.isnan(p[:32]).all() if bad else (p[:32] == want).all()
             assert (step[32:] == 1).all() and (middle[32:] == 0).all()
+
+
+def test_scales_of_more_bits_are_off_by_a_64th():
+    """What the attention's decoding makes of such a scale: 24 s and the sum, each rounded to fp16."""
+    s = np.arange(2**15, dtype=np.uint16).view(np.float16)
+    s = s[np.isfinite(s) & (s <= co.LARGEST_SCALE) & (s >= 2.0**-14)]
+    down = (s * np.float16(-24)).astype(np.float64)  # rounded
+    for c in range(-8, 8):
+        held = ((24.0 + c) * s.astype(np.float64) + down).astype(np.float16).astype(np.float64)  # one rounding, as of a multiply-add
+        assert (np.abs(held - c * s.astype(np.float64)) <= s.astype(np.float64) / 64).all()
